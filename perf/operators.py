@@ -214,9 +214,10 @@ def prepare(case, seed):
         s["plan_buf"] = torch.empty(size, dtype=torch.uint8, device="cuda")
         lora.lora_attn_plan_bind(s["plan"], desc, s["plan_buf"], size, t, n, g)
         lora.lora_attn_build_plan(s["plan"], n, t, s["cu_q"], s["kv_len"], g, s["group_start"], s["prefix_len"],
-                                  max(s["max_kv"], s["max_prefix"]))
+                                  s["max_kv"], s["max_prefix"])
         s["ws_bytes"] = lora.lora_attn_workspace_bytes(s["plan"])
-        s["ws"] = torch.empty(max(1, s["ws_bytes"]), dtype=torch.uint8, device="cuda")
+        s["ws"] = torch.empty(s["ws_bytes"], dtype=torch.uint8, device="cuda")
+        lora.lora_workspace_init(s["ws"], s["ws_bytes"])
     return s
 
 
