@@ -1,0 +1,61 @@
+// Internal definitions of the attention calls: the plan's arrays, the
+// arguments of the kernels, and what they share.
+//
+// A plan cuts a batch into *tiles* (up to 2 x kTileRows rows of one problem,
+// a row being one query token and one of the query heads that share a
+// key/value head) and each tile's keys into ranges of kBlock keys, one *item*
+// per range and key/value head.  A problem is a sequence with its own keys or
+// a group with its prefix.  A tile with one range and no prefix is written
+// where it belongs; every other item leaves a partial result (normalised
+// output and log2 of its softmax sum, fp32), and the join kernel adds the
+// partial results of each token up.
+#pragma once
+
+#include "lora_internal.cuh"
+
+namespace attn {
+
+constexpr int kTileRows = 128;  // rows of one MMA tile; an item has up to two
+constexpr int kBlock = 128;     // keys of a block
+
+// Ranges of keys: enough items for two per SM of a 152-SM device, none of
+// less than kMinBlocks blocks unless its tile has no more.
+constexpr int kTargetItems = 2 * 152;
+constexpr int kMinBlocks = 4;
+
+// One item of a plan (8 words).
+struct Item {
+    int tok0, n_tok;  // its query tokens
+    int prob;         // sequence b, or -1 - g for the prefix of group g
+    int blk0, blk1;   // its blocks of keys
+    int kv_len;       // keys of the problem
+    int lim0;         // keys that its first token sees (causal: + 1 for each token on; may be < 1)
+    int part;         // token row of its partial result, -1: the result goes to the output
+};
+static_assert(sizeof(Item) == 32, "plan items are 8 words");
+
+// counters[] of a plan
+enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3 };
+
+// tokens of an item's first or second row tile, and of an item
+__host__ __device__ inline int tile_tokens(int group) { return kTileRows / group; }
+
+struct Args {
+    const Item *items;
+    const int32_t *counters;
+    int32_t *status;
+    int hq, hkv, G, D, page, causal, T;
+    float scale_log2;  // scale * log2(e)
+    const uint16_t *q, *k, *v;
+    long long ldq, ldk, ldv, n_rows, ldo;
+    const int32_t *table, *ptable;
+    long long ld_table, ld_ptable;
+    uint16_t *out;
+    float *part_o;     // [token row][hq][D]
+    float *part_lse;   // [token row][hq]
+};
+
+}  // namespace attn
+
+// Launch the item kernel (attn.cu).
+lora_status_t lora_attn_launch(const attn::Args &a, int max_items, cudaStream_t s);

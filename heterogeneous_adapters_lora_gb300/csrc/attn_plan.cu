@@ -1,0 +1,562 @@
+// Plans of attention batches, the join of partial results, and the entry
+// points of the attention calls (see attn.cuh for the terms).
+#include <math.h>
+#include <string.h>
+
+#include "attn.cuh"
+
+using attn::Item;
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;  // of the sort of items by length
+
+struct PlanArgs {
+    const int32_t *cu_q, *kv_len, *group_start, *prefix_len;
+    int n_seqs, n_groups, T, max_kv, max_prefix;
+    int tpi;      // tokens of an item
+    int hkv, causal;
+    Item *items;
+    int32_t *tiles, *token_tiles, *first_tile, *counters;
+    int max_tokens;
+};
+
+struct Problem {
+    int tok0, n_tok, len, causal;
+};
+
+// Problems are the groups' prefixes, then the sequences.
+__device__ __forceinline__ Problem problem(const PlanArgs &p, int i) {
+    Problem r;
+    if (i < p.n_groups) {
+        r.tok0 = __ldg(p.cu_q + __ldg(p.group_start + i));
+        r.n_tok = __ldg(p.cu_q + __ldg(p.group_start + i + 1)) - r.tok0;
+        r.len = __ldg(p.prefix_len + i);
+        r.causal = 0;
+    } else {
+        const int b = i - p.n_groups;
+        r.tok0 = __ldg(p.cu_q + b);
+        r.n_tok = __ldg(p.cu_q + b + 1) - r.tok0;
+        r.len = __ldg(p.kv_len + b);
+        r.causal = p.causal;
+    }
+    return r;
+}
+
+// Exclusive sum over the CTA; *total gets the whole sum.  All threads call it.
+__device__ int block_scan(int v, int *total) {
+    __shared__ int warp_sum[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = warp_sum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        warp_sum[lane] = w;
+    }
+    __syncthreads();
+    const int before = warp ? warp_sum[warp - 1] : 0;
+    *total = warp_sum[kPlanThreads / 32 - 1];
+    __syncthreads();
+    return before + x - v;
+}
+
+// Blocks of keys that tile j (tokens from j * tpi on) of a problem has to see.
+__device__ __forceinline__ int tile_blocks(const Problem &q, int j, int tpi) {
+    const int end = min(q.n_tok, (j + 1) * tpi);
+    const long long lim = q.causal ? min((long long)q.len, (long long)q.len - q.n_tok + end) : (long long)q.len;
+    return lim <= 0 ? 0 : (int)((lim + attn::kBlock - 1) / attn::kBlock);
+}
+
+// The problem of a tile: the last one whose first tile is at or before it.
+__device__ __forceinline__ int find_problem(const int32_t *first, int n, int tile) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= tile) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
+    __shared__ int hist[kBuckets];
+    __shared__ unsigned long long total_blocks;
+    __shared__ int bad;
+    const int tid = threadIdx.x;
+    const int n = p.n_groups + p.n_seqs;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) {
+        total_blocks = 0;
+        bad = 0;
+    }
+    for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+    __syncthreads();
+    // the lengths keep to the rules, or the plan is empty
+    for (int b = tid; b < p.n_seqs; b += kPlanThreads) {
+        const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1), len = __ldg(p.kv_len + b);
+        if (c0 < 0 || c1 < c0 || c1 > p.T || (b == 0 && c0 != 0) || (b == p.n_seqs - 1 && c1 != p.T) || len < 0 ||
+            len > p.max_kv)
+            bad = 1;
+    }
+    for (int g = tid; g < p.n_groups; g += kPlanThreads) {
+        const int g0 = __ldg(p.group_start + g), g1 = __ldg(p.group_start + g + 1), len = __ldg(p.prefix_len + g);
+        if (g0 < 0 || g1 < g0 || g1 > p.n_seqs || (g == 0 && g0 != 0) || (g == p.n_groups - 1 && g1 != p.n_seqs) ||
+            len < 0 || len > p.max_prefix)
+            bad = 1;
+    }
+    for (int t = tid; t < p.T; t += kPlanThreads) p.token_tiles[t] = p.token_tiles[p.max_tokens + t] = -1;
+    __syncthreads();
+    if (bad) {
+        if (tid == 0) {
+            p.counters[attn::kItems] = p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = 0;
+            p.counters[attn::kStatus] = LORA_ERR_DEVICE_INDEX;
+        }
+        return;
+    }
+    // first tile of every problem
+    int n_tiles = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int tiles = 0, sum;
+        if (i < n) {
+            const Problem q = problem(p, i);
+            tiles = (q.n_tok + p.tpi - 1) / p.tpi;
+        }
+        const int at = block_scan(tiles, &sum);
+        if (i < n) p.first_tile[i] = n_tiles + at;
+        n_tiles += sum;
+    }
+    __syncthreads();
+    // all blocks, hence the length of a range
+    unsigned long long mine = 0;
+    for (int t = tid; t < n_tiles; t += kPlanThreads) {
+        const int i = find_problem(p.first_tile, n, t);
+        mine += tile_blocks(problem(p, i), t - p.first_tile[i], p.tpi);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((tid & 31) == 0 && mine) atomicAdd(&total_blocks, mine);
+    __syncthreads();
+    const unsigned long long want =
+        (total_blocks * (unsigned long long)p.hkv + attn::kTargetItems - 1) / attn::kTargetItems;
+    const int range = (int)max((unsigned long long)attn::kMinBlocks, want);
+    // items and partial rows of each tile; the histogram of item lengths
+    int n_items = 0, n_part = 0;
+    for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
+        const int t = t0 + tid;
+        int parts = 0, rows = 0, sum, blocks = 0, n_tok = 0, tok0 = 0, i = 0;
+        bool joined = false;
+        if (t < n_tiles) {
+            i = find_problem(p.first_tile, n, t);
+            const Problem q = problem(p, i);
+            const int j = t - p.first_tile[i];
+            blocks = tile_blocks(q, j, p.tpi);
+            tok0 = q.tok0 + j * p.tpi;
+            n_tok = min(p.tpi, q.n_tok - j * p.tpi);
+            int ahead = i < p.n_groups ? 1 : 0;  // this tile's result joins a prefix's
+            if (i >= p.n_groups && p.n_groups) {
+                int lo = 0, hi = p.n_groups - 1;  // the last group that starts at or before the sequence
+                const int b = i - p.n_groups;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (__ldg(p.group_start + mid) <= b) lo = mid; else hi = mid - 1;
+                }
+                ahead = __ldg(p.prefix_len + lo) > 0;
+            }
+            parts = (blocks + range - 1) / range;
+            // no keys: zeros are written, unless a prefix has the tokens' result
+            if (parts == 0 && !ahead) parts = 1;
+            joined = parts > 1 || ahead;
+            if (joined) rows = parts * n_tok;
+        }
+        const int part0 = n_part + block_scan(rows, &sum);
+        n_part += sum;
+        block_scan(parts, &sum);
+        n_items += sum;
+        if (t < n_tiles) {
+            *(int4 *)(p.tiles + 4 * (long long)t) = make_int4(joined ? part0 : -1, parts, tok0, n_tok);
+            if (joined && parts) {
+                int32_t *map = p.token_tiles + (i < p.n_groups ? p.max_tokens : 0);
+                for (int e = 0; e < n_tok; ++e) map[tok0 + e] = t;
+            }
+            for (int s = 0; s < parts; ++s) {
+                const int len = (int)((long long)(s + 1) * blocks / parts) - (int)((long long)s * blocks / parts);
+                atomicAdd(&hist[min(len, kBuckets - 1)], 1);
+            }
+        }
+    }
+    __syncthreads();
+    // where each length starts, the longest first
+    {
+        int sum;
+        const int b = kBuckets - 1 - tid;
+        const int at = block_scan(hist[b], &sum);
+        hist[b] = at;
+    }
+    __syncthreads();
+    for (int t = tid; t < n_tiles; t += kPlanThreads) {
+        const int4 e = *(const int4 *)(p.tiles + 4 * (long long)t);
+        const int i = find_problem(p.first_tile, n, t);
+        const Problem q = problem(p, i);
+        const int j = t - p.first_tile[i], blocks = tile_blocks(q, j, p.tpi);
+        for (int s = 0; s < e.y; ++s) {
+            Item it;
+            it.blk0 = (int)((long long)s * blocks / e.y);
+            it.blk1 = (int)((long long)(s + 1) * blocks / e.y);
+            it.tok0 = e.z;
+            it.n_tok = e.w;
+            it.prob = i < p.n_groups ? -1 - i : i - p.n_groups;
+            it.kv_len = q.len;
+            it.lim0 = q.causal ? q.len - q.n_tok + j * p.tpi + 1 : q.len;
+            it.part = e.x < 0 ? -1 : e.x + s * e.w;
+            const int at = atomicAdd(&hist[min(it.blk1 - it.blk0, kBuckets - 1)], 1);
+            int4 *dst = (int4 *)(p.items + at);
+            dst[0] = make_int4(it.tok0, it.n_tok, it.prob, it.blk0);
+            dst[1] = make_int4(it.blk1, it.kv_len, it.lim0, it.part);
+        }
+    }
+    if (tid == 0) {
+        p.counters[attn::kItems] = n_items;
+        p.counters[attn::kPartTokens] = n_part;
+        p.counters[attn::kTiles] = n_tiles;
+        p.counters[attn::kStatus] = LORA_OK;
+    }
+}
+
+// ---------------------------------------------------------------- join
+
+struct JoinArgs {
+    const int32_t *tiles, *token_tiles, *counters;
+    int max_tokens, T, hq, D;
+    const float *part_o, *part_lse;
+    uint16_t *out;
+    long long ldo;
+};
+
+constexpr int kJoinThreads = 128;
+
+// out[t][h] = sum_s 2^lse_s o_s / sum_s 2^lse_s over the partial results of
+// the token's own tile and of its prefix tile, in that order (so the result
+// does not depend on which item ended first).  One warp per token and head;
+// a lane has four elements of the head.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (__ldg(p.counters + attn::kPartTokens) == 0) return;
+    const int lane = threadIdx.x & 31;
+    const long long n = (long long)p.T * p.hq;
+    const long long step = (long long)gridDim.x * (kJoinThreads / 32);
+    for (long long w = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); w < n; w += step) {
+        const int t = (int)(w / p.hq), h = (int)(w % p.hq);
+        const int tile[2] = {__ldg(p.token_tiles + t), __ldg(p.token_tiles + p.max_tokens + t)};
+        if (tile[0] < 0 && tile[1] < 0) continue;
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (tile[k] < 0) continue;
+            const int4 e = __ldg((const int4 *)(p.tiles + 4 * (long long)tile[k]));
+            for (int s = lane; s < e.y; s += 32)
+                top = fmaxf(top, p.part_lse[(long long)(e.x + s * e.w + t - e.z) * p.hq + h]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top == -INFINITY) top = 0.f;
+        float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (tile[k] < 0) continue;
+            const int4 e = __ldg((const int4 *)(p.tiles + 4 * (long long)tile[k]));
+            for (int s = 0; s < e.y; ++s) {
+                const long long row = (long long)(e.x + s * e.w + t - e.z) * p.hq + h;
+                const float wgt = exp2f(p.part_lse[row] - top);
+                // a part without keys has a weight of zero; a NaN or infinite score makes its weight NaN
+                if (wgt == 0.f) continue;
+                sum += wgt;
+                if (4 * lane < p.D) {
+                    const float4 o = *(const float4 *)(p.part_o + row * p.D + 4 * lane);
+                    acc[0] += wgt * o.x; acc[1] += wgt * o.y; acc[2] += wgt * o.z; acc[3] += wgt * o.w;
+                }
+            }
+        }
+        const float r = sum == 0.f ? 0.f : 1.f / sum;
+        if (4 * lane < p.D) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[0] * r, acc[1] * r);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2] * r, acc[3] * r);
+            *(uint2 *)(p.out + (long long)t * p.ldo + (long long)h * p.D + 4 * lane) =
+                make_uint2(*(const uint32_t *)&x, *(const uint32_t *)&y);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+bool desc_ok(const lora_attn_desc_t &d) {
+    if (d.n_kv_heads < 1 || d.n_q_heads < d.n_kv_heads || d.n_q_heads % d.n_kv_heads || d.n_q_heads > (1 << 20))
+        return false;
+    if (d.n_q_heads / d.n_kv_heads > attn::kTileRows) return false;
+    if (d.head_dim < 8 || d.head_dim > 128 || d.head_dim % 8) return false;
+    if (d.page_size < 0 || d.page_size % 8 || (d.causal != 0 && d.causal != 1)) return false;
+    return isfinite(d.scale) && d.scale > 0.f && isfinite(d.scale * 1.44269504f);
+}
+
+struct Caps {
+    long long tpi, items, tiles, part;
+};
+
+// What a batch of the given size can need.  A tile's ranges beyond its first
+// number at most kTargetItems / n_kv_heads over all tiles (the length of a
+// range is at least all blocks * n_kv_heads / kTargetItems).  A tile of two or
+// more ranges has at most twice that many; with prefixes every token also has
+// one partial result of its own keys and one of its prefix.
+Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long groups) {
+    Caps c;
+    c.tpi = 2 * attn::tile_tokens(d.n_q_heads / d.n_kv_heads);
+    const long long extra = attn::kTargetItems / d.n_kv_heads;
+    c.tiles = (tokens / c.tpi + seqs) + (groups ? tokens / c.tpi + groups : 0);
+    c.items = c.tiles + extra;
+    const long long most = c.tpi < tokens ? c.tpi : tokens;
+    c.part = 2 * extra * most + (groups ? 2 * tokens : 0);
+    return c;
+}
+
+size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
+
+size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
+    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.tiles * 16) + align16((size_t)tokens * 8) +
+           align16((size_t)(seqs + groups) * 4) + 32;
+}
+
+bool caps_ok(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs, int32_t max_groups, Caps *c) {
+    if (!desc || !desc_ok(*desc) || max_tokens < 1 || max_seqs < 1 || max_groups < 0 || max_groups > max_seqs)
+        return false;
+    *c = caps(*desc, max_tokens, max_seqs, max_groups);
+    return c->items * desc->n_kv_heads <= 0x7fffffffLL && c->part <= 0x7fffffffLL && c->tiles <= 0x1fffffffLL;
+}
+
+size_t part_bytes(const lora_attn_plan_t &p) {
+    return align16((size_t)p.max_part * p.desc.n_q_heads * p.desc.head_dim * 4) +
+           align16((size_t)p.max_part * p.desc.n_q_heads * 4);
+}
+
+constexpr size_t kWsHead = 256;  // control words at the start of a workspace
+
+cudaLaunchConfig_t config(int grid, int threads, cudaStream_t s, cudaLaunchAttribute *at) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = s;
+    return cfg;
+}
+
+lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                        const void *v, int64_t ldv, int64_t n_rows, const int32_t *table, int64_t ld_table,
+                        const int32_t *ptable, int64_t ld_ptable, void *out, int64_t ldo, void *workspace,
+                        size_t ws_bytes, bool prefix, void *stream) {
+    if (!plan || !plan->counters || plan->total_q < 0 || plan->n_seqs < 0) return LORA_ERR_INVALID_ARG;
+    if ((plan->n_groups > 0) != prefix) return LORA_ERR_UNSUPPORTED;
+    const lora_attn_desc_t &d = plan->desc;
+    const int64_t qc = (int64_t)d.n_q_heads * d.head_dim, kc = (int64_t)d.n_kv_heads * d.head_dim;
+    if (ldq < qc || ldq % 8 || ldk < kc || ldk % 8 || ldv < kc || ldv % 8 || ldo < qc || ldo % 8 || n_rows < 0 ||
+        n_rows > 0x7fffffffLL)
+        return LORA_ERR_INVALID_ARG;
+    const int64_t page = d.page_size;
+    if (plan->max_kv_len > 0 &&
+        (!table || ((uintptr_t)table & 3) || (page ? ld_table * page < plan->max_kv_len : ld_table < 1)))
+        return LORA_ERR_INVALID_ARG;
+    if (plan->max_prefix_len > 0 &&
+        (!ptable || ((uintptr_t)ptable & 3) || (page ? ld_ptable * page < plan->max_prefix_len : ld_ptable < 1)))
+        return LORA_ERR_INVALID_ARG;
+    if (plan->total_q == 0) return LORA_OK;
+    if (!q || !k || !v || !out || !lora_aligned16(q) || !lora_aligned16(k) || !lora_aligned16(v) ||
+        !lora_aligned16(out))
+        return LORA_ERR_INVALID_ARG;
+    if (!workspace || !lora_aligned16(workspace)) return LORA_ERR_INVALID_ARG;
+    if (ws_bytes < kWsHead + part_bytes(*plan)) return LORA_ERR_CAPACITY;
+    cudaStream_t s = (cudaStream_t)stream;
+    attn::Args a;
+    memset(&a, 0, sizeof(a));
+    a.items = (const Item *)plan->items;
+    a.counters = plan->counters;
+    a.status = plan->counters + attn::kStatus;
+    a.hq = d.n_q_heads;
+    a.hkv = d.n_kv_heads;
+    a.G = d.n_q_heads / d.n_kv_heads;
+    a.D = d.head_dim;
+    a.page = d.page_size;
+    a.causal = d.causal;
+    a.T = plan->total_q;
+    a.scale_log2 = d.scale * 1.44269504088896340736f;
+    a.q = (const uint16_t *)q;
+    a.k = (const uint16_t *)k;
+    a.v = (const uint16_t *)v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.n_rows = n_rows;
+    a.ldo = ldo;
+    a.table = table;
+    a.ptable = ptable;
+    a.ld_table = ld_table;
+    a.ld_ptable = ld_ptable;
+    a.out = (uint16_t *)out;
+    a.part_o = (float *)((char *)workspace + kWsHead);
+    a.part_lse = (float *)((char *)workspace + kWsHead +
+                           align16((size_t)plan->max_part * d.n_q_heads * d.head_dim * 4));
+    const Caps c = caps(d, plan->total_q, plan->n_seqs, plan->n_groups);
+    const lora_status_t st = lora_attn_launch(a, (int)c.items, s);
+    if (st != LORA_OK) return st;
+    // without prefixes, tiles of up to kMinBlocks blocks are never split
+    if (!prefix && plan->max_kv_len <= attn::kMinBlocks * attn::kBlock) return LORA_OK;
+    JoinArgs j;
+    memset(&j, 0, sizeof(j));
+    j.tiles = plan->tiles;
+    j.token_tiles = plan->token_tiles;
+    j.counters = plan->counters;
+    j.max_tokens = plan->max_tokens;
+    j.T = plan->total_q;
+    j.hq = d.n_q_heads;
+    j.D = d.head_dim;
+    j.part_o = a.part_o;
+    j.part_lse = a.part_lse;
+    j.out = a.out;
+    j.ldo = ldo;
+    const long long warps = (long long)plan->total_q * d.n_q_heads;
+    long long grid = (warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+    if (grid > 16 * 152) grid = 16 * 152;
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = config((int)grid, kJoinThreads, s, at);
+    LORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, join_kernel, j));
+    lora_note_launch();
+    return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t lora_attn_plan_bytes(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs,
+                                       int32_t max_groups) {
+    Caps c;
+    if (!caps_ok(desc, max_tokens, max_seqs, max_groups, &c)) return 0;
+    return plan_bytes(c, max_tokens, max_seqs, max_groups);
+}
+
+extern "C" lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_attn_desc_t *desc, void *d_buf,
+                                             size_t bytes, int32_t max_tokens, int32_t max_seqs, int32_t max_groups) {
+    Caps c;
+    if (!plan || !caps_ok(desc, max_tokens, max_seqs, max_groups, &c) || !d_buf || !lora_aligned16(d_buf))
+        return LORA_ERR_INVALID_ARG;
+    if (bytes < plan_bytes(c, max_tokens, max_seqs, max_groups)) return LORA_ERR_CAPACITY;
+    memset(plan, 0, sizeof(*plan));
+    plan->desc = *desc;
+    plan->max_tokens = max_tokens;
+    plan->max_seqs = max_seqs;
+    plan->max_groups = max_groups;
+    plan->max_items = (int32_t)c.items;
+    plan->max_tiles = (int32_t)c.tiles;
+    plan->max_part = (int32_t)c.part;
+    plan->n_seqs = plan->total_q = -1;  // nothing built yet
+    char *at = (char *)d_buf;
+    plan->counters = (int32_t *)at;
+    at += 32;
+    plan->items = (int32_t *)at;
+    at += align16((size_t)c.items * sizeof(Item));
+    plan->tiles = (int32_t *)at;
+    at += align16((size_t)c.tiles * 16);
+    plan->token_tiles = (int32_t *)at;
+    at += align16((size_t)max_tokens * 8);
+    plan->first_tile = (int32_t *)at;
+    return LORA_OK;
+}
+
+extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_seqs, int32_t total_q,
+                                              const int32_t *d_cu_q, const int32_t *d_kv_len, int32_t n_groups,
+                                              const int32_t *d_group_start, const int32_t *d_prefix_len,
+                                              int32_t max_kv_len, int32_t max_prefix_len, void *stream) {
+    if (!plan || !plan->counters || n_seqs < 0 || total_q < 0 || n_groups < 0 || max_kv_len < 0 ||
+        max_prefix_len < 0 || (n_groups > 0 && n_seqs == 0) || (n_seqs == 0 && total_q > 0))
+        return LORA_ERR_INVALID_ARG;
+    if (n_seqs > plan->max_seqs || total_q > plan->max_tokens || n_groups > plan->max_groups) return LORA_ERR_CAPACITY;
+    if (n_seqs > 0 && (!d_cu_q || !d_kv_len || ((uintptr_t)d_cu_q & 3) || ((uintptr_t)d_kv_len & 3)))
+        return LORA_ERR_INVALID_ARG;
+    if (n_groups > 0 && (!d_group_start || !d_prefix_len || ((uintptr_t)d_group_start & 3) ||
+                         ((uintptr_t)d_prefix_len & 3)))
+        return LORA_ERR_INVALID_ARG;
+    PlanArgs p;
+    memset(&p, 0, sizeof(p));
+    p.cu_q = d_cu_q;
+    p.kv_len = d_kv_len;
+    p.group_start = d_group_start;
+    p.prefix_len = d_prefix_len;
+    p.n_seqs = n_seqs;
+    p.n_groups = n_groups;
+    p.T = total_q;
+    p.max_kv = max_kv_len;
+    p.max_prefix = max_prefix_len;
+    p.tpi = 2 * attn::tile_tokens(plan->desc.n_q_heads / plan->desc.n_kv_heads);
+    p.hkv = plan->desc.n_kv_heads;
+    p.causal = plan->desc.causal;
+    p.items = (Item *)plan->items;
+    p.tiles = plan->tiles;
+    p.token_tiles = plan->token_tiles;
+    p.first_tile = plan->first_tile;
+    p.counters = plan->counters;
+    p.max_tokens = plan->max_tokens;
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = config(1, kPlanThreads, (cudaStream_t)stream, at);
+    LORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, plan_kernel, p));
+    lora_note_launch();
+    plan->n_seqs = n_seqs;
+    plan->total_q = total_q;
+    plan->n_groups = n_groups;
+    plan->max_kv_len = max_kv_len;
+    plan->max_prefix_len = n_groups ? max_prefix_len : 0;
+    return LORA_OK;
+}
+
+extern "C" size_t lora_attn_workspace_bytes(const lora_attn_plan_t *plan) {
+    if (!plan || !plan->counters) return 0;
+    return kWsHead + part_bytes(*plan);
+}
+
+extern "C" lora_status_t lora_prompt_attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k,
+                                               int64_t ldk, const void *v, int64_t ldv, int64_t n_rows,
+                                               const int32_t *table, int64_t ld_table, void *out, int64_t ldo,
+                                               void *workspace, size_t ws_bytes, void *stream) {
+    return attention(plan, q, ldq, k, ldk, v, ldv, n_rows, table, ld_table, nullptr, 0, out, ldo, workspace, ws_bytes,
+                     false, stream);
+}
+
+extern "C" lora_status_t lora_prefix_attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k,
+                                               int64_t ldk, const void *v, int64_t ldv, int64_t n_rows,
+                                               const int32_t *table, int64_t ld_table, const int32_t *prefix_table,
+                                               int64_t ld_prefix, void *out, int64_t ldo, void *workspace,
+                                               size_t ws_bytes, void *stream) {
+    return attention(plan, q, ldq, k, ldk, v, ldv, n_rows, table, ld_table, prefix_table, ld_prefix, out, ldo,
+                     workspace, ws_bytes, true, stream);
+}
+
+extern "C" lora_status_t lora_attn_get_status(const lora_attn_plan_t *plan, void *stream) {
+    if (!plan || !plan->counters) return LORA_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    int32_t v = 0;
+    LORA_CUDA_TRY(cudaMemcpyAsync(&v, plan->counters + attn::kStatus, 4, cudaMemcpyDeviceToHost, s));
+    LORA_CUDA_TRY(cudaMemsetAsync(plan->counters + attn::kStatus, 0, 4, s));
+    LORA_CUDA_TRY(cudaStreamSynchronize(s));
+    return (lora_status_t)v;
+}

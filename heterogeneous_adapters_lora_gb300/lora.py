@@ -50,6 +50,23 @@ class Meta(ctypes.Structure):
                 ("ltile_tok0", c_vp), ("stile_row0", c_vp), ("stile_keyn", c_vp), ("counters", c_vp)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("n_q_heads", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32), ("rot_dim", c_i32),
+                ("interleaved", c_i32), ("max_pos", c_i32), ("eps", ctypes.c_float)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("n_q_heads", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32), ("page_size", c_i32),
+                ("causal", c_i32), ("scale", ctypes.c_float)]
+
+
+class AttnPlan(ctypes.Structure):
+    _fields_ = [("desc", AttnDesc), ("max_tokens", c_i32), ("max_seqs", c_i32), ("max_groups", c_i32),
+                ("max_items", c_i32), ("max_tiles", c_i32), ("max_part", c_i32), ("n_seqs", c_i32),
+                ("total_q", c_i32), ("n_groups", c_i32), ("max_kv_len", c_i32), ("max_prefix_len", c_i32),
+                ("items", c_vp), ("tiles", c_vp), ("token_tiles", c_vp), ("first_tile", c_vp), ("counters", c_vp)]
+
+
 class LoraError(RuntimeError):
     def __init__(self, code, where, cuda_error=None):
         self.code = int(code)
@@ -102,6 +119,19 @@ EXPORTS = {
                               c_vp]),
     "lora_sink_experts_act": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp]),
     "lora_status_string": (ctypes.c_char_p, [c_i32]),
+    "lora_qk_norm_rope": (c_i32, [ctypes.POINTER(RopeDesc), c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64,
+                                  c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "lora_attn_plan_bytes": (c_size, [ctypes.POINTER(AttnDesc), c_i32, c_i32, c_i32]),
+    "lora_attn_plan_bind": (c_i32, [ctypes.POINTER(AttnPlan), ctypes.POINTER(AttnDesc), c_vp, c_size, c_i32, c_i32,
+                                    c_i32]),
+    "lora_attn_build_plan": (c_i32, [ctypes.POINTER(AttnPlan), c_i32, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32,
+                                     c_i32, c_vp]),
+    "lora_attn_workspace_bytes": (c_size, [ctypes.POINTER(AttnPlan)]),
+    "lora_prompt_attention": (c_i32, [ctypes.POINTER(AttnPlan), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp,
+                                      c_i64, c_vp, c_i64, c_vp, c_size, c_vp]),
+    "lora_prefix_attention": (c_i32, [ctypes.POINTER(AttnPlan), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp,
+                                      c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_size, c_vp]),
+    "lora_attn_get_status": (c_i32, [ctypes.POINTER(AttnPlan), c_vp]),
 }
 
 
@@ -294,6 +324,54 @@ def lora_sink_experts_act(gate_up, ld_gate_up, gammas, ld_gammas, T, n_experts, 
     _check(lib().lora_sink_experts_act(ptr(gate_up), int(ld_gate_up), ptr(gammas), int(ld_gammas), int(T),
                                        int(n_experts), int(d_mlp), ptr(h), int(ld_h), stream_ptr(stream)),
            "lora_sink_experts_act")
+
+
+def lora_qk_norm_rope(desc: RopeDesc, qkv, ld_qkv, T, q_weight, k_weight, positions, cos_sin, q_out, ld_q, k_out, ld_k,
+                      v_out, ld_v, slots, n_rows, status, stream=None):
+    """Norms of queries and keys per head with the rotation; keys and values to their cache rows."""
+    _check(lib().lora_qk_norm_rope(ctypes.byref(desc), ptr(qkv), ld_qkv, T, ptr(q_weight), ptr(k_weight),
+                                   ptr(positions), ptr(cos_sin), ptr(q_out), ld_q, ptr(k_out), ld_k, ptr(v_out), ld_v,
+                                   ptr(slots), n_rows, ptr(status), stream_ptr(stream)), "lora_qk_norm_rope")
+
+
+def lora_attn_plan_bytes(desc: AttnDesc, max_tokens, max_seqs, max_groups=0) -> int:
+    return int(lib().lora_attn_plan_bytes(ctypes.byref(desc), max_tokens, max_seqs, max_groups))
+
+
+def lora_attn_plan_bind(plan: AttnPlan, desc: AttnDesc, d_buf, nbytes, max_tokens, max_seqs, max_groups=0):
+    _check(lib().lora_attn_plan_bind(ctypes.byref(plan), ctypes.byref(desc), ptr(d_buf), nbytes, max_tokens, max_seqs,
+                                     max_groups), "lora_attn_plan_bind")
+
+
+def lora_attn_build_plan(plan: AttnPlan, n_seqs, total_q, d_cu_q, d_kv_len, n_groups, d_group_start, d_prefix_len,
+                         max_kv_len, max_prefix_len, stream=None):
+    _check(lib().lora_attn_build_plan(ctypes.byref(plan), n_seqs, total_q, ptr(d_cu_q), ptr(d_kv_len), n_groups,
+                                      ptr(d_group_start), ptr(d_prefix_len), max_kv_len, max_prefix_len,
+                                      stream_ptr(stream)), "lora_attn_build_plan")
+
+
+def lora_attn_workspace_bytes(plan: AttnPlan) -> int:
+    return int(lib().lora_attn_workspace_bytes(ctypes.byref(plan)))
+
+
+def lora_prompt_attention(plan: AttnPlan, q, ldq, k, ldk, v, ldv, n_rows, table, ld_table, out, ldo, ws, ws_bytes,
+                          stream=None):
+    """Attention over packed sequences: prompts, chunks behind cached keys, single tokens."""
+    _check(lib().lora_prompt_attention(ctypes.byref(plan), ptr(q), ldq, ptr(k), ldk, ptr(v), ldv, n_rows, ptr(table),
+                                       ld_table, ptr(out), ldo, ptr(ws), ws_bytes, stream_ptr(stream)),
+           "lora_prompt_attention")
+
+
+def lora_prefix_attention(plan: AttnPlan, q, ldq, k, ldk, v, ldv, n_rows, table, ld_table, prefix_table, ld_prefix, out,
+                          ldo, ws, ws_bytes, stream=None):
+    """lora_prompt_attention for groups of sequences that share prefixes."""
+    _check(lib().lora_prefix_attention(ctypes.byref(plan), ptr(q), ldq, ptr(k), ldk, ptr(v), ldv, n_rows, ptr(table),
+                                       ld_table, ptr(prefix_table), ld_prefix, ptr(out), ldo, ptr(ws), ws_bytes,
+                                       stream_ptr(stream)), "lora_prefix_attention")
+
+
+def lora_attn_get_status(plan: AttnPlan, stream=None) -> int:
+    return int(lib().lora_attn_get_status(ctypes.byref(plan), stream_ptr(stream)))
 
 
 def lora_kernel_launch_count() -> int:

@@ -428,6 +428,153 @@ LORA_API lora_status_t lora_sink_experts_act(const void *gate_up, int64_t ld_gat
                                              int64_t ld_gammas, int32_t T, int32_t n_experts, int32_t d_mlp,
                                              void *h, int64_t ld_h, void *stream);
 
+/* ------------------------------------------- attention between LoRA layers
+ *
+ * What a serving step does between the LoRA QKV layer and the LoRA output
+ * layer: norms and rotation of queries and keys with the keys and values put
+ * into their cache rows, then attention over packed sequences.  Tensors are
+ * bf16 as everywhere; sums, softmax statistics and accumulators are fp32. */
+
+/* Heads of one attention layer as lora_qk_norm_rope takes them.  A packed row
+ * holds n_q_heads query heads, n_kv_heads key heads and n_kv_heads value
+ * heads of head_dim elements (the slices of a LoRA QKV layer). */
+typedef struct {
+    int32_t n_q_heads, n_kv_heads;  /* >= 1 */
+    int32_t head_dim;               /* multiple of 8, 8..256 */
+    int32_t rot_dim;                /* leading elements of a head that are rotated: multiple of 8, 0..head_dim */
+    int32_t interleaved;            /* rotated pairs: 0 = (i, i + rot_dim/2), 1 = (2i, 2i + 1) */
+    int32_t max_pos;                /* rows of the cosine/sine table (ignored when rot_dim is 0) */
+    float eps;                      /* >= 0 */
+} lora_rope_desc_t;
+
+/* Norm of every query and key head and its rotation, in one pass over the
+ * packed QKV rows ([T][ld_qkv] bf16):
+ *   n = x * rsqrt(mean_i(x_i^2) + eps) * weight        per head, fp32
+ *   (a, b) -> (a cos_m - b sin_m, b cos_m + a sin_m)   pair m < rot_dim / 2
+ * with weight = q_weight or k_weight ([head_dim] bf16, NULL = ones) and the
+ * cosines and sines of row positions[t] of cos_sin ([max_pos][rot_dim] fp32:
+ * rot_dim/2 cosines, then rot_dim/2 sines; it may hold any scaling).  Results
+ * are rounded to bf16 once.  Queries go to q_out [T][ld_q]; keys, and values
+ * unchanged, to row slots[t] of k_out [n_rows][ld_k] and v_out [n_rows][ld_v]
+ * (the rows of a paged cache: page * page_size + place), or to row t when
+ * slots is NULL.  v_out may be NULL (values stay where they are).  A slot of
+ * -1 stores no key and value.  A token whose position is outside [0, max_pos)
+ * or whose slot is outside [-1, n_rows) writes nothing and sets *status (an
+ * int32 device word, may be NULL) to LORA_ERR_DEVICE_INDEX.  In place is
+ * allowed (q_out = qkv with ld_q = ld_qkv, k_out = its key columns with
+ * ld_k = ld_qkv, v_out NULL); other overlaps of input and outputs are not,
+ * nor two tokens with one slot.
+ * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, a field or a
+ * leading dimension out of range, n_rows < T without slots). */
+LORA_API lora_status_t lora_qk_norm_rope(const lora_rope_desc_t *desc, const void *qkv, int64_t ld_qkv, int32_t T,
+                                         const void *q_weight, const void *k_weight, const int32_t *positions,
+                                         const float *cos_sin, void *q_out, int64_t ld_q, void *k_out, int64_t ld_k,
+                                         void *v_out, int64_t ld_v, const int32_t *slots, int64_t n_rows,
+                                         int32_t *status, void *stream);
+
+/* Heads and cache layout of an attention layer.  Query head h reads key/value
+ * head h / (n_q_heads / n_kv_heads). */
+typedef struct {
+    int32_t n_q_heads;   /* a multiple of n_kv_heads, at most 128 per key/value head */
+    int32_t n_kv_heads;  /* >= 1 */
+    int32_t head_dim;    /* multiple of 8, 8..128 */
+    int32_t page_size;   /* 0: a sequence's key rows follow each other; else rows of a page, a multiple of 8 */
+    int32_t causal;      /* 1: query i of n sees the keys up to len - n + i of its sequence; 0: all of them */
+    float scale;         /* factor of the scores, finite and > 0 */
+} lora_attn_desc_t;
+
+/* The work of one batch, laid out from its lengths alone: built once per step
+ * and used by every layer of the step whose heads and page size are the
+ * same.  Caller-owned device memory, bound with lora_attn_plan_bind.
+ *   items[max_items][8]  tiles of queries x ranges of keys, the longest first
+ *   tiles[max_tiles][4]  tiles of queries and where their partial results lie
+ *   token_tiles[2][max_tokens]  each token's own tile and prefix tile (-1: none
+ *                        that has to be joined)
+ *   counters[8]          items, partial token rows, tiles, (3) status word
+ * The host fields n_seqs .. max_prefix_len record the last build. */
+typedef struct {
+    lora_attn_desc_t desc;
+    int32_t max_tokens, max_seqs, max_groups, max_items, max_tiles, max_part;
+    int32_t n_seqs, total_q, n_groups, max_kv_len, max_prefix_len;
+    int32_t *items;
+    int32_t *tiles;
+    int32_t *token_tiles;
+    int32_t *first_tile;
+    int32_t *counters;
+} lora_attn_plan_t;
+
+/* Device bytes lora_attn_plan_bind needs (0 if the descriptor or a capacity
+ * is out of range).  Host only. */
+LORA_API size_t lora_attn_plan_bytes(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs,
+                                     int32_t max_groups);
+
+/* Carve `d_buf` (device, 16-byte aligned, >= lora_attn_plan_bytes) into the
+ * plan's arrays.  Host only; errors: LORA_ERR_INVALID_ARG, LORA_ERR_CAPACITY. */
+LORA_API lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_attn_desc_t *desc, void *d_buf,
+                                           size_t bytes, int32_t max_tokens, int32_t max_seqs, int32_t max_groups);
+
+/* Lay out a batch on the device (one kernel, no host synchronisation,
+ * graph-capturable).  d_cu_q: [n_seqs + 1] int32, first query of each sequence
+ * in the packed queries, cu_q[0] = 0, cu_q[n_seqs] = total_q; a sequence may
+ * have no queries.  d_kv_len: [n_seqs] int32, keys of each sequence that are
+ * its own, 0..max_kv_len.  With n_groups > 0 (lora_prefix_attention): group g
+ * is the sequences group_start[g] .. group_start[g+1] - 1
+ * (d_group_start [n_groups + 1] int32, from 0 to n_seqs), which share
+ * prefix_len[g] keys (d_prefix_len [n_groups] int32, 0..max_prefix_len) ahead
+ * of their own.  Lengths that break these rules make an empty plan (calls with
+ * it write nothing) and set the plan's status to LORA_ERR_DEVICE_INDEX.
+ * Errors: LORA_ERR_INVALID_ARG, LORA_ERR_CAPACITY. */
+LORA_API lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_seqs, int32_t total_q,
+                                            const int32_t *d_cu_q, const int32_t *d_kv_len, int32_t n_groups,
+                                            const int32_t *d_group_start, const int32_t *d_prefix_len,
+                                            int32_t max_kv_len, int32_t max_prefix_len, void *stream);
+
+/* Workspace bytes of the attention calls for any batch the bound plan can
+ * hold.  The workspace must be zero before its first use
+ * (lora_workspace_init); calls that share one must not overlap on the device. */
+LORA_API size_t lora_attn_workspace_bytes(const lora_attn_plan_t *plan);
+
+/* Attention over packed sequences (whole prompts, chunks of prompts behind
+ * cached keys, single tokens), for every sequence, query token i and head h:
+ *   out[i][h] = sum_j p_j v_j,   p = softmax_j(scale * q[i][h] . k_j)
+ * over the keys that the token sees (see lora_attn_desc_t.causal); a token
+ * that sees no key gets zeros.  q: [total_q][ldq], out: [total_q][ldo]
+ * (n_q_heads * head_dim columns); k, v: [n_rows][ldk / ldv] (n_kv_heads *
+ * head_dim columns).  Key j of sequence b is row table[b][0] + j
+ * (page_size 0), or row table[b][j / page_size] * page_size + j % page_size;
+ * table is int32 device with ld_table entries per sequence.  Keys that no
+ * query of a sequence sees do not touch its results, whatever their rows
+ * hold.  Rows that a table puts outside [0, n_rows) count as zero rows and set
+ * the plan's status to LORA_ERR_DEVICE_INDEX.  Scores and sums are fp32; the
+ * probabilities are rounded to bf16 for their product with v.
+ * The result does not change from run to run.
+ * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, leading dimension
+ * too small or not a multiple of 8, a table too narrow for max_kv_len, no
+ * built plan), LORA_ERR_CAPACITY (workspace), LORA_ERR_UNSUPPORTED (a plan
+ * with groups). */
+LORA_API lora_status_t lora_prompt_attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k,
+                                             int64_t ldk, const void *v, int64_t ldv, int64_t n_rows,
+                                             const int32_t *table, int64_t ld_table, void *out, int64_t ldo,
+                                             void *workspace, size_t ws_bytes, void *stream);
+
+/* lora_prompt_attention for a batch whose sequences share prefixes in groups
+ * (requests of one adapter behind its common instruction): every query of
+ * group g also sees the prefix_len[g] keys that prefix_table (int32 device,
+ * ld_prefix entries per group, same cache and page size) leads to.  A
+ * prefix's keys and values are read once for all the queries of a tile of
+ * its group, and the parts are joined by their softmax statistics.
+ * Errors: as lora_prompt_attention; LORA_ERR_UNSUPPORTED for a plan without
+ * groups. */
+LORA_API lora_status_t lora_prefix_attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k,
+                                             int64_t ldk, const void *v, int64_t ldv, int64_t n_rows,
+                                             const int32_t *table, int64_t ld_table, const int32_t *prefix_table,
+                                             int64_t ld_prefix, void *out, int64_t ldo, void *workspace,
+                                             size_t ws_bytes, void *stream);
+
+/* Synchronise `stream`, return the plan's status word (LORA_OK,
+ * LORA_ERR_DEVICE_INDEX or LORA_ERR_TIMEOUT) and clear it. */
+LORA_API lora_status_t lora_attn_get_status(const lora_attn_plan_t *plan, void *stream);
+
 /* Kernel selection for lora_apply_slices / lora_moe_apply (process-wide):
  * 0 = automatic (tcgen05 for long contiguous runs of a rank-64 dense pool;
  *     the fused decode kernel -- one thread-block cluster per adapter slot,
