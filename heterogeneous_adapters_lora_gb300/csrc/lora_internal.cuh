@@ -163,6 +163,12 @@ bool lora_make_tmap_2d(CUtensorMap *m, const void *base, long long cols, long lo
 bool lora_make_tmap_b3d(CUtensorMap *m, const void *base, int rs, int rows, int slots, long long slot_elems);
 // The same view with boxes of 8 ranks x 128 rows and no swizzle.
 bool lora_make_tmap_bk(CUtensorMap *m, const void *base, int rs, long long rows, int slots, long long slot_elems);
+// 3D bf16 map over rows of `heads` heads of head_dim elements (row stride in
+// elements), box {64, box_heads, box_rows} in the 128-byte swizzle: the rows of
+// a box are (row, head) pairs, heads innermost; elements past head_dim read as
+// zero (sgmv.cu).
+bool lora_make_tmap_heads(CUtensorMap *m, const void *base, int head_dim, int heads, long long rows, long long stride,
+                          int box_heads, int box_rows);
 bool lora_make_tmap_a_chunks(CUtensorMap *m, const void *base, long long rows, long long cols, int box_rows,
                              int box_chunks);
 

@@ -454,6 +454,19 @@ bool lora_make_tmap_a_chunks(CUtensorMap *m, const void *base, long long rows, l
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool lora_make_tmap_heads(CUtensorMap *m, const void *base, int head_dim, int heads, long long rows, long long stride,
+                          int box_heads, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 f = encode_fn();
+    if (!f) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t es[3] = {1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool lora_sgmv_eligible(const lora_pool_t *pool) {
     const lora_pool_desc_t &d = pool->desc;
     if (pool->is_moe || !pool->d_bmaps || d.max_rank > 64) return false;
