@@ -126,6 +126,41 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *(const uint32_t *)&v;
 }
 
+// One lane of a converged warp, as the hardware picks it: the compiler then
+// knows that what follows runs in one lane, and keeps the operands of the
+// products in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
+// The products with the upper halves of the descriptors as immediates: only
+// start addresses change from one to the next.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // see tc::desc_sw128
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHi)
+        : "memory");
+}
+
 template <int NCH>
 __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant__ KArgs p) {
     using Sh = Shape<NCH>;
@@ -262,14 +297,17 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             int use = 0;               // stages used so far
             int nq[2] = {0, 0}, np[2] = {0, 0};
             bool ok = true;
+            // lower halves of the descriptors (shared addresses end below 2^18): of K-major
+            // tiles, and of V, whose 64-element chunks are kChunkBytes apart
+            const uint32_t q_lo = (tc::smem_u32(sq) >> 4) | (1u << 16), k_lo = (tc::smem_u32(ring) >> 4) | (1u << 16);
+            const uint32_t v_lo = (tc::smem_u32(ring) >> 4) | ((uint32_t)(kChunkBytes >> 4) << 16);
             auto qk = [&](int s, int st) {
-                if (lane == 0) {
-                    const uint32_t qa = tc::smem_u32(sq) + s * Sh::kStage;
-                    const uint32_t ka = tc::smem_u32(ring) + st * Sh::kStage;
+                if (elect_one()) {
+                    const uint32_t qa = q_lo + s * (Sh::kStage >> 4), ka = k_lo + st * (Sh::kStage >> 4);
 #pragma unroll
                     for (int i = 0; i < NCH * 4; ++i) {
-                        const uint32_t off = (uint32_t)((i >> 2) * kChunkBytes + (i & 3) * 32);
-                        tc::mma_bf16(tmem + s * 128, tc::desc_sw128(qa + off), tc::desc_sw128(ka + off), id_qk, i != 0);
+                        const uint32_t off = (uint32_t)((i >> 2) * kChunkBytes + (i & 3) * 32) >> 4;
+                        mma_ss(tmem + s * 128, qa + off, ka + off, id_qk, i != 0);
                     }
                     tc::mma_commit(&bars->s_full[s]);
                 }
@@ -320,12 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                         ++np[s];
                         if (!ok) continue;
                         tc::tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t va = tc::smem_u32(ring) + sv * Sh::kStage;
+                        if (elect_one()) {
+                            const uint32_t va = v_lo + sv * (Sh::kStage >> 4);
 #pragma unroll
                             for (int i = 0; i < attn::kBlock / 16; ++i)
-                                tc::mma_bf16_ts(tmem + 256 + s * Sh::kDP, tmem + s * 128 + i * 8,
-                                                tc::desc_sw128_mn(va + i * 2048, kChunkBytes), id_pv, (j | i) != 0);
+                                mma_ts(tmem + 256 + s * Sh::kDP, tmem + s * 128 + i * 8, va + i * (2048 >> 4), id_pv,
+                                       i ? true : j != 0);
                             if (j + 1 == k.nb[s]) tc::mma_commit(&bars->o_full[s]);
                         }
                         __syncwarp();
