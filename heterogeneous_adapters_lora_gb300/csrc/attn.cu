@@ -56,30 +56,30 @@ struct Shape {
 
 struct Bars {
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], fin;
+    uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], fin;
+    uint64_t p_full[2][2];  // of each slot: the first and the second 64 keys of P
     uint32_t tmem;
     int abort;
 };
 
-// Bounded wait of a whole warp; false (for all lanes) when it gave up here
-// or somewhere else in the CTA.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status,
-                                          int limit = kMaxPolls) {
-    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
-    int polls = 0;
-    while (!__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) {
-        ++polls;
-        if ((polls & 1023) == 0 && __any_sync(0xffffffffu, *(volatile int *)&b->abort)) return false;
-        if (polls > limit) {
-            if ((threadIdx.x & 31) == 0) {
-                *(volatile int *)&b->abort = 1;
-                atomicExch(status, (int)LORA_ERR_TIMEOUT);
-            }
-            __syncwarp();
+// Bounded wait; false when it gave up here or somewhere else in the CTA.
+// The lanes of a warp may differ: callers vote before they leave a loop.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    for (int polls = 0; !tc::mbar_try_wait(bar, parity); ++polls) {
+        if ((polls & 1023) == 0 && *(volatile int *)&b->abort) return false;
+        if (polls > kMaxPolls) {
+            *(volatile int *)&b->abort = 1;
+            atomicExch(status, (int)LORA_ERR_TIMEOUT);
             return false;
         }
     }
     return true;
+}
+__device__ __forceinline__ bool all(bool ok) { return __all_sync(0xffffffffu, ok); }
+// ... of a whole warp, with the vote.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status) {
+    return all(wait(bar, parity, b, status));
 }
 
 // What the roles of a CTA all derive from an item.
@@ -121,6 +121,33 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 at a time.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 two(float lo, float hi) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 apart(f32x2 v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *(const uint32_t *)&v;
@@ -131,6 +158,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // products in uniform registers.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "elect.sync _|p, 0xffffffff;\n\t"
@@ -182,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             tc::mbar_init(&bars->q_full[i], 1);
             tc::mbar_init(&bars->q_empty[i], 1);
             tc::mbar_init(&bars->s_full[i], 1);
-            tc::mbar_init(&bars->p_full[i], 4);
+            tc::mbar_init(&bars->p_full[i][0], 4);
+            tc::mbar_init(&bars->p_full[i][1], 4);
             tc::mbar_init(&bars->o_full[i], 1);
         }
         tc::mbar_init(&bars->fin, 1);
@@ -294,24 +323,35 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
         } else if (warp == 9) {
             // ---- MMA issue
             constexpr uint32_t id_qk = tc::idesc_bf16(128, 128), id_pv = tc::idesc_bf16_bmn(128, Sh::kDP);
-            int use = 0;               // stages used so far
-            int nq[2] = {0, 0}, np[2] = {0, 0};
+            int st = 0;                // the next stage of the ring and its parity
+            uint32_t par = 0;
+            auto next = [&]() {
+                if (++st == kNS) {
+                    st = 0;
+                    par ^= 1u;
+                }
+            };
+            uint32_t pq[2] = {0, 0}, pp[2] = {0, 0};
             bool ok = true;
             // lower halves of the descriptors (shared addresses end below 2^18): of K-major
             // tiles, and of V, whose 64-element chunks are kChunkBytes apart
             const uint32_t q_lo = (tc::smem_u32(sq) >> 4) | (1u << 16), k_lo = (tc::smem_u32(ring) >> 4) | (1u << 16);
             const uint32_t v_lo = (tc::smem_u32(ring) >> 4) | ((uint32_t)(kChunkBytes >> 4) << 16);
-            auto qk = [&](int s, int st) {
-                if (elect_one()) {
-                    const uint32_t qa = q_lo + s * (Sh::kStage >> 4), ka = k_lo + st * (Sh::kStage >> 4);
+            auto qk = [&](int s, int stage) {  // by one lane
+                const uint32_t qa = q_lo + s * (Sh::kStage >> 4), ka = k_lo + stage * (Sh::kStage >> 4);
 #pragma unroll
-                    for (int i = 0; i < NCH * 4; ++i) {
-                        const uint32_t off = (uint32_t)((i >> 2) * kChunkBytes + (i & 3) * 32) >> 4;
-                        mma_ss(tmem + s * 128, qa + off, ka + off, id_qk, i != 0);
-                    }
-                    tc::mma_commit(&bars->s_full[s]);
+                for (int i = 0; i < NCH * 4; ++i) {
+                    const uint32_t off = (uint32_t)((i >> 2) * kChunkBytes + (i & 3) * 32) >> 4;
+                    mma_ss(tmem + s * 128, qa + off, ka + off, id_qk, i != 0);
                 }
-                __syncwarp();
+                tc::mma_commit(&bars->s_full[s]);
+            };
+            auto pv = [&](int s, int h, int stage, bool first) {
+                const uint32_t va = v_lo + stage * (Sh::kStage >> 4) + h * (8192 >> 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_ts(tmem + 256 + s * Sh::kDP, tmem + s * 128 + h * 32 + i * 8, va + i * (2048 >> 4), id_pv,
+                           h || i ? true : !first);
             };
             for (int r = 0; ok; ++r) {
                 const int w = work_index(r);
@@ -320,65 +360,67 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const Work k = work_of(p, w);
                 if (!k.n) continue;
                 // the first block's S
-                int st = use % kNS;
-                if (!(ok = warp_wait(&bars->kv_full[st], (uint32_t)((use / kNS) & 1), bars, status))) break;
+                ok &= wait(&bars->kv_full[st], par, bars, status);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    if (!k.nb[s] || !ok) continue;
-                    ok = warp_wait(&bars->q_full[s], (uint32_t)(nq[s] & 1), bars, status);
-                    ++nq[s];
-                    if (!ok) continue;
+                    if (!k.nb[s]) continue;
+                    ok &= wait(&bars->q_full[s], pq[s], bars, status);
+                    pq[s] ^= 1u;
                     tc::tc_fence_after();
-                    qk(s, st);
-                    if (k.nb[s] == 1 && lane == 0) tc::mma_commit(&bars->q_empty[s]);
+                    if (elect_one()) {
+                        qk(s, st);
+                        if (k.nb[s] == 1) tc::mma_commit(&bars->q_empty[s]);
+                    }
                 }
-                if (!ok) break;
-                if (lane == 0) tc::mma_commit(&bars->kv_empty[st]);
-                ++use;
-                for (int j = 0; j < k.n && ok; ++j) {
-                    const int sv = use % kNS, sk = (use + 1) % kNS;
+                if (elect_one()) tc::mma_commit(&bars->kv_empty[st]);
+                next();
+                const int full = (k.it.kv_len >> 7) - k.it.blk0;  // blocks whose keys all count
+                for (int j = 0; j < k.n; ++j) {
                     const bool more = j + 1 < k.n;
-                    if (!(ok = warp_wait(&bars->kv_full[sv], (uint32_t)((use / kNS) & 1), bars, status))) break;
+                    const int sv = st;
+                    ok &= wait(&bars->kv_full[st], par, bars, status);
+                    next();
+                    const int sk = st;
+                    if (more) {
+                        ok &= wait(&bars->kv_full[st], par, bars, status);
+                        next();
+                    }
                     // values of a block's keys past the end count for nothing, whatever their rows hold
-                    const int left = k.it.kv_len - (k.it.blk0 + j) * attn::kBlock;
-                    if (left < attn::kBlock) {
+                    if (j >= full) {
                         char *v = ring + sv * Sh::kStage;
-                        for (int i = left * 8 + lane; i < attn::kBlock * 8; i += 32)
+                        for (int i = (k.it.kv_len & 127) * 8 + lane; i < attn::kBlock * 8; i += 32)
 #pragma unroll
                             for (int c = 0; c < NCH; ++c) *(uint4 *)(v + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
                         tc::fence_proxy_async();
                         __syncwarp();
                     }
-                    if (more && !(ok = warp_wait(&bars->kv_full[sk], (uint32_t)(((use + 1) / kNS) & 1), bars, status)))
-                        break;
+                    if (!(ok = all(ok))) break;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        if (j >= k.nb[s] || !ok) continue;
-                        ok = warp_wait(&bars->p_full[s], (uint32_t)(np[s] & 1), bars, status);
-                        ++np[s];
-                        if (!ok) continue;
+                        if (j >= k.nb[s]) continue;
+                        ok &= wait(&bars->p_full[s][0], pp[s], bars, status);
+                        tc::tc_fence_after();
+                        if (elect_one()) pv(s, 0, sv, j == 0);
+                        ok &= wait(&bars->p_full[s][1], pp[s], bars, status);
+                        pp[s] ^= 1u;
                         tc::tc_fence_after();
                         if (elect_one()) {
-                            const uint32_t va = v_lo + sv * (Sh::kStage >> 4);
-#pragma unroll
-                            for (int i = 0; i < attn::kBlock / 16; ++i)
-                                mma_ts(tmem + 256 + s * Sh::kDP, tmem + s * 128 + i * 8, va + i * (2048 >> 4), id_pv,
-                                       i ? true : j != 0);
-                            if (j + 1 == k.nb[s]) tc::mma_commit(&bars->o_full[s]);
-                        }
-                        __syncwarp();
-                        if (j + 1 < k.nb[s]) {
-                            qk(s, sk);
-                            if (j + 2 == k.nb[s] && lane == 0) tc::mma_commit(&bars->q_empty[s]);
+                            pv(s, 1, sv, false);
+                            if (j + 1 < k.nb[s]) {
+                                qk(s, sk);
+                                if (j + 2 == k.nb[s]) tc::mma_commit(&bars->q_empty[s]);
+                            } else {
+                                tc::mma_commit(&bars->o_full[s]);
+                            }
+                            if (s == 1 || j >= k.nb[1]) {  // the last of the slots: the stages are free
+                                tc::mma_commit(&bars->kv_empty[sv]);
+                                if (more) tc::mma_commit(&bars->kv_empty[sk]);
+                            }
                         }
                     }
-                    if (!ok) break;
-                    if (lane == 0) {
-                        tc::mma_commit(&bars->kv_empty[sv]);
-                        if (more) tc::mma_commit(&bars->kv_empty[sk]);
-                    }
-                    use += more ? 2 : 1;
+                    __syncwarp();
                 }
+                ok = all(ok);
             }
             // all products are done before tensor memory is given back
             if (lane == 0) tc::mma_commit(&bars->fin);
@@ -405,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             const bool live = e < nt, warp_live = __any_sync(0xffffffffu, live);
             // keys that the row sees; a row that is not there masks nothing
             const int lim = live ? min(k.it.kv_len, k.it.lim0 + k.step * (s * p.tpt + e)) : 0x7fffffff;
-            float m = -INFINITY, l = 0.f;
+            const int min_lim = __reduce_min_sync(0xffffffffu, lim);
+            float m = -INFINITY, l = 0.f, base = 0.f;
+            bool huge = false;
             for (int j = 0; j < nb; ++j) {
                 if (!(ok = warp_wait(&bars->s_full[s], (uint32_t)(ns & 1), bars, status))) break;
                 ++ns;
@@ -415,30 +459,35 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + c * 32, x[c]);
                     tc::tmem_wait_ld();
-                    const int rel = lim - (k.it.blk0 + j) * attn::kBlock;
-                    if (__any_sync(0xffffffffu, rel < attn::kBlock)) {
+                    const int key0 = (k.it.blk0 + j) * attn::kBlock;
+                    if (key0 + attn::kBlock > min_lim) {
+                        const int rel = lim - key0;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (c * 32 + i >= rel) x[c][i] = 0xff800000u;
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float mx[4];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
+                    for (int c = 0; c < 4; ++c) {
+                        mx[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][i]));
-                    const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (j == 0) {
-                        m = bm;
-                    } else if (__any_sync(0xffffffffu, live && (bm - m) * p.a.scale_log2 > kLag)) {
-                        // the weights so far are rescaled to the new maximum
+                        for (int i = 3; i < 31; i += 2)
+                            mx[c] = max3(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                        mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
+                    }
+                    const float bm = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    // the maximum in use stays while no row is more than kLag above it
+                    if (__any_sync(0xffffffffu, live && !((bm - m) * p.a.scale_log2 <= kLag))) {
                         const float mn = fmaxf(m, bm);
                         const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * p.a.scale_log2);
                         m = mn;
                         l *= f;
+                        base = m == -INFINITY ? 0.f : m * p.a.scale_log2;
+                        huge = __any_sync(0xffffffffu, live && !(fabsf(base) <= kExactBase));
 #pragma unroll 1
-                        for (int c = 0; c < Sh::kDP / 32; ++c) {
+                        for (int c = 0; j && c < Sh::kDP / 32; ++c) {  // the output so far, with the weights
                             uint32_t o[32], o0[16], o1[16];
                             tc::tmem_ld32(to + c * 32, o);
                             tc::tmem_wait_ld();
@@ -453,37 +502,49 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     }
                     // 2^(x * scale - base): whatever base was rounded to divides out, unless
                     // it is so large that its rounding is
-                    float scale = p.a.scale_log2, base = m == -INFINITY ? 0.f : m * scale;
-                    if (__any_sync(0xffffffffu, live && !(fabsf(base) <= kExactBase))) {
+                    float sc = p.a.scale_log2, sb = -base;
+                    if (huge) {
                         const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                x[c][i] = __float_as_uint((__uint_as_float(x[c][i]) - mm) * scale);
-                        scale = 1.f;
-                        base = 0.f;
+                                x[c][i] = __float_as_uint((__uint_as_float(x[c][i]) - mm) * sc);
+                        sc = 1.f;
+                        sb = 0.f;
                     }
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const f32x2 sc2 = two(sc, sc), sb2 = two(sb, sb);
+                    f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float a = ex2(fmaf(__uint_as_float(x[c][2 * i]), scale, -base));
-                            const float b = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), scale, -base));
-                            sum[(2 * i) & 3] += a;
-                            sum[(2 * i + 1) & 3] += b;
-                            pk[i] = pack2(a, b);
+                            float2 v = apart(fma2(two(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])),
+                                                  sc2, sb2));
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            sum[i & 1] = add2(sum[i & 1], two(v.x, v.y));
+                            pk[i] = pack2(v.x, v.y);
                         }
                         tc::tmem_st16(ts + c * 16, pk);
+                        if (c == 1) {  // the first half of P (and the rescaled output) is there
+                            tc::tmem_wait_st();
+                            tc::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(&bars->p_full[s][0]);
+                        }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 sm = apart(add2(sum[0], sum[1]));
+                    l += sm.x + sm.y;
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars->p_full[s]);
+                if (lane == 0) {
+                    if (!warp_live) tc::mbar_arrive(&bars->p_full[s][0]);
+                    tc::mbar_arrive(&bars->p_full[s][1]);
+                }
             }
             if (!ok) break;
             if (nb) {
