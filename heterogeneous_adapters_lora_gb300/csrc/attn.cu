@@ -5,23 +5,24 @@
 //
 // A row of an MMA tile is (token, query head of the group), so the heads that
 // share a key/value head share its keys in one product, and a decode token
-// fills group-many rows instead of one.  An item has two tiles (*slots*) that
-// run over the same blocks of 128 keys: while one slot's softmax is computed
-// by its four warps, the tensor cores do the other slot's products.
+// fills group-many rows instead of one.  A CTA works on two tiles (*slots*) at
+// a time: while one slot's softmax is computed by its four warps, the tensor
+// cores do the other slot's products.  The slots are the two tiles of one
+// item, over the same stream of K/V blocks, or two one-tile items with a
+// stream each.
 //
-// Warp roles (384 threads, one CTA per SM, each CTA takes items in turn):
+// Warp roles (384 threads, one CTA per SM, each CTA takes units in turn):
 //   warps 0-3, 4-7  softmax of slot 0 / 1, one row per thread, and its epilogue
 //   warp 8          TMA of K and V blocks into a ring of stages
-//   warp 9          MMA issue
-//   warp 10         TMA of the Q tiles
-//   warp 11         TMEM allocation
+//   warps 9, 11     MMA issue of slot 0 / 1
+//   warp 10         TMEM allocation, TMA of the Q tiles
 // Tensor memory (512 columns): S of slot 0, 1 (128 columns each, P as bf16 in
 // the first half of its S), O of slot 0, 1.
 //
 // Orders that no barrier of its own is needed for: a slot's QK of block j + 1
 // is issued after its PV of block j, so "S is there" also says that O holds
-// block j; a slot's PV of an item's first block waits for P, which the same
-// warps write after they have read the item before's O.
+// block j; a slot's PV of a unit's first block waits for P, which the same
+// warps write after they have read the unit before's O.
 #include <math.h>
 #include <string.h>
 
@@ -56,7 +57,8 @@ struct Shape {
 
 struct Bars {
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], fin;
+    uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], fin[2];
+    uint64_t turn[2];       // a slot's turn to issue, when the slots share a stream
     uint64_t p_full[2][2];  // of each slot: the first and the second 64 keys of P
     uint32_t tmem;
     int abort;
@@ -82,35 +84,63 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *
     return all(wait(bar, parity, b, status));
 }
 
-// What the roles of a CTA all derive from an item.
+// A slot's part of a unit, as all roles derive it.
+struct Slot {
+    int tok0, nt;       // its tokens
+    int prob, kv_len;   // whose keys, and how many
+    int blk0, nb;       // its blocks
+    int lim0, step;     // keys that its first token sees, and that each further one sees more
+    int part;           // token row of its partial result, or -1
+};
 struct Work {
-    attn::Item it;
+    Slot s[2];
+    bool shared;  // both slots run over slot 0's stream (of n blocks)
+    int n;        // blocks of the longer slot
     int kvh;
-    int step;     // keys that each further token sees more
-    int nt[2];    // tokens of the slots
-    int nb[2];    // blocks of the slots
-    int n;        // blocks of the item
 };
 
-__device__ __forceinline__ Work work_of(const KArgs &p, int w) {
+__device__ __forceinline__ Slot slot_of(const KArgs &p, const attn::Item *at) {
+    const int4 x = __ldg((const int4 *)at), y = __ldg((const int4 *)at + 1);
+    Slot k;
+    k.tok0 = x.x; k.nt = x.y; k.prob = x.z; k.blk0 = x.w;
+    k.nb = y.x - x.w; k.kv_len = y.y; k.lim0 = y.z; k.part = y.w;
+    k.step = k.prob >= 0 && p.a.causal ? 1 : 0;
+    return k;
+}
+// Blocks of [blk0, blk0 + nb) that the slot's last token sees.
+__device__ __forceinline__ void clip(Slot &k) {
+    const int lim = min(k.kv_len, k.lim0 + k.step * (k.nt - 1));
+    const int end = lim <= 0 ? 0 : (lim - 1) / attn::kBlock + 1;
+    k.nb = k.nt ? max(0, min(k.nb, end - k.blk0)) : 0;
+}
+
+__device__ __forceinline__ Work work_of(const KArgs &p, int w, int n_pairs, int n_single, int per_unit) {
     Work k;
-    const int4 x = __ldg((const int4 *)(p.a.items + w / p.a.hkv)), y = __ldg((const int4 *)(p.a.items + w / p.a.hkv) + 1);
-    k.it.tok0 = x.x; k.it.n_tok = x.y; k.it.prob = x.z; k.it.blk0 = x.w;
-    k.it.blk1 = y.x; k.it.kv_len = y.y; k.it.lim0 = y.z; k.it.part = y.w;
-    k.kvh = w % p.a.hkv;
-    k.step = k.it.prob >= 0 && p.a.causal ? 1 : 0;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        k.nt[s] = min(max(k.it.n_tok - s * p.tpt, 0), p.tpt);
-        const int lim = min(k.it.kv_len, k.it.lim0 + k.step * (s * p.tpt + k.nt[s] - 1));
-        const int end = lim <= 0 ? 0 : (lim - 1) / attn::kBlock + 1;
-        k.nb[s] = k.nt[s] ? max(0, min(k.it.blk1, end) - k.it.blk0) : 0;
+    const int u = w / p.a.hkv;
+    k.kvh = w - u * p.a.hkv;
+    k.shared = u < n_pairs;
+    const int at = k.shared ? u : n_pairs + (u - n_pairs) * per_unit;
+    k.s[0] = slot_of(p, p.a.items + at);
+    if (k.shared) {
+        k.s[1] = k.s[0];
+        k.s[1].nt = k.s[0].nt - p.tpt;
+        k.s[0].nt = p.tpt;
+        k.s[1].tok0 += p.tpt;
+        k.s[1].lim0 += k.s[0].step * p.tpt;
+        if (k.s[1].part >= 0) k.s[1].part += p.tpt;
+    } else if (per_unit == 2 && at + 1 < n_pairs + n_single) {
+        k.s[1] = slot_of(p, p.a.items + at + 1);
+    } else {
+        k.s[1] = k.s[0];
+        k.s[1].nt = 0;
     }
-    k.n = max(k.nb[0], k.nb[1]);
+    clip(k.s[0]);
+    clip(k.s[1]);
+    k.n = max(k.s[0].nb, k.s[1].nb);
     return k;
 }
 
-// The w-th piece of work of this CTA: items come longest first, so every
+// The w-th piece of work of this CTA: units come longest first, so every
 // other round runs backwards to even the CTAs out.
 __device__ __forceinline__ int work_index(int round) {
     return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -204,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         for (int i = 0; i < kNS; ++i) {
             tc::mbar_init(&bars->kv_full[i], 1);
-            tc::mbar_init(&bars->kv_empty[i], 1);
+            tc::mbar_init(&bars->kv_empty[i], 2);  // one from each slot's MMA warp
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars->q_full[i], 1);
@@ -213,13 +243,14 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             tc::mbar_init(&bars->p_full[i][0], 4);
             tc::mbar_init(&bars->p_full[i][1], 4);
             tc::mbar_init(&bars->o_full[i], 1);
+            tc::mbar_init(&bars->fin[i], 1);
+            tc::mbar_init(&bars->turn[i], 1);
         }
-        tc::mbar_init(&bars->fin, 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tc::fence_proxy_async();
     }
-    if (warp == 11) {
+    if (warp == 10) {
         tc::tmem_alloc(&bars->tmem, 512);
         tc::tmem_relinquish();
     }
@@ -234,52 +265,73 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
     const uint32_t tmem = *(volatile uint32_t *)&bars->tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int n_work = __ldg(p.a.counters + attn::kItems) * p.a.hkv;
+    const int n_pairs = __ldg(p.a.counters + attn::kPairs), n_single = __ldg(p.a.counters + attn::kSingles);
+    // one-tile items go two to a unit when there are more of them than CTAs
+    const int per_unit = (long long)n_single * p.a.hkv > gridDim.x ? 2 : 1;
+    const int n_work = (n_pairs + (n_single + per_unit - 1) / per_unit) * p.a.hkv;
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
-            // ---- K and V blocks, one stage each, in the order K0 V0 K1 V1 ..
-            int fill = 0;
-            bool ok = true;
+            // ---- K and V blocks, one stage each: the first K of each stream, then
+            // for each block its V and the K of the block after it
             const int subs = attn::kBlock / p.box_rows;
             const int oob = (int)max(1LL, p.a.n_rows);  // a box from here on reads as zeros
+            int st = 0, fill = 0;
+            uint32_t par = 1;  // of the stage's last release
+            bool ok = true;
+            // this lane's box of a block: its first row
+            auto box_row = [&](const Slot &k, int j) {
+                const int key = (k.blk0 + j) * attn::kBlock + lane * p.box_rows;
+                if (lane >= subs || key >= k.kv_len) return oob;
+                const int32_t *tab = k.prob >= 0 ? p.a.table + (long long)k.prob * p.a.ld_table
+                                                 : p.a.ptable + (long long)(-1 - k.prob) * p.a.ld_ptable;
+                const long long x = p.a.page ? (long long)__ldg(tab + key / p.a.page) * p.a.page + key % p.a.page
+                                             : (long long)__ldg(tab) + key;
+                if (x < 0 || x + min(p.box_rows, k.kv_len - key) > p.a.n_rows)
+                    atomicExch(status, (int)LORA_ERR_DEVICE_INDEX);
+                return x < -(long long)p.box_rows || x > p.a.n_rows ? oob : (int)x;
+            };
+            auto load = [&](const CUtensorMap *map, int kvh, int row) {
+                if (fill >= kNS) ok &= wait(&bars->kv_empty[st], par, bars, status);
+                if (ok = all(ok); ok) {
+                    if (lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
+                    __syncwarp();
+                    if (lane < subs) {
+                        char *dst = ring + st * Sh::kStage + lane * p.box_rows * 128;
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            tc::tma_load_3d(dst + c * kChunkBytes, map, c * 64, kvh, row, &bars->kv_full[st]);
+                    }
+                    ++fill;
+                }
+                if (++st == kNS) {
+                    st = 0;
+                    par ^= 1u;
+                }
+            };
             for (int r = 0; ok; ++r) {
                 const int w = work_index(r);
                 if (r * (int)gridDim.x >= n_work) break;
                 if (w >= n_work) continue;
-                const Work k = work_of(p, w);
-                const int32_t *tab = k.it.prob >= 0 ? p.a.table + (long long)k.it.prob * p.a.ld_table
-                                                    : p.a.ptable + (long long)(-1 - k.it.prob) * p.a.ld_ptable;
-                for (int j = 0; j < k.n && ok; ++j) {
-                    // this lane's box: its first row
-                    int row = oob;
-                    const int key = (k.it.blk0 + j) * attn::kBlock + lane * p.box_rows;
-                    if (lane < subs && key < k.it.kv_len) {
-                        long long x = p.a.page ? (long long)__ldg(tab + key / p.a.page) * p.a.page + key % p.a.page
-                                               : (long long)__ldg(tab) + key;
-                        const int need = min(p.box_rows, k.it.kv_len - key);
-                        if (x < 0 || x + need > p.a.n_rows) atomicExch(status, (int)LORA_ERR_DEVICE_INDEX);
-                        row = x < -(long long)p.box_rows || x > p.a.n_rows ? oob : (int)x;
-                    }
+                const Work k = work_of(p, w, n_pairs, n_single, per_unit);
+                const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
+                int row[2] = {oob, oob};
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++fill) {
-                        const int st = fill % kNS;
-                        if (fill >= kNS && !warp_wait(&bars->kv_empty[st], (uint32_t)((fill / kNS - 1) & 1), bars, status)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
-                        __syncwarp();
-                        if (lane < subs) {
-                            char *dst = ring + st * Sh::kStage + lane * p.box_rows * 128;
-#pragma unroll
-                            for (int c = 0; c < NCH; ++c)
-                                tc::tma_load_3d(dst + c * kChunkBytes, kv ? &p.tv : &p.tk, c * 64, k.kvh, row,
-                                                &bars->kv_full[st]);
-                        }
+                for (int c = 0; c < 2; ++c)
+                    if (nb[c]) {
+                        row[c] = box_row(k.s[c], 0);
+                        load(&p.tk, k.kvh, row[c]);
                     }
-                }
+                for (int j = 0; j < k.n && ok; ++j)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (j < nb[c]) {
+                            const int next = j + 1 < nb[c] ? box_row(k.s[c], j + 1) : oob;
+                            load(&p.tv, k.kvh, row[c]);
+                            if (j + 1 < nb[c]) load(&p.tk, k.kvh, next);
+                            row[c] = next;
+                        }
             }
             // every copy has landed before the CTA ends
             for (int s = 0; s < kNS && s < fill; ++s) {
@@ -295,10 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const int w = work_index(r);
                 if (r * (int)gridDim.x >= n_work) break;
                 if (w >= n_work) continue;
-                const Work k = work_of(p, w);
+                const Work k = work_of(p, w, n_pairs, n_single, per_unit);
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    if (!k.nb[s] || !ok) continue;
+                    if (!k.s[s].nb || !ok) continue;
                     if (fill[s] && !warp_wait(&bars->q_empty[s], (uint32_t)((fill[s] - 1) & 1), bars, status)) {
                         ok = false;
                         continue;
@@ -308,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
 #pragma unroll
                         for (int c = 0; c < NCH; ++c)
                             tc::tma_load_3d(sq + s * Sh::kStage + c * kChunkBytes, &p.tq, c * 64, k.kvh * p.a.G,
-                                            k.it.tok0 + s * p.tpt, &bars->q_full[s]);
+                                            k.s[s].tok0, &bars->q_full[s]);
                     }
                     __syncwarp();
                     ++fill[s];
@@ -320,146 +372,192 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 while (fill[s] && !tc::mbar_try_wait(&bars->q_full[s], (uint32_t)((fill[s] - 1) & 1)) &&
                        ++polls < (1 << 16)) {}
             }
-        } else if (warp == 9) {
-            // ---- MMA issue
+        } else {
+            // ---- MMA issue of one slot
             constexpr uint32_t id_qk = tc::idesc_bf16(128, 128), id_pv = tc::idesc_bf16_bmn(128, Sh::kDP);
+            const int s = warp == 9 ? 0 : 1;
             int st = 0;                // the next stage of the ring and its parity
             uint32_t par = 0;
-            auto next = [&]() {
+            auto step = [&]() {
                 if (++st == kNS) {
                     st = 0;
                     par ^= 1u;
                 }
             };
-            uint32_t pq[2] = {0, 0}, pp[2] = {0, 0};
+            uint32_t pq = 0, pp = 0, pt = 0;
             bool ok = true;
             // lower halves of the descriptors (shared addresses end below 2^18): of K-major
             // tiles, and of V, whose 64-element chunks are kChunkBytes apart
-            const uint32_t q_lo = (tc::smem_u32(sq) >> 4) | (1u << 16), k_lo = (tc::smem_u32(ring) >> 4) | (1u << 16);
+            const uint32_t q_lo = ((tc::smem_u32(sq) + s * Sh::kStage) >> 4) | (1u << 16);
+            const uint32_t k_lo = (tc::smem_u32(ring) >> 4) | (1u << 16);
             const uint32_t v_lo = (tc::smem_u32(ring) >> 4) | ((uint32_t)(kChunkBytes >> 4) << 16);
-            auto qk = [&](int s, int stage) {  // by one lane
-                const uint32_t qa = q_lo + s * (Sh::kStage >> 4), ka = k_lo + stage * (Sh::kStage >> 4);
+            const uint32_t ts = tmem + s * 128, to = tmem + 256 + s * Sh::kDP;
+            uint64_t *s_full = &bars->s_full[s], *p_full = bars->p_full[s];
+            auto qk = [&](int stage) {  // by one lane
+                const uint32_t ka = k_lo + stage * (Sh::kStage >> 4);
 #pragma unroll
                 for (int i = 0; i < NCH * 4; ++i) {
                     const uint32_t off = (uint32_t)((i >> 2) * kChunkBytes + (i & 3) * 32) >> 4;
-                    mma_ss(tmem + s * 128, qa + off, ka + off, id_qk, i != 0);
+                    mma_ss(ts, q_lo + off, ka + off, id_qk, i != 0);
                 }
-                tc::mma_commit(&bars->s_full[s]);
+                tc::mma_commit(s_full);
             };
-            auto pv = [&](int s, int h, int stage, bool first) {
+            auto pv = [&](int h, int stage, bool first) {
                 const uint32_t va = v_lo + stage * (Sh::kStage >> 4) + h * (8192 >> 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mma_ts(tmem + 256 + s * Sh::kDP, tmem + s * 128 + h * 32 + i * 8, va + i * (2048 >> 4), id_pv,
-                           h || i ? true : !first);
+                    mma_ts(to, ts + h * 32 + i * 8, va + i * (2048 >> 4), id_pv, h || i ? true : !first);
+            };
+            // Fills of the other slot's stream.  Both warps see every phase of every stage
+            // (a parity wait is exact only within one phase), so both give every stage back.
+            auto pass = [&](int n) {
+                for (; n; --n) {
+                    ok &= wait(&bars->kv_full[st], par, bars, status);
+                    if (elect_one()) tc::mbar_arrive(&bars->kv_empty[st]);
+                    step();
+                }
             };
             for (int r = 0; ok; ++r) {
                 const int w = work_index(r);
                 if (r * (int)gridDim.x >= n_work) break;
                 if (w >= n_work) continue;
-                const Work k = work_of(p, w);
-                if (!k.n) continue;
-                // the first block's S
-                ok &= wait(&bars->kv_full[st], par, bars, status);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (!k.nb[s]) continue;
-                    ok &= wait(&bars->q_full[s], pq[s], bars, status);
-                    pq[s] ^= 1u;
-                    tc::tc_fence_after();
-                    if (elect_one()) {
-                        qk(s, st);
-                        if (k.nb[s] == 1) tc::mma_commit(&bars->q_empty[s]);
-                    }
-                }
-                if (elect_one()) tc::mma_commit(&bars->kv_empty[st]);
-                next();
-                const int full = (k.it.kv_len >> 7) - k.it.blk0;  // blocks whose keys all count
-                for (int j = 0; j < k.n; ++j) {
-                    const bool more = j + 1 < k.n;
-                    const int sv = st;
+                const Work k = work_of(p, w, n_pairs, n_single, per_unit);
+                const Slot &me = s ? k.s[1] : k.s[0];
+                const int nb = me.nb, other = s ? k.s[0].nb : k.s[1].nb;
+                const bool alone = !k.shared;
+                const int n = alone ? nb : k.n;  // blocks of the stream
+                // the first K of the slot's stream; another stream's K comes before or after it
+                if (alone && s && other) pass(1);
+                if (n) {
                     ok &= wait(&bars->kv_full[st], par, bars, status);
-                    next();
-                    const int sk = st;
-                    if (more) {
-                        ok &= wait(&bars->kv_full[st], par, bars, status);
-                        next();
-                    }
-                    // values of a block's keys past the end count for nothing, whatever their rows hold
-                    if (j >= full) {
-                        char *v = ring + sv * Sh::kStage;
-                        for (int i = (k.it.kv_len & 127) * 8 + lane; i < attn::kBlock * 8; i += 32)
-#pragma unroll
-                            for (int c = 0; c < NCH; ++c) *(uint4 *)(v + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
-                        tc::fence_proxy_async();
-                        __syncwarp();
-                    }
-                    if (!(ok = all(ok))) break;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (j >= k.nb[s]) continue;
-                        ok &= wait(&bars->p_full[s][0], pp[s], bars, status);
+                    if (nb) {
+                        ok &= wait(&bars->q_full[s], pq, bars, status);
+                        pq ^= 1u;
                         tc::tc_fence_after();
-                        if (elect_one()) pv(s, 0, sv, j == 0);
-                        ok &= wait(&bars->p_full[s][1], pp[s], bars, status);
-                        pp[s] ^= 1u;
-                        tc::tc_fence_after();
-                        if (elect_one()) {
-                            pv(s, 1, sv, false);
-                            if (j + 1 < k.nb[s]) {
-                                qk(s, sk);
-                                if (j + 2 == k.nb[s]) tc::mma_commit(&bars->q_empty[s]);
-                            } else {
-                                tc::mma_commit(&bars->o_full[s]);
+                    }
+                    if (elect_one()) {
+                        if (nb) qk(st);
+                        if (nb == 1) tc::mma_commit(&bars->q_empty[s]);
+                        tc::mma_commit(&bars->kv_empty[st]);
+                    }
+                    step();
+                }
+                if (alone && !s && other) pass(1);
+                const int full = (me.kv_len >> 7) - me.blk0;  // blocks whose keys all count
+                for (int j = 0; j < k.n; ++j) {
+                    // fills of the other stream that come between
+                    const int between = alone && j < other ? (j + 1 < other ? 2 : 1) : 0;
+                    if (s) pass(between);
+                    // The slots of one stream issue by turns, so that one slot's products are
+                    // done, and its softmax begins, while the other's are still to come.
+                    auto turn = [&]() {
+                        if (alone || (!s && !j)) return;
+                        ok &= wait(&bars->turn[s], pt, bars, status);
+                        pt ^= 1u;
+                    };
+                    if (j < n) {
+                        const bool more = j + 1 < n;
+                        const int sv = st;
+                        const uint32_t par_v = par;
+                        step();
+                        const int sk = st;
+                        const uint32_t par_k = par;
+                        if (more) step();
+                        if (!(tc::mbar_try_wait(&bars->kv_full[sv], par_v) &
+                              (!more || tc::mbar_try_wait(&bars->kv_full[sk], par_k)))) {
+                            ok &= wait(&bars->kv_full[sv], par_v, bars, status);
+                            if (more) ok &= wait(&bars->kv_full[sk], par_k, bars, status);
+                        }
+                        if (j >= full) {
+                            // values past the last key count for nothing, whatever their rows
+                            // hold (boxes past the one it is in are zeros already; the slots of
+                            // one stream both write the same zeros)
+                            const int left = me.kv_len - (me.blk0 + j) * attn::kBlock;
+                            const int end = (left + p.box_rows - 1) / p.box_rows * p.box_rows * 8;
+                            char *v = ring + sv * Sh::kStage;
+                            for (int i = left * 8 + lane; i < end; i += 32)
+#pragma unroll
+                                for (int c = 0; c < NCH; ++c)
+                                    *(uint4 *)(v + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                            tc::fence_proxy_async();
+                        }
+                        if (j < nb) {
+                            ok &= wait(&p_full[0], pp, bars, status);
+                            turn();
+                            tc::tc_fence_after();
+                            if (elect_one()) pv(0, sv, j == 0);
+                            ok &= wait(&p_full[1], pp, bars, status);
+                            pp ^= 1u;
+                            tc::tc_fence_after();
+                            if (elect_one()) {
+                                pv(1, sv, false);
+                                if (j + 1 < nb) {
+                                    qk(sk);
+                                    if (j + 2 == nb) tc::mma_commit(&bars->q_empty[s]);
+                                } else {
+                                    tc::mma_commit(&bars->o_full[s]);
+                                }
+                                if (!alone && (j + 1 < n || !s)) tc::mbar_arrive(&bars->turn[1 - s]);
+                                tc::mma_commit(&bars->kv_empty[sv]);
+                                if (more) tc::mma_commit(&bars->kv_empty[sk]);
                             }
-                            if (s == 1 || j >= k.nb[1]) {  // the last of the slots: the stages are free
+                        } else {
+                            turn();
+                            if (elect_one()) {
+                                if (!alone && (j + 1 < n || !s)) tc::mbar_arrive(&bars->turn[1 - s]);
                                 tc::mma_commit(&bars->kv_empty[sv]);
                                 if (more) tc::mma_commit(&bars->kv_empty[sk]);
                             }
                         }
                     }
-                    __syncwarp();
+                    if (!s) pass(between);
                 }
                 ok = all(ok);
             }
             // all products are done before tensor memory is given back
-            if (lane == 0) tc::mma_commit(&bars->fin);
+            if (lane == 0) tc::mma_commit(&bars->fin[s]);
             __syncwarp();
             int polls = 0;
-            while (!tc::mbar_try_wait(&bars->fin, 0) && ++polls < (1 << 20)) {}
+            while (!tc::mbar_try_wait(&bars->fin[s], 0) && ++polls < (1 << 20)) {}
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax and epilogue of one slot, a row per thread
         const int s = warp >> 2, q = warp & 3, row = q * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
         const uint32_t ts = tl + s * 128, to = tl + 256 + s * Sh::kDP;
         const int e = row / p.a.G, g = row - e * p.a.G;
-        int ns = 0, no = 0;
+        const float scale = p.a.scale_log2;
+        uint32_t ps = 0, po = 0;
         bool ok = true;
         for (int r = 0; ok; ++r) {
             const int w = work_index(r);
             if (r * (int)gridDim.x >= n_work) break;
             if (w >= n_work) continue;
-            const Work k = work_of(p, w);
-            const int nt = k.nt[s], nb = k.nb[s];
-            if (!nt) continue;
-            const bool live = e < nt, warp_live = __any_sync(0xffffffffu, live);
+            Slot k;
+            int kvh;
+            {
+                const Work u = work_of(p, w, n_pairs, n_single, per_unit);
+                k = s ? u.s[1] : u.s[0];
+                kvh = u.kvh;
+            }
+            if (!k.nt) continue;
+            const bool live = e < k.nt, warp_live = __any_sync(0xffffffffu, live);
             // keys that the row sees; a row that is not there masks nothing
-            const int lim = live ? min(k.it.kv_len, k.it.lim0 + k.step * (s * p.tpt + e)) : 0x7fffffff;
+            const int lim = live ? min(k.kv_len, k.lim0 + k.step * e) : 0x7fffffff;
             const int min_lim = __reduce_min_sync(0xffffffffu, lim);
             float m = -INFINITY, l = 0.f, base = 0.f;
             bool huge = false;
-            for (int j = 0; j < nb; ++j) {
-                if (!(ok = warp_wait(&bars->s_full[s], (uint32_t)(ns & 1), bars, status))) break;
-                ++ns;
+            for (int j = 0; j < k.nb; ++j) {
+                if (!(ok = warp_wait(&bars->s_full[s], ps, bars, status))) break;
+                ps ^= 1u;
                 if (warp_live) {
                     tc::tc_fence_after();
                     uint32_t x[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + c * 32, x[c]);
                     tc::tmem_wait_ld();
-                    const int key0 = (k.it.blk0 + j) * attn::kBlock;
+                    const int key0 = (k.blk0 + j) * attn::kBlock;
                     if (key0 + attn::kBlock > min_lim) {
                         const int rel = lim - key0;
 #pragma unroll
@@ -478,43 +576,51 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                         mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
                     }
                     const float bm = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    // the maximum in use stays while no row is more than kLag above it
-                    if (__any_sync(0xffffffffu, live && !((bm - m) * p.a.scale_log2 <= kLag))) {
+                    // the maximum in use stays while no row's scores are more than kLag above it
+                    if (__any_sync(0xffffffffu, live && !((bm - m) * scale <= kLag))) {
                         const float mn = fmaxf(m, bm);
-                        const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * p.a.scale_log2);
+                        const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * scale);
                         m = mn;
                         l *= f;
-                        base = m == -INFINITY ? 0.f : m * p.a.scale_log2;
+                        base = m == -INFINITY ? 0.f : m * scale;
                         huge = __any_sync(0xffffffffu, live && !(fabsf(base) <= kExactBase));
 #pragma unroll 1
-                        for (int c = 0; j && c < Sh::kDP / 32; ++c) {  // the output so far, with the weights
-                            uint32_t o[32], o0[16], o1[16];
-                            tc::tmem_ld32(to + c * 32, o);
+                        for (int c = 0; j && c < Sh::kDP / 16; ++c) {  // the output so far, with the weights
+                            uint32_t o[16];
+                            tc::tmem_ld16(to + c * 16, o);
                             tc::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                o0[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                o1[i] = __float_as_uint(__uint_as_float(o[16 + i]) * f);
-                            }
-                            tc::tmem_st16(to + c * 32, o0);
-                            tc::tmem_st16(to + c * 32 + 16, o1);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc::tmem_st16(to + c * 16, o);
                         }
                     }
                     // 2^(x * scale - base): whatever base was rounded to divides out, unless
-                    // it is so large that its rounding is
-                    float sc = p.a.scale_log2, sb = -base;
+                    // it is so large that its rounding is; then x - maximum goes first
+                    f32x2 sc2 = two(scale, scale), sb2 = two(-base, -base), s0 = two(0.f, 0.f), s1 = s0;
                     if (huge) {
                         const float mm = m == -INFINITY ? 0.f : m;
+                        tc::tmem_st32(ts, x[0]);
+                        tc::tmem_st32(ts + 32, x[1]);
+                        tc::tmem_st32(ts + 64, x[2]);
+                        tc::tmem_st32(ts + 96, x[3]);
+                        tc::tmem_wait_st();
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            tc::tmem_ld16(ts + c * 16, o);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint((__uint_as_float(o[i]) - mm) * scale);
+                            tc::tmem_st16(ts + c * 16, o);
+                        }
+                        tc::tmem_wait_st();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[c][i] = __float_as_uint((__uint_as_float(x[c][i]) - mm) * sc);
-                        sc = 1.f;
-                        sb = 0.f;
+                        for (int c = 0; c < 4; ++c) tc::tmem_ld32(ts + c * 32, x[c]);
+                        tc::tmem_wait_ld();
+                        sc2 = two(1.f, 1.f);
+                        sb2 = two(0.f, 0.f);
                     }
-                    const f32x2 sc2 = two(sc, sc), sb2 = two(sb, sb);
-                    f32x2 sum[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t pk[16];
@@ -524,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                                                   sc2, sb2));
                             v.x = ex2(v.x);
                             v.y = ex2(v.y);
-                            sum[i & 1] = add2(sum[i & 1], two(v.x, v.y));
+                            if (i & 1) s1 = add2(s1, two(v.x, v.y)); else s0 = add2(s0, two(v.x, v.y));
                             pk[i] = pack2(v.x, v.y);
                         }
                         tc::tmem_st16(ts + c * 16, pk);
@@ -535,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                             if (lane == 0) tc::mbar_arrive(&bars->p_full[s][0]);
                         }
                     }
-                    const float2 sm = apart(add2(sum[0], sum[1]));
+                    const float2 sm = apart(add2(s0, s1));
                     l += sm.x + sm.y;
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
@@ -547,44 +653,43 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 }
             }
             if (!ok) break;
-            if (nb) {
-                if (!(ok = warp_wait(&bars->o_full[s], (uint32_t)(no & 1), bars, status))) break;
-                ++no;
+            if (k.nb) {
+                if (!(ok = warp_wait(&bars->o_full[s], po, bars, status))) break;
+                po ^= 1u;
                 tc::tc_fence_after();
             }
             if (warp_live) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int t = k.it.tok0 + s * p.tpt + e, h = k.kvh * p.a.G + g;
-                const long long prow = (long long)(k.it.part + s * p.tpt + e) * p.a.hq + h;
+                const int t = k.tok0 + e, h = kvh * p.a.G + g;
+                const long long prow = (long long)(k.part + e) * p.a.hq + h;
                 uint16_t *out = p.a.out + (long long)t * p.a.ldo + (long long)h * p.a.D;
-                float *po = p.a.part_o + prow * p.a.D;
+                float *part = p.a.part_o + prow * p.a.D;
 #pragma unroll 1
                 for (int c = 0; c < Sh::kDP / 32; ++c) {
                     uint32_t o[32];
-                    if (nb) {
+                    if (k.nb) {
                         tc::tmem_ld32(to + c * 32, o);
                         tc::tmem_wait_ld();
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        o[i] = nb && l != 0.f ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                        o[i] = k.nb && l != 0.f ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
                     if (!live) continue;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int col = c * 32 + i * 8;
                         if (col >= p.a.D) break;
                         const float *f = (const float *)&o[i * 8];
-                        if (k.it.part < 0) {
+                        if (k.part < 0) {
                             *(uint4 *)(out + col) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]),
                                                                pack2(f[6], f[7]));
                         } else {
-                            *(float4 *)(po + col) = make_float4(f[0], f[1], f[2], f[3]);
-                            *(float4 *)(po + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                            *(float4 *)(part + col) = make_float4(f[0], f[1], f[2], f[3]);
+                            *(float4 *)(part + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
                         }
                     }
                 }
-                if (live && k.it.part >= 0)
-                    p.a.part_lse[prow] = l == 0.f ? -INFINITY : m * p.a.scale_log2 + log2f(l);
+                if (live && k.part >= 0) p.a.part_lse[prow] = l == 0.f ? -INFINITY : m * scale + log2f(l);
                 tc::tc_fence_before();
             }
         }
@@ -592,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    if (warp == 11) tc::tmem_dealloc(tmem, 512);
+    if (warp == 10) tc::tmem_dealloc(tmem, 512);
 }
 
 std::atomic<int> g_attn_sms[64];  // SM count per device, looked up once

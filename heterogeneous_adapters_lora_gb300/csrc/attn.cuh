@@ -23,7 +23,8 @@ constexpr int kBlock = 128;     // keys of a block
 constexpr int kTargetItems = 2 * 152;
 constexpr int kMinBlocks = 4;
 
-// One item of a plan (8 words).
+// One item of a plan (8 words).  The kPairs items of two row tiles come first,
+// then the kSingles items of one, each kind longest first.
 struct Item {
     int tok0, n_tok;  // its query tokens
     int prob;         // sequence b, or -1 - g for the prefix of group g
@@ -35,7 +36,7 @@ struct Item {
 static_assert(sizeof(Item) == 32, "plan items are 8 words");
 
 // counters[] of a plan
-enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3 };
+enum { kPairs = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kSingles = 4 };
 
 // tokens of an item's first or second row tile, and of an item
 __host__ __device__ inline int tile_tokens(int group) { return kTileRows / group; }

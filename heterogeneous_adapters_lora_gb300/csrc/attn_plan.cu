@@ -90,7 +90,7 @@ __device__ __forceinline__ int find_problem(const int32_t *first, int n, int til
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
-    __shared__ int hist[kBuckets];
+    __shared__ int hist[2][kBuckets];  // items of two tiles, of one
     __shared__ unsigned long long total_blocks;
     __shared__ int bad;
     const int tid = threadIdx.x;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         total_blocks = 0;
         bad = 0;
     }
-    for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+    for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = hist[1][i] = 0;
     __syncthreads();
     // the lengths keep to the rules, or the plan is empty
     for (int b = tid; b < p.n_seqs; b += kPlanThreads) {
@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     if (bad) {
         if (tid == 0) {
-            p.counters[attn::kItems] = p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = 0;
+            p.counters[attn::kPairs] = p.counters[attn::kSingles] = 0;
+            p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = 0;
             p.counters[attn::kStatus] = LORA_ERR_DEVICE_INDEX;
         }
         return;
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         (total_blocks * (unsigned long long)p.hkv + attn::kTargetItems - 1) / attn::kTargetItems;
     const int range = (int)max((unsigned long long)attn::kMinBlocks, want);
     // items and partial rows of each tile; the histogram of item lengths
-    int n_items = 0, n_part = 0;
+    int n_part = 0;
     for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
         const int t = t0 + tid;
         int parts = 0, rows = 0, sum, blocks = 0, n_tok = 0, tok0 = 0, i = 0;
@@ -183,8 +184,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         const int part0 = n_part + block_scan(rows, &sum);
         n_part += sum;
-        block_scan(parts, &sum);
-        n_items += sum;
         if (t < n_tiles) {
             *(int4 *)(p.tiles + 4 * (long long)t) = make_int4(joined ? part0 : -1, parts, tok0, n_tok);
             if (joined && parts) {
@@ -193,17 +192,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             }
             for (int s = 0; s < parts; ++s) {
                 const int len = (int)((long long)(s + 1) * blocks / parts) - (int)((long long)s * blocks / parts);
-                atomicAdd(&hist[min(len, kBuckets - 1)], 1);
+                atomicAdd(&hist[2 * n_tok <= p.tpi][min(len, kBuckets - 1)], 1);
             }
         }
     }
     __syncthreads();
     // where each length starts, the longest first
     {
-        int sum;
+        int pairs, singles;
         const int b = kBuckets - 1 - tid;
-        const int at = block_scan(hist[b], &sum);
-        hist[b] = at;
+        const int at0 = block_scan(hist[0][b], &pairs), at1 = block_scan(hist[1][b], &singles);
+        hist[0][b] = at0;
+        hist[1][b] = pairs + at1;
+        if (tid == 0) {
+            p.counters[attn::kPairs] = pairs;
+            p.counters[attn::kSingles] = singles;
+        }
     }
     __syncthreads();
     for (int t = tid; t < n_tiles; t += kPlanThreads) {
@@ -221,14 +225,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             it.kv_len = q.len;
             it.lim0 = q.causal ? q.len - q.n_tok + j * p.tpi + 1 : q.len;
             it.part = e.x < 0 ? -1 : e.x + s * e.w;
-            const int at = atomicAdd(&hist[min(it.blk1 - it.blk0, kBuckets - 1)], 1);
+            const int at = atomicAdd(&hist[2 * it.n_tok <= p.tpi][min(it.blk1 - it.blk0, kBuckets - 1)], 1);
             int4 *dst = (int4 *)(p.items + at);
             dst[0] = make_int4(it.tok0, it.n_tok, it.prob, it.blk0);
             dst[1] = make_int4(it.blk1, it.kv_len, it.lim0, it.part);
         }
     }
     if (tid == 0) {
-        p.counters[attn::kItems] = n_items;
         p.counters[attn::kPartTokens] = n_part;
         p.counters[attn::kTiles] = n_tiles;
         p.counters[attn::kStatus] = LORA_OK;

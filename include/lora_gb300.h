@@ -486,11 +486,13 @@ typedef struct {
 /* The work of one batch, laid out from its lengths alone: built once per step
  * and used by every layer of the step whose heads and page size are the
  * same.  Caller-owned device memory, bound with lora_attn_plan_bind.
- *   items[max_items][8]  tiles of queries x ranges of keys, the longest first
+ *   items[max_items][8]  tiles of queries x ranges of keys: those of two row tiles,
+ *                        then those of one, each the longest first
  *   tiles[max_tiles][4]  tiles of queries and where their partial results lie
  *   token_tiles[2][max_tokens]  each token's own tile and prefix tile (-1: none
  *                        that has to be joined)
- *   counters[8]          items, partial token rows, tiles, (3) status word
+ *   counters[8]          items of two row tiles, partial token rows, tiles, status
+ *                        word, items of one row tile
  * The host fields n_seqs .. max_prefix_len record the last build. */
 typedef struct {
     lora_attn_desc_t desc;
