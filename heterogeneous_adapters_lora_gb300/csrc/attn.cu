@@ -47,21 +47,40 @@ struct KArgs {
     int q_bytes;   // bytes of a Q tile's copies
 };
 
-template <int NCH>
-struct Shape {
-    static constexpr int kDP = 64 * NCH;                      // head size in the products
-    static constexpr int kStage = NCH * kChunkBytes;          // one K or V block
-    static constexpr int kStages = NCH == 2 ? 5 : 10;
-    static constexpr int kSmem = 1024 + 2 * kStage + kStages * kStage + 512;
+// A slot's part of a unit.
+struct Slot {
+    int tok0, nt;       // its tokens
+    int prob, kv_len;   // whose keys, and how many
+    int blk0, nb;       // its blocks
+    int lim0, step;     // keys that its first token sees, and that each further one sees more
+    int part;           // token row of its partial result, or -1
 };
+struct Work {
+    Slot s[2];
+    int shared;  // both slots run over slot 0's stream (of n blocks)
+    int n;       // blocks of the longer slot; -1: no more work
+    int kvh;
+};
+constexpr int kWorks = 4;
 
 struct Bars {
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[2], q_empty[2], s_full[2], o_full[2], fin[2];
     uint64_t turn[2];       // a slot's turn to issue, when the slots share a stream
     uint64_t p_full[2][2];  // of each slot: the first and the second 64 keys of P
+    uint64_t work_full[kWorks], work_empty[kWorks];
+    Work work[kWorks];
     uint32_t tmem;
     int abort;
+};
+
+template <int NCH>
+struct Shape {
+    static constexpr int kDP = 64 * NCH;                      // head size in the products
+    static constexpr int kStage = NCH * kChunkBytes;          // one K or V block
+    static constexpr int kStages = NCH == 2 ? 5 : 10;
+    static constexpr int kSmem = 1024 + 2 * kStage + kStages * kStage + 1024;
+    static_assert(sizeof(Bars) <= 1024, "barriers and work");
 };
 
 // Bounded wait; false when it gave up here or somewhere else in the CTA.
@@ -84,23 +103,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *
     return all(wait(bar, parity, b, status));
 }
 
-// A slot's part of a unit, as all roles derive it.
-struct Slot {
-    int tok0, nt;       // its tokens
-    int prob, kv_len;   // whose keys, and how many
-    int blk0, nb;       // its blocks
-    int lim0, step;     // keys that its first token sees, and that each further one sees more
-    int part;           // token row of its partial result, or -1
-};
-struct Work {
-    Slot s[2];
-    bool shared;  // both slots run over slot 0's stream (of n blocks)
-    int n;        // blocks of the longer slot
-    int kvh;
-};
-
-__device__ __forceinline__ Slot slot_of(const KArgs &p, const attn::Item *at) {
-    const int4 x = __ldg((const int4 *)at), y = __ldg((const int4 *)at + 1);
+__device__ __forceinline__ Slot slot_of(const KArgs &p, int item) {
+    const int4 *at = (const int4 *)(p.a.items + item);
+    const int4 x = __ldg(at), y = __ldg(at + 1);
     Slot k;
     k.tok0 = x.x; k.nt = x.y; k.prob = x.z; k.blk0 = x.w;
     k.nb = y.x - x.w; k.kv_len = y.y; k.lim0 = y.z; k.part = y.w;
@@ -113,37 +118,28 @@ __device__ __forceinline__ void clip(Slot &k) {
     const int end = lim <= 0 ? 0 : (lim - 1) / attn::kBlock + 1;
     k.nb = k.nt ? max(0, min(k.nb, end - k.blk0)) : 0;
 }
-
-__device__ __forceinline__ Work work_of(const KArgs &p, int w, int n_pairs, int n_single, int per_unit) {
+__device__ __forceinline__ Work work_of(const KArgs &p, int w) {
     Work k;
     const int u = w / p.a.hkv;
     k.kvh = w - u * p.a.hkv;
-    k.shared = u < n_pairs;
-    const int at = k.shared ? u : n_pairs + (u - n_pairs) * per_unit;
-    k.s[0] = slot_of(p, p.a.items + at);
+    const int word = __ldg(p.a.units + u);
+    k.shared = (word & 3) == attn::kPair;
+    k.s[0] = k.s[1] = slot_of(p, word >> 2);
     if (k.shared) {
-        k.s[1] = k.s[0];
         k.s[1].nt = k.s[0].nt - p.tpt;
         k.s[0].nt = p.tpt;
         k.s[1].tok0 += p.tpt;
         k.s[1].lim0 += k.s[0].step * p.tpt;
         if (k.s[1].part >= 0) k.s[1].part += p.tpt;
-    } else if (per_unit == 2 && at + 1 < n_pairs + n_single) {
-        k.s[1] = slot_of(p, p.a.items + at + 1);
+    } else if ((word & 3) == attn::kTwo) {
+        k.s[1] = slot_of(p, (word >> 2) + 1);
     } else {
-        k.s[1] = k.s[0];
         k.s[1].nt = 0;
     }
     clip(k.s[0]);
     clip(k.s[1]);
     k.n = max(k.s[0].nb, k.s[1].nb);
     return k;
-}
-
-// The w-th piece of work of this CTA: units come longest first, so every
-// other round runs backwards to even the CTAs out.
-__device__ __forceinline__ int work_index(int round) {
-    return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -247,6 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             tc::mbar_init(&bars->turn[i], 1);
         }
         bars->abort = 0;
+        for (int i = 0; i < kWorks; ++i) {
+            tc::mbar_init(&bars->work_full[i], 1);
+            tc::mbar_init(&bars->work_empty[i], kThreads / 32 - 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tc::fence_proxy_async();
     }
@@ -265,10 +265,19 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
     const uint32_t tmem = *(volatile uint32_t *)&bars->tmem;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const int n_pairs = __ldg(p.a.counters + attn::kPairs), n_single = __ldg(p.a.counters + attn::kSingles);
-    // one-tile items go two to a unit when there are more of them than CTAs
-    const int per_unit = (long long)n_single * p.a.hkv > gridDim.x ? 2 : 1;
-    const int n_work = (n_pairs + (n_single + per_unit - 1) / per_unit) * p.a.hkv;
+    // The units of this CTA, as warp 8 takes them; every other warp waits for
+    // the next, reads it in place and gives it back.
+    int round = 0;
+    auto next_work = [&](bool &ok) -> const Work * {
+        ok = ok && warp_wait(&bars->work_full[round % kWorks], (uint32_t)((round / kWorks) & 1), bars, status);
+        const Work *k = &bars->work[round % kWorks];
+        return ok && k->n >= 0 ? k : nullptr;
+    };
+    auto done_work = [&]() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->work_empty[round % kWorks]);
+        ++round;
+    };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -310,11 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     par ^= 1u;
                 }
             };
-            for (int r = 0; ok; ++r) {
-                const int w = work_index(r);
-                if (r * (int)gridDim.x >= n_work) break;
-                if (w >= n_work) continue;
-                const Work k = work_of(p, w, n_pairs, n_single, per_unit);
+            const int n_work = __ldg(p.a.counters + attn::kUnits) * p.a.hkv;
+            int w = blockIdx.x;  // the first is given, the others are taken as they come
+            while (ok) {
+                Work k;
+                if (w < n_work) k = work_of(p, w);
+                if (round >= kWorks)
+                    ok = warp_wait(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
+                if (lane == 0) {
+                    if (w < n_work) bars->work[round % kWorks] = k; else bars->work[round % kWorks].n = -1;
+                    tc::mbar_arrive(&bars->work_full[round % kWorks]);
+                }
+                __syncwarp();
+                ++round;
+                if (w >= n_work) break;
                 const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
                 int row[2] = {oob, oob};
 #pragma unroll
@@ -332,6 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                             if (j + 1 < nb[c]) load(&p.tk, k.kvh, next);
                             row[c] = next;
                         }
+                if (lane == 0) w = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
+                w = __shfl_sync(0xffffffffu, w, 0);
+            }
+            if (lane == 0 && atomicAdd(p.a.tickets + 1, 1) == (int)gridDim.x - 1) {
+                p.a.tickets[0] = 0;  // the last CTA to end leaves them as they were
+                p.a.tickets[1] = 0;
             }
             // every copy has landed before the CTA ends
             for (int s = 0; s < kNS && s < fill; ++s) {
@@ -343,11 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             // ---- Q tiles
             int fill[2] = {0, 0};
             bool ok = true;
-            for (int r = 0; ok; ++r) {
-                const int w = work_index(r);
-                if (r * (int)gridDim.x >= n_work) break;
-                if (w >= n_work) continue;
-                const Work k = work_of(p, w, n_pairs, n_single, per_unit);
+            while (const Work *at = next_work(ok)) {
+                const Work &k = *at;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!k.s[s].nb || !ok) continue;
@@ -365,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     __syncwarp();
                     ++fill[s];
                 }
+                done_work();
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -417,15 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     step();
                 }
             };
-            for (int r = 0; ok; ++r) {
-                const int w = work_index(r);
-                if (r * (int)gridDim.x >= n_work) break;
-                if (w >= n_work) continue;
-                const Work k = work_of(p, w, n_pairs, n_single, per_unit);
-                const Slot &me = s ? k.s[1] : k.s[0];
-                const int nb = me.nb, other = s ? k.s[0].nb : k.s[1].nb;
-                const bool alone = !k.shared;
-                const int n = alone ? nb : k.n;  // blocks of the stream
+            while (const Work *k = next_work(ok)) {
+                const Slot &me = k->s[s];
+                const int nb = me.nb, other = k->s[1 - s].nb, most = k->n;
+                const bool alone = !k->shared;
+                const int n = alone ? nb : most;  // blocks of the stream
                 // the first K of the slot's stream; another stream's K comes before or after it
                 if (alone && s && other) pass(1);
                 if (n) {
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 }
                 if (alone && !s && other) pass(1);
                 const int full = (me.kv_len >> 7) - me.blk0;  // blocks whose keys all count
-                for (int j = 0; j < k.n; ++j) {
+                for (int j = 0; j < most; ++j) {
                     // fills of the other stream that come between
                     const int between = alone && j < other ? (j + 1 < other ? 2 : 1) : 0;
                     if (s) pass(between);
@@ -513,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     if (!s) pass(between);
                 }
                 ok = all(ok);
+                done_work();
             }
             // all products are done before tensor memory is given back
             if (lane == 0) tc::mma_commit(&bars->fin[s]);
@@ -530,17 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
         const float scale = p.a.scale_log2;
         uint32_t ps = 0, po = 0;
         bool ok = true;
-        for (int r = 0; ok; ++r) {
-            const int w = work_index(r);
-            if (r * (int)gridDim.x >= n_work) break;
-            if (w >= n_work) continue;
-            Slot k;
-            int kvh;
-            {
-                const Work u = work_of(p, w, n_pairs, n_single, per_unit);
-                k = s ? u.s[1] : u.s[0];
-                kvh = u.kvh;
-            }
+        while (const Work *at = next_work(ok)) {
+            const Slot k = at->s[s];
+            const int kvh = at->kvh;
+            done_work();
             if (!k.nt) continue;
             const bool live = e < k.nt, warp_live = __any_sync(0xffffffffu, live);
             // keys that the row sees; a row that is not there masks nothing

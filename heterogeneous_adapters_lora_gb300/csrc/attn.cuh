@@ -20,11 +20,12 @@ constexpr int kBlock = 128;     // keys of a block
 
 // Ranges of keys: enough items for two per SM of a 152-SM device, none of
 // less than kMinBlocks blocks unless its tile has no more.
-constexpr int kTargetItems = 2 * 152;
+constexpr int kSms = 152;
+constexpr int kTargetItems = 2 * kSms;
 constexpr int kMinBlocks = 4;
 
-// One item of a plan (8 words).  The kPairs items of two row tiles come first,
-// then the kSingles items of one, each kind longest first.
+// One item of a plan (8 words).  The items of two row tiles come first, then
+// those of one, each kind longest first.
 struct Item {
     int tok0, n_tok;  // its query tokens
     int prob;         // sequence b, or -1 - g for the prefix of group g
@@ -36,14 +37,24 @@ struct Item {
 static_assert(sizeof(Item) == 32, "plan items are 8 words");
 
 // counters[] of a plan
-enum { kPairs = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kSingles = 4 };
+enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4 };
+
+// A unit is what a CTA works on at a time, for one key/value head: an item of
+// two row tiles, or one or two items of one tile.  units[] holds
+// (its first item << 2) | kind, the longest first.
+enum { kOne = 0, kTwo = 1, kPair = 2 };
+// Time of a block of keys, relative to each other: of a kPair unit (bound by
+// the products and the softmax) and of one stream of the others (by HBM).
+constexpr int kPairBlock = 10, kStreamBlock = 11;
 
 // tokens of an item's first or second row tile, and of an item
 __host__ __device__ inline int tile_tokens(int group) { return kTileRows / group; }
 
 struct Args {
     const Item *items;
+    const int32_t *units;
     const int32_t *counters;
+    int32_t *tickets;  // [0] units taken beyond each CTA's first, [1] CTAs done; zero between calls
     int32_t *status;
     int hq, hkv, G, D, page, causal, T;
     float scale_log2;  // scale * log2(e)

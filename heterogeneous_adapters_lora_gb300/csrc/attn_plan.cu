@@ -18,7 +18,7 @@ struct PlanArgs {
     int tpi;      // tokens of an item
     int hkv, causal;
     Item *items;
-    int32_t *tiles, *token_tiles, *first_tile, *counters;
+    int32_t *units, *tiles, *token_tiles, *first_tile, *counters;
     int max_tokens;
 };
 
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     if (bad) {
         if (tid == 0) {
-            p.counters[attn::kPairs] = p.counters[attn::kSingles] = 0;
+            p.counters[attn::kItems] = p.counters[attn::kUnits] = 0;
             p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = 0;
             p.counters[attn::kStatus] = LORA_ERR_DEVICE_INDEX;
         }
@@ -198,16 +198,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     __syncthreads();
     // where each length starts, the longest first
+    int pairs, singles;
     {
-        int pairs, singles;
         const int b = kBuckets - 1 - tid;
         const int at0 = block_scan(hist[0][b], &pairs), at1 = block_scan(hist[1][b], &singles);
         hist[0][b] = at0;
         hist[1][b] = pairs + at1;
-        if (tid == 0) {
-            p.counters[attn::kPairs] = pairs;
-            p.counters[attn::kSingles] = singles;
-        }
     }
     __syncthreads();
     for (int t = tid; t < n_tiles; t += kPlanThreads) {
@@ -231,7 +227,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             dst[1] = make_int4(it.blk1, it.kv_len, it.lim0, it.part);
         }
     }
+    __syncthreads();
+    // units: one-tile items go two to a CTA when there are more of them than
+    // CTAs; all units by the time they take, the longest first
+    const int per = (long long)singles * p.hkv > attn::kSms ? 2 : 1;
+    const int n_units = pairs + (singles + per - 1) / per;
+    const long long top = 2LL * attn::kStreamBlock * range;
+    for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = 0;
+    __syncthreads();
+    auto unit = [&](int u, int *word) {
+        const int at = u < pairs ? u : pairs + (u - pairs) * per;
+        const bool two = u >= pairs && per == 2 && at + 1 < pairs + singles;
+        *word = (at << 2) | (u < pairs ? attn::kPair : two ? attn::kTwo : attn::kOne);
+        const long long time = u < pairs ? (long long)attn::kPairBlock * (p.items[at].blk1 - p.items[at].blk0)
+                                         : (long long)attn::kStreamBlock *
+                                               (p.items[at].blk1 - p.items[at].blk0 +
+                                                (two ? p.items[at + 1].blk1 - p.items[at + 1].blk0 : 0));
+        return (int)min((long long)kBuckets - 1, time * (kBuckets - 1) / top);
+    };
+    int word;
+    for (int u = tid; u < n_units; u += kPlanThreads) atomicAdd(&hist[0][unit(u, &word)], 1);
+    __syncthreads();
+    {
+        int sum;
+        const int b = kBuckets - 1 - tid;
+        const int at = block_scan(hist[0][b], &sum);
+        hist[0][b] = at;
+    }
+    __syncthreads();
+    for (int u = tid; u < n_units; u += kPlanThreads) {
+        const int b = unit(u, &word);
+        p.units[atomicAdd(&hist[0][b], 1)] = word;
+    }
     if (tid == 0) {
+        p.counters[attn::kItems] = pairs + singles;
+        p.counters[attn::kUnits] = n_units;
         p.counters[attn::kPartTokens] = n_part;
         p.counters[attn::kTiles] = n_tiles;
         p.counters[attn::kStatus] = LORA_OK;
@@ -337,7 +367,7 @@ Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
-    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.tiles * 16) + align16((size_t)tokens * 8) +
+    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.items * 4) + align16((size_t)c.tiles * 16) + align16((size_t)tokens * 8) +
            align16((size_t)(seqs + groups) * 4) + 32;
 }
 
@@ -396,7 +426,9 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     attn::Args a;
     memset(&a, 0, sizeof(a));
     a.items = (const Item *)plan->items;
+    a.units = plan->units;
     a.counters = plan->counters;
+    a.tickets = (int32_t *)workspace;
     a.status = plan->counters + attn::kStatus;
     a.hq = d.n_q_heads;
     a.hkv = d.n_kv_heads;
@@ -479,6 +511,8 @@ extern "C" lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_
     at += 32;
     plan->items = (int32_t *)at;
     at += align16((size_t)c.items * sizeof(Item));
+    plan->units = (int32_t *)at;
+    at += align16((size_t)c.items * 4);
     plan->tiles = (int32_t *)at;
     at += align16((size_t)c.tiles * 16);
     plan->token_tiles = (int32_t *)at;
@@ -515,6 +549,7 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
     p.hkv = plan->desc.n_kv_heads;
     p.causal = plan->desc.causal;
     p.items = (Item *)plan->items;
+    p.units = plan->units;
     p.tiles = plan->tiles;
     p.token_tiles = plan->token_tiles;
     p.first_tile = plan->first_tile;

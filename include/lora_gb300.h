@@ -488,17 +488,18 @@ typedef struct {
  * same.  Caller-owned device memory, bound with lora_attn_plan_bind.
  *   items[max_items][8]  tiles of queries x ranges of keys: those of two row tiles,
  *                        then those of one, each the longest first
+ *   units[max_items]     items that a CTA works on together, the longest first
  *   tiles[max_tiles][4]  tiles of queries and where their partial results lie
  *   token_tiles[2][max_tokens]  each token's own tile and prefix tile (-1: none
  *                        that has to be joined)
- *   counters[8]          items of two row tiles, partial token rows, tiles, status
- *                        word, items of one row tile
+ *   counters[8]          items, partial token rows, tiles, status word, units
  * The host fields n_seqs .. max_prefix_len record the last build. */
 typedef struct {
     lora_attn_desc_t desc;
     int32_t max_tokens, max_seqs, max_groups, max_items, max_tiles, max_part;
     int32_t n_seqs, total_q, n_groups, max_kv_len, max_prefix_len;
     int32_t *items;
+    int32_t *units;
     int32_t *tiles;
     int32_t *token_tiles;
     int32_t *first_tile;
