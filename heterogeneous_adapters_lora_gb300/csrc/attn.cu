@@ -45,6 +45,7 @@ struct KArgs {
     int box_rows;  // rows of a K/V box: a whole block, or what pages divide it into
     int tpt;       // tokens of a slot's tile
     int q_bytes;   // bytes of a Q tile's copies
+    int out32;     // output rows of a head begin on 32-byte boundaries, in pieces of 32
 };
 
 // A slot's part of a unit.
@@ -173,6 +174,11 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
     f32x2 d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+__device__ __forceinline__ void st_global32(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -671,37 +677,49 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 tc::tc_fence_after();
             }
             if (warp_live) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint32_t o[Sh::kDP / 32][32];
+#pragma unroll
+                for (int c = 0; c < Sh::kDP / 32; ++c) tc::tmem_ld32(to + c * 32, o[c]);
+                const bool some = k.nb && l != 0.f;  // a row that saw no key gets zeros
+                const float inv = some ? 1.f / l : 0.f;
                 const int t = k.tok0 + e, h = kvh * p.a.G + g;
-                const long long prow = (long long)(k.part + e) * p.a.hq + h;
+                const int rows = k.nt * p.a.G;
+                const long long prow = (long long)k.part * p.a.hq + (long long)kvh * rows;
                 uint16_t *out = p.a.out + (long long)t * p.a.ldo + (long long)h * p.a.D;
-                float *part = p.a.part_o + prow * p.a.D;
-#pragma unroll 1
+                float *part = p.a.part_o + prow * p.a.D + 4 * row;
+                tc::tmem_wait_ld();
+#pragma unroll
                 for (int c = 0; c < Sh::kDP / 32; ++c) {
-                    uint32_t o[32];
-                    if (k.nb) {
-                        tc::tmem_ld32(to + c * 32, o);
-                        tc::tmem_wait_ld();
-                    }
+                    if (!live || c * 32 >= p.a.D) continue;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = k.nb && l != 0.f ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
-                    if (!live) continue;
+                    for (int i = 0; i < 32; ++i) o[c][i] = some ? __float_as_uint(__uint_as_float(o[c][i]) * inv) : 0u;
+                    if (k.part >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int col = c * 32 + i * 8;
-                        if (col >= p.a.D) break;
-                        const float *f = (const float *)&o[i * 8];
-                        if (k.part < 0) {
-                            *(uint4 *)(out + col) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]),
-                                                               pack2(f[6], f[7]));
-                        } else {
-                            *(float4 *)(part + col) = make_float4(f[0], f[1], f[2], f[3]);
-                            *(float4 *)(part + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                        for (int i = 0; i < 8; ++i) {
+                            if (c * 32 + 4 * i < p.a.D)
+                                *(uint4 *)part = make_uint4(o[c][4 * i], o[c][4 * i + 1], o[c][4 * i + 2], o[c][4 * i + 3]);
+                            part += 4 * rows;
+                        }
+                    } else {
+                        uint32_t b[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            b[i] = pack2(__uint_as_float(o[c][2 * i]), __uint_as_float(o[c][2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            if (p.out32 && c * 32 + i * 8 < p.a.D) {  // whole 32-byte sectors
+                                st_global32(out + c * 32 + i * 8, &b[i * 4]);
+                            } else {
+                                if (c * 32 + i * 8 < p.a.D)
+                                    *(uint4 *)(out + c * 32 + i * 8) = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+                                if (c * 32 + i * 8 + 8 < p.a.D)
+                                    *(uint4 *)(out + c * 32 + i * 8 + 8) =
+                                        make_uint4(b[4 * i + 4], b[4 * i + 5], b[4 * i + 6], b[4 * i + 7]);
+                            }
                         }
                     }
                 }
-                if (live && k.part >= 0) p.a.part_lse[prow] = l == 0.f ? -INFINITY : m * scale + log2f(l);
+                if (live && k.part >= 0) p.a.part_lse[prow + row] = l == 0.f ? -INFINITY : m * scale + log2f(l);
                 tc::tc_fence_before();
             }
         }
@@ -753,6 +771,7 @@ lora_status_t lora_attn_launch(const attn::Args &a, int max_items, cudaStream_t 
         while (a.page % p.box_rows) p.box_rows >>= 1;
     const int nch = a.D > 64 ? 2 : 1;
     p.q_bytes = nch * 128 * a.G * p.tpt;
+    p.out32 = a.D % 16 == 0 && a.ldo % 16 == 0 && ((uintptr_t)a.out & 31) == 0;
     const long long rows = a.n_rows > 0 ? a.n_rows : 1;
     if (!lora_make_tmap_heads(&p.tq, a.q, a.D, a.hq, a.T, a.ldq, a.G, p.tpt) ||
         !lora_make_tmap_heads(&p.tk, a.k, a.D, a.hkv, rows, a.ldk, 1, p.box_rows) ||

@@ -18,10 +18,12 @@ namespace attn {
 constexpr int kTileRows = 128;  // rows of one MMA tile; an item has up to two
 constexpr int kBlock = 128;     // keys of a block
 
-// Ranges of keys: enough items for two per SM of a 152-SM device, none of
-// less than kMinBlocks blocks unless its tile has no more.
+// Ranges of keys: a batch is cut into about this many of one length (times
+// key/value heads), if its tiles are that long; tiles of one row tile into
+// shorter ones, whose partial results are small.  None has less than
+// kMinBlocks blocks unless its tile has no more.
 constexpr int kSms = 152;
-constexpr int kTargetItems = 2 * kSms;
+constexpr int kPairRanges = kSms, kOneRanges = 2 * kSms;
 constexpr int kMinBlocks = 4;
 
 // One item of a plan (8 words).  The items of two row tiles come first, then
@@ -37,7 +39,7 @@ struct Item {
 static_assert(sizeof(Item) == 32, "plan items are 8 words");
 
 // counters[] of a plan
-enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4 };
+enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4, kJoins = 5 };
 
 // A unit is what a CTA works on at a time, for one key/value head: an item of
 // two row tiles, or one or two items of one tile.  units[] holds
@@ -63,8 +65,11 @@ struct Args {
     const int32_t *table, *ptable;
     long long ld_table, ld_ptable;
     uint16_t *out;
-    float *part_o;     // [token row][hq][D]
-    float *part_lse;   // [token row][hq]
+    // Partial results: a slot of nt tokens has, per key/value head, nt * G rows from
+    // row part * hq + head * nt * G on; its outputs lie as [D / 4][rows][4], so that
+    // the warps, with a row per lane, store them in one piece.
+    float *part_o;
+    float *part_lse;
 };
 
 }  // namespace attn

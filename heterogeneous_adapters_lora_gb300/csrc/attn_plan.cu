@@ -18,7 +18,7 @@ struct PlanArgs {
     int tpi;      // tokens of an item
     int hkv, causal;
     Item *items;
-    int32_t *units, *tiles, *token_tiles, *first_tile, *counters;
+    int32_t *units, *tiles, *token_tiles, *joins, *first_tile, *counters;
     int max_tokens;
 };
 
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (bad) {
         if (tid == 0) {
             p.counters[attn::kItems] = p.counters[attn::kUnits] = 0;
-            p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = 0;
+            p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = p.counters[attn::kJoins] = 0;
             p.counters[attn::kStatus] = LORA_ERR_DEVICE_INDEX;
         }
         return;
@@ -150,9 +150,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if ((tid & 31) == 0 && mine) atomicAdd(&total_blocks, mine);
     __syncthreads();
-    const unsigned long long want =
-        (total_blocks * (unsigned long long)p.hkv + attn::kTargetItems - 1) / attn::kTargetItems;
-    const int range = (int)max((unsigned long long)attn::kMinBlocks, want);
+    const unsigned long long blocks_all = total_blocks * (unsigned long long)p.hkv;
+    const int range_pair = (int)max((unsigned long long)attn::kMinBlocks, (blocks_all + attn::kPairRanges - 1) / attn::kPairRanges);
+    const int range_one = (int)max((unsigned long long)attn::kMinBlocks, (blocks_all + attn::kOneRanges - 1) / attn::kOneRanges);
     // items and partial rows of each tile; the histogram of item lengths
     int n_part = 0;
     for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 }
                 ahead = __ldg(p.prefix_len + lo) > 0;
             }
+            const int range = 2 * n_tok <= p.tpi ? range_one : range_pair;
             parts = (blocks + range - 1) / range;
             // no keys: zeros are written, unless a prefix has the tokens' result
             if (parts == 0 && !ahead) parts = 1;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     // CTAs; all units by the time they take, the longest first
     const int per = (long long)singles * p.hkv > attn::kSms ? 2 : 1;
     const int n_units = pairs + (singles + per - 1) / per;
-    const long long top = 2LL * attn::kStreamBlock * range;
+    const long long top = 2LL * attn::kStreamBlock * max(range_one, range_pair);
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = 0;
     __syncthreads();
     auto unit = [&](int u, int *word) {
@@ -259,7 +260,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int b = unit(u, &word);
         p.units[atomicAdd(&hist[0][b], 1)] = word;
     }
+    // the tokens with partial results
+    int n_joins = 0;
+    for (int t0 = 0; n_part && t0 < p.T; t0 += kPlanThreads) {
+        const int t = t0 + tid;
+        const int has = t < p.T && (p.token_tiles[t] >= 0 || p.token_tiles[p.max_tokens + t] >= 0);
+        int sum;
+        const int at = block_scan(has, &sum);
+        if (has) p.joins[n_joins + at] = t;
+        n_joins += sum;
+    }
     if (tid == 0) {
+        p.counters[attn::kJoins] = n_joins;
         p.counters[attn::kItems] = pairs + singles;
         p.counters[attn::kUnits] = n_units;
         p.counters[attn::kPartTokens] = n_part;
@@ -271,66 +283,113 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // ---------------------------------------------------------------- join
 
 struct JoinArgs {
-    const int32_t *tiles, *token_tiles, *counters;
-    int max_tokens, T, hq, D;
+    const int32_t *tiles, *token_tiles, *joins, *counters;
+    int max_tokens, T, hq, hkv, G, D, tpt;
     const float *part_o, *part_lse;
     uint16_t *out;
     long long ldo;
 };
 
 constexpr int kJoinThreads = 128;
+constexpr int kJoinCtas = 3 * attn::kSms;  // what the registers let be resident
+constexpr int kJoinAhead = 4;  // parts that it reads together
+constexpr int kJoinHeads = 4;  // query heads of a key/value head that a warp has in hand
 
 // out[t][h] = sum_s 2^lse_s o_s / sum_s 2^lse_s over the partial results of
 // the token's own tile and of its prefix tile, in that order (so the result
-// does not depend on which item ended first).  One warp per token and head;
-// a lane has four elements of the head.
+// does not depend on which item ended first).  A warp takes a token and
+// kJoinHeads heads of one key/value head: their rows are neighbours in a
+// partial result, so each line that a lane (four elements of a head) fetches
+// serves all of them.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs p) {
+    // The plan was complete before the item kernel began, which lets this one
+    // start: only the partial results are waited for.
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (__ldg(p.counters + attn::kPartTokens) == 0) return;
     const int lane = threadIdx.x & 31;
-    const long long n = (long long)p.T * p.hq;
+    const int per = (p.G + kJoinHeads - 1) / kJoinHeads * p.hkv;  // warps of a token
+    const long long n = (long long)__ldg(p.counters + attn::kJoins) * per;
     const long long step = (long long)gridDim.x * (kJoinThreads / 32);
+    bool waited = false;
     for (long long w = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); w < n; w += step) {
-        const int t = (int)(w / p.hq), h = (int)(w % p.hq);
-        const int tile[2] = {__ldg(p.token_tiles + t), __ldg(p.token_tiles + p.max_tokens + t)};
-        if (tile[0] < 0 && tile[1] < 0) continue;
-        float top = -INFINITY;
+        const int t = __ldg(p.joins + w / per), kvh = (int)(w % per) % p.hkv, g0 = (int)(w % per) / p.hkv * kJoinHeads;
+        // the token's parts, first its own tile's, then its prefix's: the row in the
+        // first of them, rows of a part, how far apart they are, and how many
+        long long first[2], apart[2];
+        int parts[2], rows[2], at[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (tile[k] < 0) continue;
-            const int4 e = __ldg((const int4 *)(p.tiles + 4 * (long long)tile[k]));
-            for (int s = lane; s < e.y; s += 32)
-                top = fmaxf(top, p.part_lse[(long long)(e.x + s * e.w + t - e.z) * p.hq + h]);
+            const int tile = __ldg(p.token_tiles + k * p.max_tokens + t);
+            parts[k] = rows[k] = at[k] = 0;
+            first[k] = apart[k] = 0;
+            if (tile < 0) continue;
+            const int4 e = __ldg((const int4 *)(p.tiles + 4 * (long long)tile));
+            const int i = t - e.z, slot = i / p.tpt;  // slots of tpt tokens, the last one of what is left
+            rows[k] = min(p.tpt, e.w - slot * p.tpt) * p.G;
+            at[k] = (i - slot * p.tpt) * p.G + g0;
+            first[k] = (long long)(e.x + slot * p.tpt) * p.hq + (long long)kvh * rows[k];
+            apart[k] = (long long)e.w * p.hq;
+            parts[k] = e.y;
         }
+        const int all = parts[0] + parts[1];
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+        const int heads = min(kJoinHeads, p.G - g0);
+        float top[kJoinHeads], sum[kJoinHeads], acc[kJoinHeads][4];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (top == -INFINITY) top = 0.f;
-        float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < kJoinHeads; ++u) {
+            top[u] = -INFINITY;
+            sum[u] = acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
+        }
+        // kJoinAhead parts at a time, their loads together; the sums so far are
+        // rescaled when a part's maximum is above theirs
+        for (int s0 = 0; s0 < all; s0 += kJoinAhead) {
+            float lse[kJoinAhead][kJoinHeads];
+            float4 v[kJoinAhead][kJoinHeads];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (tile[k] < 0) continue;
-            const int4 e = __ldg((const int4 *)(p.tiles + 4 * (long long)tile[k]));
-            for (int s = 0; s < e.y; ++s) {
-                const long long row = (long long)(e.x + s * e.w + t - e.z) * p.hq + h;
-                const float wgt = exp2f(p.part_lse[row] - top);
-                // a part without keys has a weight of zero; a NaN or infinite score makes its weight NaN
-                if (wgt == 0.f) continue;
-                sum += wgt;
-                if (4 * lane < p.D) {
-                    const float4 o = *(const float4 *)(p.part_o + row * p.D + 4 * lane);
-                    acc[0] += wgt * o.x; acc[1] += wgt * o.y; acc[2] += wgt * o.z; acc[3] += wgt * o.w;
+            for (int a = 0; a < kJoinAhead; ++a) {
+                const int s = s0 + a, k = s >= parts[0] ? 1 : 0;
+                const long long row = k ? first[1] + (s - parts[0]) * apart[1] : first[0] + s * apart[0];
+                const long long one = row + (k ? at[1] : at[0]);
+                const float *o = p.part_o + row * p.D + ((long long)lane * (k ? rows[1] : rows[0]) + (k ? at[1] : at[0])) * 4;
+#pragma unroll
+                for (int u = 0; u < kJoinHeads; ++u) {
+                    const bool is = s < all && u < heads;
+                    lse[a][u] = is ? p.part_lse[one + u] : -INFINITY;
+                    v[a][u] = is && 4 * lane < p.D ? *(const float4 *)(o + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinHeads; ++u) {
+                float m = top[u];
+#pragma unroll
+                for (int a = 0; a < kJoinAhead; ++a) m = fmaxf(m, lse[a][u]);
+                const float base = m == -INFINITY ? 0.f : m, old = exp2f(top[u] - base);
+                top[u] = m;
+                sum[u] *= old;
+                acc[u][0] *= old; acc[u][1] *= old; acc[u][2] *= old; acc[u][3] *= old;
+#pragma unroll
+                for (int a = 0; a < kJoinAhead; ++a) {
+                    // a part without keys weighs nothing; a NaN or infinite score makes its weight NaN
+                    const float x = exp2f(lse[a][u] - base);
+                    if (x == 0.f) continue;
+                    sum[u] += x;
+                    acc[u][0] += x * v[a][u].x; acc[u][1] += x * v[a][u].y;
+                    acc[u][2] += x * v[a][u].z; acc[u][3] += x * v[a][u].w;
                 }
             }
         }
-        const float r = sum == 0.f ? 0.f : 1.f / sum;
-        if (4 * lane < p.D) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[0] * r, acc[1] * r);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2] * r, acc[3] * r);
-            *(uint2 *)(p.out + (long long)t * p.ldo + (long long)h * p.D + 4 * lane) =
+#pragma unroll
+        for (int u = 0; u < kJoinHeads; ++u) {
+            if (u >= heads || 4 * lane >= p.D) continue;
+            const float r = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[u][0] * r, acc[u][1] * r);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[u][2] * r, acc[u][3] * r);
+            *(uint2 *)(p.out + (long long)t * p.ldo + (long long)(kvh * p.G + g0 + u) * p.D + 4 * lane) =
                 make_uint2(*(const uint32_t *)&x, *(const uint32_t *)&y);
         }
     }
+    // a kernel after this one must not start on what the item kernel still writes
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- host
@@ -344,19 +403,21 @@ bool desc_ok(const lora_attn_desc_t &d) {
     return isfinite(d.scale) && d.scale > 0.f && isfinite(d.scale * 1.44269504f);
 }
 
+constexpr int kMostRanges = attn::kOneRanges > attn::kPairRanges ? attn::kOneRanges : attn::kPairRanges;
+
 struct Caps {
     long long tpi, items, tiles, part;
 };
 
 // What a batch of the given size can need.  A tile's ranges beyond its first
-// number at most kTargetItems / n_kv_heads over all tiles (the length of a
-// range is at least all blocks * n_kv_heads / kTargetItems).  A tile of two or
+// number at most kMostRanges / n_kv_heads over all tiles (the length of a
+// range is at least all blocks * n_kv_heads / kMostRanges).  A tile of two or
 // more ranges has at most twice that many; with prefixes every token also has
 // one partial result of its own keys and one of its prefix.
 Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long groups) {
     Caps c;
     c.tpi = 2 * attn::tile_tokens(d.n_q_heads / d.n_kv_heads);
-    const long long extra = attn::kTargetItems / d.n_kv_heads;
+    const long long extra = kMostRanges / d.n_kv_heads;
     c.tiles = (tokens / c.tpi + seqs) + (groups ? tokens / c.tpi + groups : 0);
     c.items = c.tiles + extra;
     const long long most = c.tpi < tokens ? c.tpi : tokens;
@@ -367,7 +428,7 @@ Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
-    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.items * 4) + align16((size_t)c.tiles * 16) + align16((size_t)tokens * 8) +
+    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.items * 4) + align16((size_t)c.tiles * 16) + align16((size_t)tokens * 8) + align16((size_t)tokens * 4) +
            align16((size_t)(seqs + groups) * 4) + 32;
 }
 
@@ -463,18 +524,22 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     memset(&j, 0, sizeof(j));
     j.tiles = plan->tiles;
     j.token_tiles = plan->token_tiles;
+    j.joins = plan->joins;
     j.counters = plan->counters;
     j.max_tokens = plan->max_tokens;
     j.T = plan->total_q;
     j.hq = d.n_q_heads;
+    j.hkv = d.n_kv_heads;
+    j.G = a.G;
     j.D = d.head_dim;
+    j.tpt = attn::tile_tokens(a.G);
     j.part_o = a.part_o;
     j.part_lse = a.part_lse;
     j.out = a.out;
     j.ldo = ldo;
-    const long long warps = (long long)plan->total_q * d.n_q_heads;
+    const long long warps = (long long)plan->total_q * ((a.G + kJoinHeads - 1) / kJoinHeads * d.n_kv_heads);
     long long grid = (warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-    if (grid > 16 * 152) grid = 16 * 152;
+    if (grid > kJoinCtas) grid = kJoinCtas;
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = config((int)grid, kJoinThreads, s, at);
     LORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, join_kernel, j));
@@ -517,6 +582,8 @@ extern "C" lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_
     at += align16((size_t)c.tiles * 16);
     plan->token_tiles = (int32_t *)at;
     at += align16((size_t)max_tokens * 8);
+    plan->joins = (int32_t *)at;
+    at += align16((size_t)max_tokens * 4);
     plan->first_tile = (int32_t *)at;
     return LORA_OK;
 }
@@ -552,6 +619,7 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
     p.units = plan->units;
     p.tiles = plan->tiles;
     p.token_tiles = plan->token_tiles;
+    p.joins = plan->joins;
     p.first_tile = plan->first_tile;
     p.counters = plan->counters;
     p.max_tokens = plan->max_tokens;

@@ -492,7 +492,8 @@ typedef struct {
  *   tiles[max_tiles][4]  tiles of queries and where their partial results lie
  *   token_tiles[2][max_tokens]  each token's own tile and prefix tile (-1: none
  *                        that has to be joined)
- *   counters[8]          items, partial token rows, tiles, status word, units
+ *   joins[max_tokens]    the tokens that have partial results
+ *   counters[8]          items, partial token rows, tiles, status word, units, joins
  * The host fields n_seqs .. max_prefix_len record the last build. */
 typedef struct {
     lora_attn_desc_t desc;
@@ -502,6 +503,7 @@ typedef struct {
     int32_t *units;
     int32_t *tiles;
     int32_t *token_tiles;
+    int32_t *joins;
     int32_t *first_tile;
     int32_t *counters;
 } lora_attn_plan_t;
