@@ -733,9 +733,14 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
 std::atomic<int> g_attn_sms[64];  // SM count per device, looked up once
 
 template <int NCH>
-cudaError_t launch(KArgs &p, int grid, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(item_kernel<NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NCH>::kSmem);
-    if (e != cudaSuccess) return e;
+cudaError_t launch(KArgs &p, int dev, int grid, cudaStream_t s) {
+    static std::atomic<bool> ready[64];  // the shared-memory limit is set once per device
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(item_kernel<NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<NCH>::kSmem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cudaLaunchAttribute at[1];
@@ -779,7 +784,7 @@ lora_status_t lora_attn_launch(const attn::Args &a, int max_items, cudaStream_t 
         return LORA_ERR_UNSUPPORTED;
     const long long n = (long long)max_items * a.hkv;
     const int grid = (int)(n < n_sms ? n : n_sms);
-    LORA_CUDA_TRY(nch == 2 ? launch<2>(p, grid, s) : launch<1>(p, grid, s));
+    LORA_CUDA_TRY(nch == 2 ? launch<2>(p, dev, grid, s) : launch<1>(p, dev, grid, s));
     lora_note_launch();
     return LORA_OK;
 }

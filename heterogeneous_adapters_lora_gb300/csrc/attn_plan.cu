@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     int n_part = 0;
     for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
         const int t = t0 + tid;
-        int parts = 0, rows = 0, sum, blocks = 0, n_tok = 0, tok0 = 0, i = 0;
+        int parts = 0, rows = 0, sum, blocks = 0, range = 1, n_tok = 0, tok0 = 0, i = 0;
         bool joined = false;
         if (t < n_tiles) {
             i = find_problem(p.first_tile, n, t);
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 }
                 ahead = __ldg(p.prefix_len + lo) > 0;
             }
-            const int range = 2 * n_tok <= p.tpi ? range_one : range_pair;
+            range = 2 * n_tok <= p.tpi ? range_one : range_pair;
             parts = (blocks + range - 1) / range;
             // no keys: zeros are written, unless a prefix has the tokens' result
             if (parts == 0 && !ahead) parts = 1;
@@ -191,8 +191,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 int32_t *map = p.token_tiles + (i < p.n_groups ? p.max_tokens : 0);
                 for (int e = 0; e < n_tok; ++e) map[tok0 + e] = t;
             }
+            // whole ranges and what is left: the short ones even the CTAs out
             for (int s = 0; s < parts; ++s) {
-                const int len = (int)((long long)(s + 1) * blocks / parts) - (int)((long long)s * blocks / parts);
+                const int len = min(blocks - s * range, range);
                 atomicAdd(&hist[2 * n_tok <= p.tpi][min(len, kBuckets - 1)], 1);
             }
         }
@@ -212,10 +213,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int i = find_problem(p.first_tile, n, t);
         const Problem q = problem(p, i);
         const int j = t - p.first_tile[i], blocks = tile_blocks(q, j, p.tpi);
+        const int range = 2 * e.w <= p.tpi ? range_one : range_pair;
         for (int s = 0; s < e.y; ++s) {
             Item it;
-            it.blk0 = (int)((long long)s * blocks / e.y);
-            it.blk1 = (int)((long long)(s + 1) * blocks / e.y);
+            it.blk0 = s * range;
+            it.blk1 = min(blocks, (s + 1) * range);
             it.tok0 = e.z;
             it.n_tok = e.w;
             it.prob = i < p.n_groups ? -1 - i : i - p.n_groups;

@@ -139,6 +139,8 @@ EXPORTS = {
 def lib():
     """Load liblora_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -165,17 +167,31 @@ def ptr(obj):
         return None
     if isinstance(obj, int):
         return obj
-    if hasattr(obj, "data_ptr"):
-        return obj.data_ptr()
+    data_ptr = getattr(obj, "data_ptr", None)
+    if data_ptr is not None:
+        return data_ptr()
     if hasattr(obj, "ctypes"):
         return obj.ctypes.data
     raise TypeError(type(obj))
 
 
+def _current_stream():
+    """Handle of PyTorch's current stream (its raw accessor where it has one: a Stream object costs microseconds)."""
+    global _current_stream
+    import torch
+
+    def by_object():
+        return torch.cuda.current_stream().cuda_stream
+
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    handle = by_object()  # also brings CUDA up
+    _current_stream = by_object if raw is None or device is None else lambda: raw(device())
+    return handle
+
+
 def stream_ptr(stream=None):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
