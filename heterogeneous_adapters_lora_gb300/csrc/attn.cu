@@ -86,22 +86,41 @@ struct Shape {
 
 // Bounded wait; false when it gave up here or somewhere else in the CTA.
 // The lanes of a warp may differ: callers vote before they leave a loop.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status) {
+#pragma unroll 1
     for (int polls = 0; !tc::mbar_try_wait(bar, parity); ++polls) {
-        if ((polls & 1023) == 0 && *(volatile int *)&b->abort) return false;
+        if ((polls & 1023) == 0 && *abort) return false;
         if (polls > kMaxPolls) {
-            *(volatile int *)&b->abort = 1;
+            *abort = 1;
             atomicExch(status, (int)LORA_ERR_TIMEOUT);
             return false;
         }
     }
     return true;
 }
+// The warps with few registers call it; the softmax warps, whose registers
+// leave a call no room, have it inline.
+__device__ __noinline__ bool wait_call(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status) {
+    return wait_on(bar, parity, abort, status);
+}
+template <bool kCall>
+__device__ __forceinline__ bool wait_as(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status) {
+    const uint32_t at = tc::smem_u32(bar);
+    if (tc::mbar_try_wait(at, parity)) return true;
+    return kCall ? wait_call(at, parity, &b->abort, status) : wait_on(at, parity, &b->abort, status);
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status) {
+    return wait_as<true>(bar, parity, b, status);
+}
+template <bool kCall>
+struct Call {
+    static constexpr bool value = kCall;
+};
 __device__ __forceinline__ bool all(bool ok) { return __all_sync(0xffffffffu, ok); }
 // ... of a whole warp, with the vote.
+template <bool kCall>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *b, int32_t *status) {
-    return all(wait(bar, parity, b, status));
+    return all(wait_as<kCall>(bar, parity, b, status));
 }
 
 __device__ __forceinline__ Slot slot_of(const KArgs &p, int item) {
@@ -274,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
     // The units of this CTA, as warp 8 takes them; every other warp waits for
     // the next, reads it in place and gives it back.
     int round = 0;
-    auto next_work = [&](bool &ok) -> const Work * {
-        ok = ok && warp_wait(&bars->work_full[round % kWorks], (uint32_t)((round / kWorks) & 1), bars, status);
+    auto next_work = [&](bool &ok, auto call) -> const Work * {
+        ok = ok && warp_wait<decltype(call)::value>(&bars->work_full[round % kWorks], (uint32_t)((round / kWorks) & 1), bars, status);
         const Work *k = &bars->work[round % kWorks];
         return ok && k->n >= 0 ? k : nullptr;
     };
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 Work k;
                 if (w < n_work) k = work_of(p, w);
                 if (round >= kWorks)
-                    ok = warp_wait(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
+                    ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
                 if (lane == 0) {
                     if (w < n_work) bars->work[round % kWorks] = k; else bars->work[round % kWorks].n = -1;
                     tc::mbar_arrive(&bars->work_full[round % kWorks]);
@@ -347,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                         row[c] = box_row(k.s[c], 0);
                         load(&p.tk, k.kvh, row[c]);
                     }
+#pragma unroll 1
                 for (int j = 0; j < k.n && ok; ++j)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
@@ -364,21 +384,23 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 p.a.tickets[1] = 0;
             }
             // every copy has landed before the CTA ends
+#pragma unroll 1
             for (int s = 0; s < kNS && s < fill; ++s) {
                 const int last = fill - 1 - ((fill - 1 - s) % kNS);
                 int polls = 0;
+#pragma unroll 1
                 while (!tc::mbar_try_wait(&bars->kv_full[s], (uint32_t)((last / kNS) & 1)) && ++polls < (1 << 16)) {}
             }
         } else if (warp == 10) {
             // ---- Q tiles
             int fill[2] = {0, 0};
             bool ok = true;
-            while (const Work *at = next_work(ok)) {
+            while (const Work *at = next_work(ok, Call<true>())) {
                 const Work &k = *at;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!k.s[s].nb || !ok) continue;
-                    if (fill[s] && !warp_wait(&bars->q_empty[s], (uint32_t)((fill[s] - 1) & 1), bars, status)) {
+                    if (fill[s] && !warp_wait<true>(&bars->q_empty[s], (uint32_t)((fill[s] - 1) & 1), bars, status)) {
                         ok = false;
                         continue;
                     }
@@ -397,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 int polls = 0;
+#pragma unroll 1
                 while (fill[s] && !tc::mbar_try_wait(&bars->q_full[s], (uint32_t)((fill[s] - 1) & 1)) &&
                        ++polls < (1 << 16)) {}
             }
@@ -439,13 +462,14 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             // Fills of the other slot's stream.  Both warps see every phase of every stage
             // (a parity wait is exact only within one phase), so both give every stage back.
             auto pass = [&](int n) {
+#pragma unroll 1
                 for (; n; --n) {
                     ok &= wait(&bars->kv_full[st], par, bars, status);
                     if (elect_one()) tc::mbar_arrive(&bars->kv_empty[st]);
                     step();
                 }
             };
-            while (const Work *k = next_work(ok)) {
+            while (const Work *k = next_work(ok, Call<true>())) {
                 const Slot &me = k->s[s];
                 const int nb = me.nb, other = k->s[1 - s].nb, most = k->n;
                 const bool alone = !k->shared;
@@ -468,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 }
                 if (alone && !s && other) pass(1);
                 const int full = (me.kv_len >> 7) - me.blk0;  // blocks whose keys all count
+#pragma unroll 1
                 for (int j = 0; j < most; ++j) {
                     // fills of the other stream that come between
                     const int between = alone && j < other ? (j + 1 < other ? 2 : 1) : 0;
@@ -499,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                             const int left = me.kv_len - (me.blk0 + j) * attn::kBlock;
                             const int end = (left + p.box_rows - 1) / p.box_rows * p.box_rows * 8;
                             char *v = ring + sv * Sh::kStage;
+#pragma unroll 1
                             for (int i = left * 8 + lane; i < end; i += 32)
 #pragma unroll
                                 for (int c = 0; c < NCH; ++c)
@@ -543,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             if (lane == 0) tc::mma_commit(&bars->fin[s]);
             __syncwarp();
             int polls = 0;
+#pragma unroll 1
             while (!tc::mbar_try_wait(&bars->fin[s], 0) && ++polls < (1 << 20)) {}
         }
     } else {
@@ -555,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
         const float scale = p.a.scale_log2;
         uint32_t ps = 0, po = 0;
         bool ok = true;
-        while (const Work *at = next_work(ok)) {
+        while (const Work *at = next_work(ok, Call<false>())) {
             const Slot k = at->s[s];
             const int kvh = at->kvh;
             done_work();
@@ -566,8 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             const int min_lim = __reduce_min_sync(0xffffffffu, lim);
             float m = -INFINITY, l = 0.f, base = 0.f;
             bool huge = false;
+#pragma unroll 1
             for (int j = 0; j < k.nb; ++j) {
-                if (!(ok = warp_wait(&bars->s_full[s], ps, bars, status))) break;
+                if (!(ok = warp_wait<false>(&bars->s_full[s], ps, bars, status))) break;
                 ps ^= 1u;
                 if (warp_live) {
                     tc::tc_fence_after();
@@ -672,51 +700,45 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             }
             if (!ok) break;
             if (k.nb) {
-                if (!(ok = warp_wait(&bars->o_full[s], po, bars, status))) break;
+                if (!(ok = warp_wait<false>(&bars->o_full[s], po, bars, status))) break;
                 po ^= 1u;
                 tc::tc_fence_after();
             }
             if (warp_live) {
-                uint32_t o[Sh::kDP / 32][32];
-#pragma unroll
-                for (int c = 0; c < Sh::kDP / 32; ++c) tc::tmem_ld32(to + c * 32, o[c]);
                 const bool some = k.nb && l != 0.f;  // a row that saw no key gets zeros
                 const float inv = some ? 1.f / l : 0.f;
-                const int t = k.tok0 + e, h = kvh * p.a.G + g;
                 const int rows = k.nt * p.a.G;
                 const long long prow = (long long)k.part * p.a.hq + (long long)kvh * rows;
-                uint16_t *out = p.a.out + (long long)t * p.a.ldo + (long long)h * p.a.D;
+                uint16_t *out = p.a.out + (long long)(k.tok0 + e) * p.a.ldo + (long long)(kvh * p.a.G + g) * p.a.D;
                 float *part = p.a.part_o + prow * p.a.D + 4 * row;
-                tc::tmem_wait_ld();
+                // a loop, though of few rounds: code that a unit runs once comes from beyond
+                // the instruction cache, and unrolled this took longer than its work
+#pragma unroll 1
+                for (int c = 0; c < p.a.D; c += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(to + c, o);
+                    tc::tmem_wait_ld();
+                    if (!live) continue;
 #pragma unroll
-                for (int c = 0; c < Sh::kDP / 32; ++c) {
-                    if (!live || c * 32 >= p.a.D) continue;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[c][i] = some ? __float_as_uint(__uint_as_float(o[c][i]) * inv) : 0u;
+                    for (int i = 0; i < 32; ++i) o[i] = some ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
                     if (k.part >= 0) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            if (c * 32 + 4 * i < p.a.D)
-                                *(uint4 *)part = make_uint4(o[c][4 * i], o[c][4 * i + 1], o[c][4 * i + 2], o[c][4 * i + 3]);
+                            if (c + 4 * i < p.a.D) *(uint4 *)part = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                             part += 4 * rows;
                         }
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                    if (p.out32) {  // whole 32-byte sectors
+                        st_global32(out + c, o);
+                        if (c + 16 < p.a.D) st_global32(out + c + 16, o + 8);
                     } else {
-                        uint32_t b[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            b[i] = pack2(__uint_as_float(o[c][2 * i]), __uint_as_float(o[c][2 * i + 1]));
-#pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            if (p.out32 && c * 32 + i * 8 < p.a.D) {  // whole 32-byte sectors
-                                st_global32(out + c * 32 + i * 8, &b[i * 4]);
-                            } else {
-                                if (c * 32 + i * 8 < p.a.D)
-                                    *(uint4 *)(out + c * 32 + i * 8) = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
-                                if (c * 32 + i * 8 + 8 < p.a.D)
-                                    *(uint4 *)(out + c * 32 + i * 8 + 8) =
-                                        make_uint4(b[4 * i + 4], b[4 * i + 5], b[4 * i + 6], b[4 * i + 7]);
-                            }
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            if (c + 8 * i < p.a.D)
+                                *(uint4 *)(out + c + 8 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
                 if (live && k.part >= 0) p.a.part_lse[prow + row] = l == 0.f ? -INFINITY : m * scale + log2f(l);
