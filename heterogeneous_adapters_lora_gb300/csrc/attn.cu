@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kChunkBytes = attn::kBlock * 128;  // 128 rows of 64 bf16
+constexpr int kBrief = 4;                        // blocks of a short unit
 constexpr int kMaxPolls = 1 << 25;               // of a wait (seconds)
 constexpr float kLag = 8.f;                      // the maximum in use may lag by 2^8
 constexpr float kExactBase = 1048576.f;          // up to here the rounding of the maximum is small against 1
@@ -42,6 +43,7 @@ constexpr float kExactBase = 1048576.f;          // up to here the rounding of t
 struct KArgs {
     attn::Args a;
     CUtensorMap tq, tk, tv;
+    int page_shift;  // log2 of the boxes of a page, -1 if they are no power of two
     int box_rows;  // rows of a K/V box: a whole block, or what pages divide it into
     int tpt;       // tokens of a slot's tile
     int q_bytes;   // bytes of a Q tile's copies
@@ -123,12 +125,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *
     return all(wait_as<kCall>(bar, parity, b, status));
 }
 
-__device__ __forceinline__ Slot slot_of(const KArgs &p, int item) {
+// An item as the plan holds it.
+struct Raw {
+    int4 x, y;
+};
+__device__ __forceinline__ Raw raw_of(const KArgs &p, int item) {
     const int4 *at = (const int4 *)(p.a.items + item);
-    const int4 x = __ldg(at), y = __ldg(at + 1);
+    return {__ldg(at), __ldg(at + 1)};
+}
+__device__ __forceinline__ Slot slot_of(const KArgs &p, const Raw &r) {
     Slot k;
-    k.tok0 = x.x; k.nt = x.y; k.prob = x.z; k.blk0 = x.w;
-    k.nb = y.x - x.w; k.kv_len = y.y; k.lim0 = y.z; k.part = y.w;
+    k.tok0 = r.x.x; k.nt = r.x.y; k.prob = r.x.z; k.blk0 = r.x.w;
+    k.nb = r.y.x - r.x.w; k.kv_len = r.y.y; k.lim0 = r.y.z; k.part = r.y.w;
     k.step = k.prob >= 0 && p.a.causal ? 1 : 0;
     return k;
 }
@@ -138,13 +146,12 @@ __device__ __forceinline__ void clip(Slot &k) {
     const int end = lim <= 0 ? 0 : (lim - 1) / attn::kBlock + 1;
     k.nb = k.nt ? max(0, min(k.nb, end - k.blk0)) : 0;
 }
-__device__ __forceinline__ Work work_of(const KArgs &p, int w) {
+// The unit `word` (see attn::kOne ..) with items r0 and, for kTwo, r1.
+__device__ __forceinline__ Work work_of(const KArgs &p, int word, int kvh, const Raw &r0, const Raw &r1) {
     Work k;
-    const int u = w / p.a.hkv;
-    k.kvh = w - u * p.a.hkv;
-    const int word = __ldg(p.a.units + u);
+    k.kvh = kvh;
     k.shared = (word & 3) == attn::kPair;
-    k.s[0] = k.s[1] = slot_of(p, word >> 2);
+    k.s[0] = k.s[1] = slot_of(p, r0);
     if (k.shared) {
         k.s[1].nt = k.s[0].nt - p.tpt;
         k.s[0].nt = p.tpt;
@@ -152,7 +159,7 @@ __device__ __forceinline__ Work work_of(const KArgs &p, int w) {
         k.s[1].lim0 += k.s[0].step * p.tpt;
         if (k.s[1].part >= 0) k.s[1].part += p.tpt;
     } else if ((word & 3) == attn::kTwo) {
-        k.s[1] = slot_of(p, (word >> 2) + 1);
+        k.s[1] = slot_of(p, r1);
     } else {
         k.s[1].nt = 0;
     }
@@ -314,23 +321,31 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             int st = 0, fill = 0;
             uint32_t par = 1;  // of the stage's last release
             bool ok = true;
-            // this lane's box of a block: its first row
-            auto box_row = [&](const Slot &k, int j) {
-                const int key = (k.blk0 + j) * attn::kBlock + lane * p.box_rows;
-                if (lane >= subs || key >= k.kv_len) return oob;
+            // This lane's box of a block of a stream: what the table says of it, fetched a
+            // step ahead, and then its first row.
+            auto entry = [&](const Slot &k, int j) {
+                const int box = (k.blk0 + j) * subs + lane;
+                if (lane >= subs || box * p.box_rows >= k.kv_len) return 0;
                 const int32_t *tab = k.prob >= 0 ? p.a.table + (long long)k.prob * p.a.ld_table
                                                  : p.a.ptable + (long long)(-1 - k.prob) * p.a.ld_ptable;
-                const long long x = p.a.page ? (long long)__ldg(tab + key / p.a.page) * p.a.page + key % p.a.page
-                                             : (long long)__ldg(tab) + key;
-                if (x < 0 || x + min(p.box_rows, k.kv_len - key) > p.a.n_rows)
+                const int at = !p.a.page ? 0 : p.page_shift >= 0 ? box >> p.page_shift : box * p.box_rows / p.a.page;
+                return __ldg(tab + at);
+            };
+            auto box_row = [&](const Slot &k, int j, int tab) {
+                const int box = (k.blk0 + j) * subs + lane, key = box * p.box_rows;
+                if (lane >= subs || key >= k.kv_len) return oob;
+                const int in = !p.a.page ? key : p.page_shift >= 0 ? key & (p.a.page - 1) : key % p.a.page;
+                const long long x = p.a.page ? (long long)tab * p.a.page + in : (long long)tab + in;
+                if (x < 0 || x + min(p.box_rows, k.kv_len - key) > p.a.n_rows) {
                     atomicExch(status, (int)LORA_ERR_DEVICE_INDEX);
-                return x < -(long long)p.box_rows || x > p.a.n_rows ? oob : (int)x;
+                    if (x < -(long long)p.box_rows || x > p.a.n_rows) return oob;
+                }
+                return (int)x;
             };
             auto load = [&](const CUtensorMap *map, int kvh, int row) {
                 if (fill >= kNS) ok &= wait(&bars->kv_empty[st], par, bars, status);
-                if (ok = all(ok); ok) {
+                if (ok) {
                     if (lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
-                    __syncwarp();
                     if (lane < subs) {
                         char *dst = ring + st * Sh::kStage + lane * p.box_rows * 128;
 #pragma unroll
@@ -344,11 +359,32 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     par ^= 1u;
                 }
             };
+            // Units are taken one after the other, each when the one before is nearly loaded
+            // (sooner would bind the rest of the work to whoever asked first).  From a short
+            // unit on the next two are bound instead, and what the plan says of the next one
+            // is fetched between the loads: its dependent reads would otherwise take longer
+            // than the unit.
             const int n_work = __ldg(p.a.counters + attn::kUnits) * p.a.hkv;
-            int w = blockIdx.x;  // the first is given, the others are taken as they come
+            int w = blockIdx.x;       // the first is given
+            int ahead = -1;           // the one after it, when it is taken
+            bool known = false;       // ... and what the plan says of it fetched
+            int word = 0;
+            Raw r0, r1;
+            auto take = [&]() { return (int)gridDim.x + atomicAdd(p.a.tickets, 1); };
+            auto fetch_word = [&](int unit) { word = unit < n_work ? __ldg(p.a.units + unit / p.a.hkv) : 0; };
+            auto fetch_items = [&](int unit) {
+                if (unit < n_work) {
+                    r0 = raw_of(p, word >> 2);
+                    r1 = raw_of(p, (word >> 2) + ((word & 3) == attn::kTwo));
+                }
+            };
             while (ok) {
                 Work k;
-                if (w < n_work) k = work_of(p, w);
+                if (!known) {
+                    fetch_word(w);
+                    fetch_items(w);
+                }
+                if (w < n_work) k = work_of(p, word, w % p.a.hkv, r0, r1);
                 if (round >= kWorks)
                     ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
                 if (lane == 0) {
@@ -359,26 +395,51 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 ++round;
                 if (w >= n_work) break;
                 const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
-                int row[2] = {oob, oob};
+                const bool brief = k.n <= kBrief;
+                known = brief && ahead >= 0;
+                int taken = -1;  // lane 0: tickets asked for during the unit, not yet looked at
+                int row[2], tab[2];
+                tab[0] = nb[0] ? entry(k.s[0], 0) : 0;
+                tab[1] = nb[1] ? entry(k.s[1], 0) : 0;
+                if (known) fetch_word(ahead);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (nb[c]) {
-                        row[c] = box_row(k.s[c], 0);
+                        row[c] = box_row(k.s[c], 0, tab[c]);
+                        if (nb[c] > 1) tab[c] = entry(k.s[c], 1);
                         load(&p.tk, k.kvh, row[c]);
                     }
+                if (known) fetch_items(ahead);
 #pragma unroll 1
-                for (int j = 0; j < k.n && ok; ++j)
+                for (int j = 0; j < k.n; ++j) {
+                    if (j == max(0, k.n - kBrief) && lane == 0 && (known || ahead < 0)) taken = take();
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         if (j < nb[c]) {
-                            const int next = j + 1 < nb[c] ? box_row(k.s[c], j + 1) : oob;
                             load(&p.tv, k.kvh, row[c]);
-                            if (j + 1 < nb[c]) load(&p.tk, k.kvh, next);
-                            row[c] = next;
+                            if (j + 1 < nb[c]) {
+                                row[c] = box_row(k.s[c], j + 1, tab[c]);
+                                if (j + 2 < nb[c]) tab[c] = entry(k.s[c], j + 2);
+                                load(&p.tk, k.kvh, row[c]);
+                            }
                         }
-                if (lane == 0) w = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
-                w = __shfl_sync(0xffffffffu, w, 0);
+                }
+                if (!k.n && lane == 0 && (known || ahead < 0)) taken = take();
+                const int got = __shfl_sync(0xffffffffu, taken, 0);
+                if (ahead < 0) {
+                    w = got;
+                } else {
+                    w = ahead;
+                    ahead = got;
+                }
+                // the first short unit binds one more
+                if (brief && ahead < 0) {
+                    if (lane == 0) taken = take();
+                    ahead = __shfl_sync(0xffffffffu, taken, 0);
+                }
+                ok = all(ok);
             }
+            __threadfence();  // what was taken is taken before the CTA counts as done
             if (lane == 0 && atomicAdd(p.a.tickets + 1, 1) == (int)gridDim.x - 1) {
                 p.a.tickets[0] = 0;  // the last CTA to end leaves them as they were
                 p.a.tickets[1] = 0;
@@ -796,6 +857,9 @@ lora_status_t lora_attn_launch(const attn::Args &a, int max_items, cudaStream_t 
     p.box_rows = attn::kBlock;
     if (a.page)
         while (a.page % p.box_rows) p.box_rows >>= 1;
+    const int boxes = a.page / p.box_rows;
+    p.page_shift = boxes & (boxes - 1) ? -1 : 0;
+    while (p.page_shift >= 0 && boxes >> (p.page_shift + 1)) ++p.page_shift;
     const int nch = a.D > 64 ? 2 : 1;
     p.q_bytes = nch * 128 * a.G * p.tpt;
     p.out32 = a.D % 16 == 0 && a.ldo % 16 == 0 && ((uintptr_t)a.out & 31) == 0;

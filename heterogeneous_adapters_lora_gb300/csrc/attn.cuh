@@ -17,13 +17,19 @@ namespace attn {
 
 constexpr int kTileRows = 128;  // rows of one MMA tile; an item has up to two
 constexpr int kBlock = 128;     // keys of a block
+constexpr int kMostKeys = 1 << 30;  // of a sequence or prefix: block ends stay within 32 bits
 
-// Ranges of keys: a batch is cut into about this many of one length (times
-// key/value heads), if its tiles are that long; tiles of one row tile into
-// shorter ones, whose partial results are small.  None has less than
-// kMinBlocks blocks unless its tile has no more.
+// How long a unit takes a CTA, in tenths of a microsecond: a block of keys of
+// an item of two row tiles (bound by the products and the softmax), a block of
+// an item of one (by HBM, two such streams at a time), and what an item takes
+// beside its blocks.
 constexpr int kSms = 152;
-constexpr int kPairRanges = kSms, kOneRanges = 2 * kSms;
+constexpr int kPairBlock = 18, kPairItem = 20, kOneBlock = 16, kOneItem = 10;
+
+// Ranges of keys: with the batch's time spread evenly over the SMs, a range of
+// a two-tile item takes at most one SM's share, one of a one-tile item, whose
+// partial results are small, half of it.  None has less than kMinBlocks blocks
+// unless its tile has no more.
 constexpr int kMinBlocks = 4;
 
 // One item of a plan (8 words).  The items of two row tiles come first, then
@@ -45,9 +51,6 @@ enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4, kJoins 
 // two row tiles, or one or two items of one tile.  units[] holds
 // (its first item << 2) | kind, the longest first.
 enum { kOne = 0, kTwo = 1, kPair = 2 };
-// Time of a block of keys, relative to each other: of a kPair unit (bound by
-// the products and the softmax) and of one stream of the others (by HBM).
-constexpr int kPairBlock = 10, kStreamBlock = 11;
 
 // tokens of an item's first or second row tile, and of an item
 __host__ __device__ inline int tile_tokens(int group) { return kTileRows / group; }

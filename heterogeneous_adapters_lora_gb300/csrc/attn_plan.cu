@@ -91,14 +91,14 @@ __device__ __forceinline__ int find_problem(const int32_t *first, int n, int til
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
     __shared__ int hist[2][kBuckets];  // items of two tiles, of one
-    __shared__ unsigned long long total_blocks;
+    __shared__ unsigned long long total_time;
     __shared__ int bad;
     const int tid = threadIdx.x;
     const int n = p.n_groups + p.n_seqs;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == 0) {
-        total_blocks = 0;
+        total_time = 0;
         bad = 0;
     }
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = hist[1][i] = 0;
@@ -140,19 +140,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         n_tiles += sum;
     }
     __syncthreads();
-    // all blocks, hence the length of a range
+    // an SM's share of the time, hence the lengths of the ranges
     unsigned long long mine = 0;
     for (int t = tid; t < n_tiles; t += kPlanThreads) {
-        const int i = find_problem(p.first_tile, n, t);
-        mine += tile_blocks(problem(p, i), t - p.first_tile[i], p.tpi);
+        const int i = find_problem(p.first_tile, n, t), j = t - p.first_tile[i];
+        const Problem q = problem(p, i);
+        const unsigned long long b = tile_blocks(q, j, p.tpi);
+        mine += 2 * min(p.tpi, q.n_tok - j * p.tpi) <= p.tpi ? attn::kOneBlock * b + attn::kOneItem
+                                                             : attn::kPairBlock * b + attn::kPairItem;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if ((tid & 31) == 0 && mine) atomicAdd(&total_blocks, mine);
+    if ((tid & 31) == 0 && mine) atomicAdd(&total_time, mine);
     __syncthreads();
-    const unsigned long long blocks_all = total_blocks * (unsigned long long)p.hkv;
-    const int range_pair = (int)max((unsigned long long)attn::kMinBlocks, (blocks_all + attn::kPairRanges - 1) / attn::kPairRanges);
-    const int range_one = (int)max((unsigned long long)attn::kMinBlocks, (blocks_all + attn::kOneRanges - 1) / attn::kOneRanges);
+    const unsigned long long share = total_time * (unsigned long long)p.hkv / attn::kSms;
+    const int range_pair = (int)max((unsigned long long)attn::kMinBlocks, share / attn::kPairBlock + 1);
+    const int range_one = (int)max((unsigned long long)attn::kMinBlocks, share / (2 * attn::kOneBlock) + 1);
     // items and partial rows of each tile; the histogram of item lengths
     int n_part = 0;
     for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
@@ -235,17 +238,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     // CTAs; all units by the time they take, the longest first
     const int per = (long long)singles * p.hkv > attn::kSms ? 2 : 1;
     const int n_units = pairs + (singles + per - 1) / per;
-    const long long top = 2LL * attn::kStreamBlock * max(range_one, range_pair);
+    const long long top = max(attn::kPairBlock * (long long)range_pair + attn::kPairItem,
+                              2LL * (attn::kOneBlock * range_one + attn::kOneItem));
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = 0;
     __syncthreads();
     auto unit = [&](int u, int *word) {
         const int at = u < pairs ? u : pairs + (u - pairs) * per;
         const bool two = u >= pairs && per == 2 && at + 1 < pairs + singles;
         *word = (at << 2) | (u < pairs ? attn::kPair : two ? attn::kTwo : attn::kOne);
-        const long long time = u < pairs ? (long long)attn::kPairBlock * (p.items[at].blk1 - p.items[at].blk0)
-                                         : (long long)attn::kStreamBlock *
-                                               (p.items[at].blk1 - p.items[at].blk0 +
-                                                (two ? p.items[at + 1].blk1 - p.items[at + 1].blk0 : 0));
+        auto blocks = [&](int i) { return (long long)(p.items[i].blk1 - p.items[i].blk0); };
+        const long long time = u < pairs ? attn::kPairBlock * blocks(at) + attn::kPairItem
+                                         : attn::kOneBlock * (blocks(at) + (two ? blocks(at + 1) : 0)) +
+                                               attn::kOneItem * (two ? 2 : 1);
         return (int)min((long long)kBuckets - 1, time * (kBuckets - 1) / top);
     };
     int word;
@@ -405,17 +409,18 @@ bool desc_ok(const lora_attn_desc_t &d) {
     return isfinite(d.scale) && d.scale > 0.f && isfinite(d.scale * 1.44269504f);
 }
 
-constexpr int kMostRanges = attn::kOneRanges > attn::kPairRanges ? attn::kOneRanges : attn::kPairRanges;
+constexpr int kMostRanges = 2 * attn::kSms;
 
 struct Caps {
     long long tpi, items, tiles, part;
 };
 
-// What a batch of the given size can need.  A tile's ranges beyond its first
-// number at most kMostRanges / n_kv_heads over all tiles (the length of a
-// range is at least all blocks * n_kv_heads / kMostRanges).  A tile of two or
-// more ranges has at most twice that many; with prefixes every token also has
-// one partial result of its own keys and one of its prefix.
+// What a batch of the given size can need.  A range of a tile beyond its first
+// stands for a range's length of blocks; all ranges of one length take at
+// least half an SM's share each, so there are at most 2 * kSms of them (times
+// key/value heads).  A tile of two or more ranges has at most twice the ranges
+// that it has beyond the first; with prefixes every token also has one partial
+// result of its own keys and one of its prefix.
 Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long groups) {
     Caps c;
     c.tpi = 2 * attn::tile_tokens(d.n_q_heads / d.n_kv_heads);
@@ -430,8 +435,8 @@ Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
-    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.items * 4) + align16((size_t)c.tiles * 16) + align16((size_t)tokens * 8) + align16((size_t)tokens * 4) +
-           align16((size_t)(seqs + groups) * 4) + 32;
+    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.items * 4) + align16((size_t)c.tiles * 16) +
+           align16((size_t)tokens * 8) + align16((size_t)tokens * 4) + align16((size_t)(seqs + groups) * 4) + 32;
 }
 
 bool caps_ok(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs, int32_t max_groups, Caps *c) {
@@ -595,7 +600,8 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
                                               const int32_t *d_group_start, const int32_t *d_prefix_len,
                                               int32_t max_kv_len, int32_t max_prefix_len, void *stream) {
     if (!plan || !plan->counters || n_seqs < 0 || total_q < 0 || n_groups < 0 || max_kv_len < 0 ||
-        max_prefix_len < 0 || (n_groups > 0 && n_seqs == 0) || (n_seqs == 0 && total_q > 0))
+        max_prefix_len < 0 || max_kv_len > attn::kMostKeys || max_prefix_len > attn::kMostKeys ||
+        (n_groups > 0 && n_seqs == 0) || (n_seqs == 0 && total_q > 0))
         return LORA_ERR_INVALID_ARG;
     if (n_seqs > plan->max_seqs || total_q > plan->max_tokens || n_groups > plan->max_groups) return LORA_ERR_CAPACITY;
     if (n_seqs > 0 && (!d_cu_q || !d_kv_len || ((uintptr_t)d_cu_q & 3) || ((uintptr_t)d_kv_len & 3)))

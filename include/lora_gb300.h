@@ -528,6 +528,7 @@ LORA_API lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_at
  * prefix_len[g] keys (d_prefix_len [n_groups] int32, 0..max_prefix_len) ahead
  * of their own.  Lengths that break these rules make an empty plan (calls with
  * it write nothing) and set the plan's status to LORA_ERR_DEVICE_INDEX.
+ * max_kv_len and max_prefix_len are at most 2^30.
  * Errors: LORA_ERR_INVALID_ARG, LORA_ERR_CAPACITY. */
 LORA_API lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_seqs, int32_t total_q,
                                             const int32_t *d_cu_q, const int32_t *d_kv_len, int32_t n_groups,

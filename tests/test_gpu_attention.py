@@ -290,6 +290,8 @@ def test_refusals():
     refused(inv, build(n=-1))
     refused(inv, build(t=-1))
     refused(inv, build(mk=-1))
+    refused(inv, build(mk=(1 << 30) + 1))
+    refused(inv, build(mp=(1 << 30) + 1))
     for field, value in (("n_q_heads", 3), ("n_q_heads", 0), ("n_kv_heads", 0), ("head_dim", 12), ("head_dim", 136),
                          ("head_dim", 0), ("page_size", 12), ("page_size", -8), ("causal", 2), ("scale", 0.0),
                          ("scale", -1.0), ("scale", float("nan")), ("scale", float("inf"))):
