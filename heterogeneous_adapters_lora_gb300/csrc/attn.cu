@@ -35,7 +35,6 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kChunkBytes = attn::kBlock * 128;  // 128 rows of 64 bf16
-constexpr int kBrief = 4;                        // blocks of a short unit
 constexpr int kMaxPolls = 1 << 25;               // of a wait (seconds)
 constexpr float kLag = 8.f;                      // the maximum in use may lag by 2^8
 constexpr float kExactBase = 1048576.f;          // up to here the rounding of the maximum is small against 1
@@ -125,18 +124,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *
     return all(wait_as<kCall>(bar, parity, b, status));
 }
 
-// An item as the plan holds it.
-struct Raw {
-    int4 x, y;
-};
-__device__ __forceinline__ Raw raw_of(const KArgs &p, int item) {
+__device__ __forceinline__ Slot slot_of(const KArgs &p, int item) {
     const int4 *at = (const int4 *)(p.a.items + item);
-    return {__ldg(at), __ldg(at + 1)};
-}
-__device__ __forceinline__ Slot slot_of(const KArgs &p, const Raw &r) {
+    const int4 x = __ldg(at), y = __ldg(at + 1);
     Slot k;
-    k.tok0 = r.x.x; k.nt = r.x.y; k.prob = r.x.z; k.blk0 = r.x.w;
-    k.nb = r.y.x - r.x.w; k.kv_len = r.y.y; k.lim0 = r.y.z; k.part = r.y.w;
+    k.tok0 = x.x; k.nt = x.y; k.prob = x.z; k.blk0 = x.w;
+    k.nb = y.x - x.w; k.kv_len = y.y; k.lim0 = y.z; k.part = y.w;
     k.step = k.prob >= 0 && p.a.causal ? 1 : 0;
     return k;
 }
@@ -146,12 +139,12 @@ __device__ __forceinline__ void clip(Slot &k) {
     const int end = lim <= 0 ? 0 : (lim - 1) / attn::kBlock + 1;
     k.nb = k.nt ? max(0, min(k.nb, end - k.blk0)) : 0;
 }
-// The unit `word` (see attn::kOne ..) with items r0 and, for kTwo, r1.
-__device__ __forceinline__ Work work_of(const KArgs &p, int word, int kvh, const Raw &r0, const Raw &r1) {
+__device__ __forceinline__ Work work_of(const KArgs &p, int w) {
     Work k;
-    k.kvh = kvh;
+    const int u = w / p.a.hkv, word = __ldg(p.a.units + u);
+    k.kvh = w - u * p.a.hkv;
     k.shared = (word & 3) == attn::kPair;
-    k.s[0] = k.s[1] = slot_of(p, r0);
+    k.s[0] = k.s[1] = slot_of(p, word >> 2);
     if (k.shared) {
         k.s[1].nt = k.s[0].nt - p.tpt;
         k.s[0].nt = p.tpt;
@@ -159,7 +152,7 @@ __device__ __forceinline__ Work work_of(const KArgs &p, int word, int kvh, const
         k.s[1].lim0 += k.s[0].step * p.tpt;
         if (k.s[1].part >= 0) k.s[1].part += p.tpt;
     } else if ((word & 3) == attn::kTwo) {
-        k.s[1] = slot_of(p, r1);
+        k.s[1] = slot_of(p, (word >> 2) + 1);
     } else {
         k.s[1].nt = 0;
     }
@@ -360,31 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 }
             };
             // Units are taken one after the other, each when the one before is nearly loaded
-            // (sooner would bind the rest of the work to whoever asked first).  From a short
-            // unit on the next two are bound instead, and what the plan says of the next one
-            // is fetched between the loads: its dependent reads would otherwise take longer
-            // than the unit.
+            // (sooner would bind the rest of the work to whoever asked first).
             const int n_work = __ldg(p.a.counters + attn::kUnits) * p.a.hkv;
-            int w = blockIdx.x;       // the first is given
-            int ahead = -1;           // the one after it, when it is taken
-            bool known = false;       // ... and what the plan says of it fetched
-            int word = 0;
-            Raw r0, r1;
-            auto take = [&]() { return (int)gridDim.x + atomicAdd(p.a.tickets, 1); };
-            auto fetch_word = [&](int unit) { word = unit < n_work ? __ldg(p.a.units + unit / p.a.hkv) : 0; };
-            auto fetch_items = [&](int unit) {
-                if (unit < n_work) {
-                    r0 = raw_of(p, word >> 2);
-                    r1 = raw_of(p, (word >> 2) + ((word & 3) == attn::kTwo));
-                }
-            };
+            int w = blockIdx.x;  // the first is given
             while (ok) {
                 Work k;
-                if (!known) {
-                    fetch_word(w);
-                    fetch_items(w);
-                }
-                if (w < n_work) k = work_of(p, word, w % p.a.hkv, r0, r1);
+                if (w < n_work) k = work_of(p, w);
                 if (round >= kWorks)
                     ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
                 if (lane == 0) {
@@ -395,13 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 ++round;
                 if (w >= n_work) break;
                 const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
-                const bool brief = k.n <= kBrief;
-                known = brief && ahead >= 0;
-                int taken = -1;  // lane 0: tickets asked for during the unit, not yet looked at
                 int row[2], tab[2];
                 tab[0] = nb[0] ? entry(k.s[0], 0) : 0;
                 tab[1] = nb[1] ? entry(k.s[1], 0) : 0;
-                if (known) fetch_word(ahead);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (nb[c]) {
@@ -409,10 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                         if (nb[c] > 1) tab[c] = entry(k.s[c], 1);
                         load(&p.tk, k.kvh, row[c]);
                     }
-                if (known) fetch_items(ahead);
+                int taken = 0;
+                const int ask = max(0, k.n - 2);
 #pragma unroll 1
-                for (int j = 0; j < k.n; ++j) {
-                    if (j == max(0, k.n - kBrief) && lane == 0 && (known || ahead < 0)) taken = take();
+                for (int j = 0; j < max(k.n, 1); ++j) {
+                    if (j == ask && lane == 0) taken = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         if (j < nb[c]) {
@@ -424,19 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                             }
                         }
                 }
-                if (!k.n && lane == 0 && (known || ahead < 0)) taken = take();
-                const int got = __shfl_sync(0xffffffffu, taken, 0);
-                if (ahead < 0) {
-                    w = got;
-                } else {
-                    w = ahead;
-                    ahead = got;
-                }
-                // the first short unit binds one more
-                if (brief && ahead < 0) {
-                    if (lane == 0) taken = take();
-                    ahead = __shfl_sync(0xffffffffu, taken, 0);
-                }
+                w = __shfl_sync(0xffffffffu, taken, 0);
                 ok = all(ok);
             }
             __threadfence();  // what was taken is taken before the CTA counts as done
