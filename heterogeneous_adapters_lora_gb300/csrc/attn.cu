@@ -13,9 +13,9 @@
 //
 // Warp roles (384 threads, one CTA per SM, each CTA takes units in turn):
 //   warps 0-3, 4-7  softmax of slot 0 / 1, one row per thread, and its epilogue
-//   warp 8          TMA of K and V blocks into a ring of stages
+//   warps 8, 10     TMA of K and V blocks into a ring of stages, half a block each;
+//                   8 takes the units, 10 loads the Q tiles and allocates TMEM
 //   warps 9, 11     MMA issue of slot 0 / 1
-//   warp 10         TMEM allocation, TMA of the Q tiles
 // Tensor memory (512 columns): S of slot 0, 1 (128 columns each, P as bf16 in
 // the first half of its S), O of slot 0, 1.
 //
@@ -306,27 +306,34 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == 8) {
-            // ---- K and V blocks, one stage each: the first K of each stream, then
-            // for each block its V and the K of the block after it
+        if (warp == 8 || warp == 10) {
+            // ---- K and V blocks, one stage each: the first K of each stream, then for each
+            // block its V and the K of the block after it.  A stage is up to 16 boxes of a
+            // page by two chunks, which one warp issues one after the other: the two warps
+            // take half of them each.  Warp 8 takes the units, warp 10 loads the Q tiles.
+            const int half = warp == 8 ? 0 : 1;
             const int subs = attn::kBlock / p.box_rows;
             const int oob = (int)max(1LL, p.a.n_rows);  // a box from here on reads as zeros
+            // with two chunks each warp has one, else each has every other box
+            const int box0 = NCH == 2 ? lane : 2 * lane + half;
+            const bool mine = box0 < subs;
             int st = 0, fill = 0;
             uint32_t par = 1;  // of the stage's last release
+            int nq[2] = {0, 0};
             bool ok = true;
             // This lane's box of a block of a stream: what the table says of it, fetched a
             // step ahead, and then its first row.
             auto entry = [&](const Slot &k, int j) {
-                const int box = (k.blk0 + j) * subs + lane;
-                if (lane >= subs || box * p.box_rows >= k.kv_len) return 0;
+                const int box = (k.blk0 + j) * subs + box0;
+                if (!mine || box * p.box_rows >= k.kv_len) return 0;
                 const int32_t *tab = k.prob >= 0 ? p.a.table + (long long)k.prob * p.a.ld_table
                                                  : p.a.ptable + (long long)(-1 - k.prob) * p.a.ld_ptable;
                 const int at = !p.a.page ? 0 : p.page_shift >= 0 ? box >> p.page_shift : box * p.box_rows / p.a.page;
                 return __ldg(tab + at);
             };
             auto box_row = [&](const Slot &k, int j, int tab) {
-                const int box = (k.blk0 + j) * subs + lane, key = box * p.box_rows;
-                if (lane >= subs || key >= k.kv_len) return oob;
+                const int box = (k.blk0 + j) * subs + box0, key = box * p.box_rows;
+                if (!mine || key >= k.kv_len) return oob;
                 const int in = !p.a.page ? key : p.page_shift >= 0 ? key & (p.a.page - 1) : key % p.a.page;
                 const long long x = p.a.page ? (long long)tab * p.a.page + in : (long long)tab + in;
                 if (x < 0 || x + min(p.box_rows, k.kv_len - key) > p.a.n_rows) {
@@ -338,13 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             auto load = [&](const CUtensorMap *map, int kvh, int row) {
                 if (fill >= kNS) ok &= wait(&bars->kv_empty[st], par, bars, status);
                 if (ok) {
-                    if (lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
-                    if (lane < subs) {
-                        char *dst = ring + st * Sh::kStage + lane * p.box_rows * 128;
-#pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tc::tma_load_3d(dst + c * kChunkBytes, map, c * 64, kvh, row, &bars->kv_full[st]);
-                    }
+                    if (!half && lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
+                    if (mine)
+                        tc::tma_load_3d(ring + st * Sh::kStage + (NCH == 2 ? half * kChunkBytes : 0) + box0 * p.box_rows * 128,
+                                        map, NCH == 2 ? half * 64 : 0, kvh, row, &bars->kv_full[st]);
                     ++fill;
                 }
                 if (++st == kNS) {
@@ -352,26 +356,55 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     par ^= 1u;
                 }
             };
+            auto load_q = [&](const Work &k) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (!k.s[s].nb) continue;
+                    if (nq[s]) ok &= wait(&bars->q_empty[s], (uint32_t)((nq[s] - 1) & 1), bars, status);
+                    if (ok && lane == 0) {
+                        tc::mbar_expect_tx(&bars->q_full[s], p.q_bytes);
+#pragma unroll
+                        for (int c = 0; c < NCH; ++c)
+                            tc::tma_load_3d(sq + s * Sh::kStage + c * kChunkBytes, &p.tq, c * 64, k.kvh * p.a.G,
+                                            k.s[s].tok0, &bars->q_full[s]);
+                    }
+                    ++nq[s];
+                }
+            };
             // Units are taken one after the other, each when the one before is nearly loaded
             // (sooner would bind the rest of the work to whoever asked first).
-            const int n_work = __ldg(p.a.counters + attn::kUnits) * p.a.hkv;
+            const int n_work = half ? 0 : __ldg(p.a.counters + attn::kUnits) * p.a.hkv;
             int w = blockIdx.x;  // the first is given
             while (ok) {
                 Work k;
-                if (w < n_work) k = work_of(p, w);
-                if (round >= kWorks)
-                    ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
-                if (lane == 0) {
-                    if (w < n_work) bars->work[round % kWorks] = k; else bars->work[round % kWorks].n = -1;
-                    tc::mbar_arrive(&bars->work_full[round % kWorks]);
+                if (half) {
+                    const Work *at = next_work(ok, Call<true>());
+                    if (!at) break;
+                    k = *at;
+                    done_work();
+                } else {
+                    if (w < n_work) k = work_of(p, w);
+                    if (round >= kWorks)
+                        ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
+                    if (lane == 0) {
+                        if (w < n_work) bars->work[round % kWorks] = k; else bars->work[round % kWorks].n = -1;
+                        tc::mbar_arrive(&bars->work_full[round % kWorks]);
+                    }
+                    __syncwarp();
+                    ++round;
+                    if (w >= n_work) break;
                 }
-                __syncwarp();
-                ++round;
-                if (w >= n_work) break;
                 const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
                 int row[2], tab[2];
                 tab[0] = nb[0] ? entry(k.s[0], 0) : 0;
                 tab[1] = nb[1] ? entry(k.s[1], 0) : 0;
+                // The Q tiles are free when the unit before has issued its last QK: by then
+                // some of this unit's blocks are on their way, but not more than the ring holds.
+                bool q_due = half;
+                if (q_due && !fill) {
+                    load_q(k);
+                    q_due = false;
+                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (nb[c]) {
@@ -383,25 +416,32 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const int ask = max(0, k.n - 2);
 #pragma unroll 1
                 for (int j = 0; j < max(k.n, 1); ++j) {
-                    if (j == ask && lane == 0) taken = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
+                    if (!half && j == ask && lane == 0) taken = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c) {
                         if (j < nb[c]) {
                             load(&p.tv, k.kvh, row[c]);
                             if (j + 1 < nb[c]) {
                                 row[c] = box_row(k.s[c], j + 1, tab[c]);
                                 if (j + 2 < nb[c]) tab[c] = entry(k.s[c], j + 2);
-                                load(&p.tk, k.kvh, row[c]);
                             }
                         }
+                        if (q_due) {
+                            load_q(k);
+                            q_due = false;
+                        }
+                        if (j + 1 < nb[c]) load(&p.tk, k.kvh, row[c]);
+                    }
                 }
                 w = __shfl_sync(0xffffffffu, taken, 0);
                 ok = all(ok);
             }
-            __threadfence();  // what was taken is taken before the CTA counts as done
-            if (lane == 0 && atomicAdd(p.a.tickets + 1, 1) == (int)gridDim.x - 1) {
-                p.a.tickets[0] = 0;  // the last CTA to end leaves them as they were
-                p.a.tickets[1] = 0;
+            if (!half) {
+                __threadfence();  // what was taken is taken before the CTA counts as done
+                if (lane == 0 && atomicAdd(p.a.tickets + 1, 1) == (int)gridDim.x - 1) {
+                    p.a.tickets[0] = 0;  // the last CTA to end leaves them as they were
+                    p.a.tickets[1] = 0;
+                }
             }
             // every copy has landed before the CTA ends
 #pragma unroll 1
@@ -411,37 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
 #pragma unroll 1
                 while (!tc::mbar_try_wait(&bars->kv_full[s], (uint32_t)((last / kNS) & 1)) && ++polls < (1 << 16)) {}
             }
-        } else if (warp == 10) {
-            // ---- Q tiles
-            int fill[2] = {0, 0};
-            bool ok = true;
-            while (const Work *at = next_work(ok, Call<true>())) {
-                const Work &k = *at;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (!k.s[s].nb || !ok) continue;
-                    if (fill[s] && !warp_wait<true>(&bars->q_empty[s], (uint32_t)((fill[s] - 1) & 1), bars, status)) {
-                        ok = false;
-                        continue;
-                    }
-                    if (lane == 0) {
-                        tc::mbar_expect_tx(&bars->q_full[s], p.q_bytes);
-#pragma unroll
-                        for (int c = 0; c < NCH; ++c)
-                            tc::tma_load_3d(sq + s * Sh::kStage + c * kChunkBytes, &p.tq, c * 64, k.kvh * p.a.G,
-                                            k.s[s].tok0, &bars->q_full[s]);
-                    }
-                    __syncwarp();
-                    ++fill[s];
-                }
-                done_work();
-            }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 int polls = 0;
 #pragma unroll 1
-                while (fill[s] && !tc::mbar_try_wait(&bars->q_full[s], (uint32_t)((fill[s] - 1) & 1)) &&
-                       ++polls < (1 << 16)) {}
+                while (nq[s] && !tc::mbar_try_wait(&bars->q_full[s], (uint32_t)((nq[s] - 1) & 1)) && ++polls < (1 << 16)) {}
             }
         } else {
             // ---- MMA issue of one slot
