@@ -309,14 +309,17 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
         if (warp == 8 || warp == 10) {
             // ---- K and V blocks, one stage each: the first K of each stream, then for each
             // block its V and the K of the block after it.  A stage is up to 16 boxes of a
-            // page by two chunks, which one warp issues one after the other: the two warps
-            // take half of them each.  Warp 8 takes the units, warp 10 loads the Q tiles.
+            // page by two chunks, which one warp issues one after the other: of more than
+            // four pieces the two warps take half each (64 single tokens, 16-row pages: 103 us
+            // with one warp, 91 us with two).  Warp 8 takes the units, warp 10 loads the Q tiles.
             const int half = warp == 8 ? 0 : 1;
             const int subs = attn::kBlock / p.box_rows;
             const int oob = (int)max(1LL, p.a.n_rows);  // a box from here on reads as zeros
-            // with two chunks each warp has one, else each has every other box
-            const int box0 = NCH == 2 ? lane : 2 * lane + half;
-            const bool mine = box0 < subs;
+            const bool split = subs * NCH > 4;
+            // this lane's box and chunk: of two chunks a warp has one, else every other box
+            const int box0 = split ? (NCH == 2 ? lane : 2 * lane + half) : lane / NCH;
+            const int chunk = split ? (NCH == 2 ? half : 0) : lane % NCH;
+            const bool mine = box0 < subs && (split || !half);
             int st = 0, fill = 0;
             uint32_t par = 1;  // of the stage's last release
             int nq[2] = {0, 0};
@@ -347,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 if (ok) {
                     if (!half && lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
                     if (mine)
-                        tc::tma_load_3d(ring + st * Sh::kStage + (NCH == 2 ? half * kChunkBytes : 0) + box0 * p.box_rows * 128,
-                                        map, NCH == 2 ? half * 64 : 0, kvh, row, &bars->kv_full[st]);
+                        tc::tma_load_3d(ring + st * Sh::kStage + chunk * kChunkBytes + box0 * p.box_rows * 128, map,
+                                        chunk * 64, kvh, row, &bars->kv_full[st]);
                     ++fill;
                 }
                 if (++st == kNS) {
@@ -395,42 +398,37 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     if (w >= n_work) break;
                 }
                 const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
-                int row[2], tab[2];
+                int row[2] = {oob, oob}, tab[2];
                 tab[0] = nb[0] ? entry(k.s[0], 0) : 0;
                 tab[1] = nb[1] ? entry(k.s[1], 0) : 0;
                 // The Q tiles are free when the unit before has issued its last QK: by then
                 // some of this unit's blocks are on their way, but not more than the ring holds.
                 bool q_due = half;
-                if (q_due && !fill) {
+                if (half && (!split || !fill)) {
                     load_q(k);
                     q_due = false;
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (nb[c]) {
-                        row[c] = box_row(k.s[c], 0, tab[c]);
-                        if (nb[c] > 1) tab[c] = entry(k.s[c], 1);
-                        load(&p.tk, k.kvh, row[c]);
+                    if (!split) {
+                        ok = all(ok);
+                        continue;
                     }
+                }
                 int taken = 0;
-                const int ask = max(0, k.n - 2);
+                const int ask = max(-1, k.n - 3);
 #pragma unroll 1
-                for (int j = 0; j < max(k.n, 1); ++j) {
+                for (int j = -1; j < k.n; ++j) {
                     if (!half && j == ask && lane == 0) taken = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        if (j < nb[c]) {
-                            load(&p.tv, k.kvh, row[c]);
-                            if (j + 1 < nb[c]) {
-                                row[c] = box_row(k.s[c], j + 1, tab[c]);
-                                if (j + 2 < nb[c]) tab[c] = entry(k.s[c], j + 2);
-                            }
-                        }
-                        if (q_due) {
+                        if (j >= 0 && j < nb[c]) load(&p.tv, k.kvh, row[c]);
+                        if (q_due && j >= 0) {
                             load_q(k);
                             q_due = false;
                         }
-                        if (j + 1 < nb[c]) load(&p.tk, k.kvh, row[c]);
+                        if (j + 1 < nb[c]) {
+                            row[c] = box_row(k.s[c], j + 1, tab[c]);
+                            if (j + 2 < nb[c]) tab[c] = entry(k.s[c], j + 2);
+                            load(&p.tk, k.kvh, row[c]);
+                        }
                     }
                 }
                 w = __shfl_sync(0xffffffffu, taken, 0);
@@ -508,50 +506,31 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const int nb = me.nb, other = k->s[1 - s].nb, most = k->n;
                 const bool alone = !k->shared;
                 const int n = alone ? nb : most;  // blocks of the stream
-                // the first K of the slot's stream; another stream's K comes before or after it
-                if (alone && s && other) pass(1);
-                if (n) {
-                    ok &= wait(&bars->kv_full[st], par, bars, status);
-                    if (nb) {
-                        ok &= wait(&bars->q_full[s], pq, bars, status);
-                        pq ^= 1u;
-                        tc::tc_fence_after();
-                    }
-                    if (elect_one()) {
-                        if (nb) qk(st);
-                        if (nb == 1) tc::mma_commit(&bars->q_empty[s]);
-                        tc::mma_commit(&bars->kv_empty[st]);
-                    }
-                    step();
-                }
-                if (alone && !s && other) pass(1);
                 const int full = (me.kv_len >> 7) - me.blk0;  // blocks whose keys all count
+                // step j: PV of block j and QK of block j + 1, from -1 on
 #pragma unroll 1
-                for (int j = 0; j < most; ++j) {
+                for (int j = -1; j < most; ++j) {
                     // fills of the other stream that come between
-                    const int between = alone && j < other ? (j + 1 < other ? 2 : 1) : 0;
+                    const int between = alone ? (j >= 0 && j < other) + (j + 1 < other) : 0;
                     if (s) pass(between);
                     // The slots of one stream issue by turns, so that one slot's products are
                     // done, and its softmax begins, while the other's are still to come.
                     auto turn = [&]() {
-                        if (alone || (!s && !j)) return;
+                        if (alone || (!s && j <= 0) || j < 0) return;
                         ok &= wait(&bars->turn[s], pt, bars, status);
                         pt ^= 1u;
                     };
                     if (j < n) {
-                        const bool more = j + 1 < n;
+                        const bool has = j >= 0, more = j + 1 < n;
                         const int sv = st;
                         const uint32_t par_v = par;
-                        step();
+                        if (has) step();
                         const int sk = st;
                         const uint32_t par_k = par;
                         if (more) step();
-                        if (!(tc::mbar_try_wait(&bars->kv_full[sv], par_v) &
-                              (!more || tc::mbar_try_wait(&bars->kv_full[sk], par_k)))) {
-                            ok &= wait(&bars->kv_full[sv], par_v, bars, status);
-                            if (more) ok &= wait(&bars->kv_full[sk], par_k, bars, status);
-                        }
-                        if (j >= full) {
+                        if (has) ok &= wait(&bars->kv_full[sv], par_v, bars, status);
+                        if (more) ok &= wait(&bars->kv_full[sk], par_k, bars, status);
+                        if (has && j >= full) {
                             // values past the last key count for nothing, whatever their rows
                             // hold (boxes past the one it is in are zeros already; the slots of
                             // one stream both write the same zeros)
@@ -565,33 +544,31 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                                     *(uint4 *)(v + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
                             tc::fence_proxy_async();
                         }
-                        if (j < nb) {
-                            ok &= wait(&p_full[0], pp, bars, status);
-                            turn();
+                        const bool pv_due = has && j < nb, qk_due = j + 1 < nb;
+                        if (pv_due) ok &= wait(&p_full[0], pp, bars, status);
+                        turn();
+                        if (pv_due) {
                             tc::tc_fence_after();
                             if (elect_one()) pv(0, sv, j == 0);
                             ok &= wait(&p_full[1], pp, bars, status);
                             pp ^= 1u;
-                            tc::tc_fence_after();
-                            if (elect_one()) {
-                                pv(1, sv, false);
-                                if (j + 1 < nb) {
-                                    qk(sk);
-                                    if (j + 2 == nb) tc::mma_commit(&bars->q_empty[s]);
-                                } else {
-                                    tc::mma_commit(&bars->o_full[s]);
-                                }
-                                if (!alone && (j + 1 < n || !s)) tc::mbar_arrive(&bars->turn[1 - s]);
-                                tc::mma_commit(&bars->kv_empty[sv]);
-                                if (more) tc::mma_commit(&bars->kv_empty[sk]);
+                        }
+                        if (!has && qk_due) {
+                            ok &= wait(&bars->q_full[s], pq, bars, status);
+                            pq ^= 1u;
+                        }
+                        tc::tc_fence_after();
+                        if (elect_one()) {
+                            if (pv_due) pv(1, sv, false);
+                            if (qk_due) {
+                                qk(sk);
+                                if (j + 2 == nb) tc::mma_commit(&bars->q_empty[s]);
+                            } else if (pv_due) {
+                                tc::mma_commit(&bars->o_full[s]);
                             }
-                        } else {
-                            turn();
-                            if (elect_one()) {
-                                if (!alone && (j + 1 < n || !s)) tc::mbar_arrive(&bars->turn[1 - s]);
-                                tc::mma_commit(&bars->kv_empty[sv]);
-                                if (more) tc::mma_commit(&bars->kv_empty[sk]);
-                            }
+                            if (has && !alone && (more || !s)) tc::mbar_arrive(&bars->turn[1 - s]);
+                            if (has) tc::mma_commit(&bars->kv_empty[sv]);
+                            if (more) tc::mma_commit(&bars->kv_empty[sk]);
                         }
                     }
                     if (!s) pass(between);
