@@ -120,6 +120,43 @@ def test_many_tokens():
     Case(3001, heads=(8, 2, 128), max_pos=4000, seed=1).run().check()
 
 
+@pytest.mark.parametrize("heads,rot,inter,kw", [
+    ((8, 2, 128), 128, 0, dict(pad=40)), ((6, 3, 64), 32, 1, {}), ((5, 1, 40), 24, 0, {}), ((7, 1, 72), 72, 1, {}),
+    ((3, 1, 256), 256, 0, {}), ((8, 2, 64), 0, 0, dict(weights=False)), ((4, 2, 96), 96, 0, dict(slots=False, copy_v=False)),
+    ((2, 2, 128), 64, 0, dict(slots=False))])
+def test_many_tokens_of_every_kind(heads, rot, inter, kw):
+    """Enough tokens for the path over row buffers, a few of them outside the tables."""
+    c = Case(4000, heads=heads, rot=rot, interleaved=inter, max_pos=500, seed=10, **kw)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    skipped, no_kv = [], []
+    if rot:
+        c.pos[0], c.pos[1700], c.pos[3999] = -3, 500, 1 << 30
+        skipped += [0, 1700, 3999]
+    if c.slots is not None:
+        c.slots[5], c.slots[2500], c.slots[3998] = -1, c.rows, -2
+        skipped += [2500, 3998]
+        no_kv.append(5)
+    c.run(status)
+    for t in skipped:  # for the reference, which leaves these tokens out
+        c.pos[t] = 0
+    if c.slots is not None:
+        c.slots[torch.tensor(skipped + no_kv, dtype=torch.long)] = 0
+    c.check(skipped, no_kv)
+    assert int(status) == (L.CODE["LORA_ERR_DEVICE_INDEX"] if skipped else 0)
+
+
+def test_many_tokens_in_place_and_again():
+    c = Case(4000, heads=(4, 2, 64), slots=False, copy_v=False, max_pos=4000, seed=11)
+    qc, kc = c.hq * c.d, c.hkv * c.d
+    c.run().check()
+    x = c.qkv.cuda()
+    w, _, pos, cs = c.keep
+    L.lora_qk_norm_rope(c.desc(), x, x.stride(0), c.T, w[0], w[1], pos, cs, x, x.stride(0), x[:, qc:], x.stride(0),
+                        None, 0, None, c.T, None)
+    assert torch.equal(x[:, :qc], c.q) and torch.equal(x[:, qc:qc + kc], c.k)
+    assert torch.equal(x[:, qc + kc:].cpu(), c.qkv[:, qc + kc:])
+
+
 def test_no_slots_no_weights_no_values():
     Case(20, slots=False, weights=False, copy_v=False, seed=2).run().check()
 
