@@ -537,7 +537,8 @@ LORA_API lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_se
 
 /* Workspace bytes of the attention calls for any batch the bound plan can
  * hold.  The workspace must be zero before its first use
- * (lora_workspace_init); calls that share one must not overlap on the device. */
+ * (lora_workspace_init) and serve no other kind of call; calls that share one
+ * must not overlap on the device. */
 LORA_API size_t lora_attn_workspace_bytes(const lora_attn_plan_t *plan);
 
 /* Attention over packed sequences (whole prompts, chunks of prompts behind
@@ -550,7 +551,9 @@ LORA_API size_t lora_attn_workspace_bytes(const lora_attn_plan_t *plan);
  * (page_size 0), or row table[b][j / page_size] * page_size + j % page_size;
  * table is int32 device with ld_table entries per sequence.  Keys that no
  * query of a sequence sees do not touch its results, whatever their rows
- * hold.  Rows that a table puts outside [0, n_rows) count as zero rows and set
+ * hold (but a value that is not finite makes NaN of the results of earlier
+ * queries that share its block of 128 keys, as its product with a weight of
+ * zero is NaN).  Rows that a table puts outside [0, n_rows) count as zero rows and set
  * the plan's status to LORA_ERR_DEVICE_INDEX.  Scores and sums are fp32; the
  * probabilities are rounded to bf16 for their product with v.
  * The result does not change from run to run.
