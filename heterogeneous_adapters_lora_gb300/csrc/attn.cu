@@ -124,9 +124,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Bars *
     return all(wait_as<kCall>(bar, parity, b, status));
 }
 
-__device__ __forceinline__ Slot slot_of(const KArgs &p, int item) {
-    const int4 *at = (const int4 *)(p.a.items + item);
-    const int4 x = __ldg(at), y = __ldg(at + 1);
+__device__ __forceinline__ Slot slot_of(const KArgs &p, const int4 x, const int4 y) {
     Slot k;
     k.tok0 = x.x; k.nt = x.y; k.prob = x.z; k.blk0 = x.w;
     k.nb = y.x - x.w; k.kv_len = y.y; k.lim0 = y.z; k.part = y.w;
@@ -141,20 +139,20 @@ __device__ __forceinline__ void clip(Slot &k) {
 }
 __device__ __forceinline__ Work work_of(const KArgs &p, int w) {
     Work k;
-    const int u = w / p.a.hkv, word = __ldg(p.a.units + u);
+    const int u = w / p.a.hkv;
     k.kvh = w - u * p.a.hkv;
-    k.shared = (word & 3) == attn::kPair;
-    k.s[0] = k.s[1] = slot_of(p, word >> 2);
+    const int4 *at = (const int4 *)(p.a.units + u);
+    const int4 x0 = __ldg(at), y0 = __ldg(at + 1), x1 = __ldg(at + 2), y1 = __ldg(at + 3);
+    k.s[0] = slot_of(p, x0, y0);
+    k.s[1] = slot_of(p, x1, y1);
+    k.shared = k.s[0].nt > p.tpt;
     if (k.shared) {
+        k.s[1] = k.s[0];
         k.s[1].nt = k.s[0].nt - p.tpt;
         k.s[0].nt = p.tpt;
         k.s[1].tok0 += p.tpt;
         k.s[1].lim0 += k.s[0].step * p.tpt;
         if (k.s[1].part >= 0) k.s[1].part += p.tpt;
-    } else if ((word & 3) == attn::kTwo) {
-        k.s[1] = slot_of(p, (word >> 2) + 1);
-    } else {
-        k.s[1].nt = 0;
     }
     clip(k.s[0]);
     clip(k.s[1]);
@@ -376,17 +374,18 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             };
             // Units are taken one after the other, each when the one before is nearly loaded
             // (sooner would bind the rest of the work to whoever asked first).
+            int w = blockIdx.x;  // the first is given (the plan has room for it, built or not)
+            Work k;
+            if (!half) k = work_of(p, w);
             const int n_work = half ? 0 : __ldg(p.a.counters + attn::kUnits) * p.a.hkv;
-            int w = blockIdx.x;  // the first is given
             while (ok) {
-                Work k;
                 if (half) {
                     const Work *at = next_work(ok, Call<true>());
                     if (!at) break;
                     k = *at;
                     done_work();
                 } else {
-                    if (w < n_work) k = work_of(p, w);
+                    if (round && w < n_work) k = work_of(p, w);
                     if (round >= kWorks)
                         ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
                     if (lane == 0) {

@@ -48,16 +48,17 @@ static_assert(sizeof(Item) == 32, "plan items are 8 words");
 enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4, kJoins = 5 };
 
 // A unit is what a CTA works on at a time, for one key/value head: an item of
-// two row tiles, or one or two items of one tile.  units[] holds
-// (its first item << 2) | kind, the longest first.
-enum { kOne = 0, kTwo = 1, kPair = 2 };
+// two row tiles, or one or two items of one tile.  Units come the longest
+// first, and hold their items, so that one read tells all of the next one.
+struct Unit {
+    Item item[2];  // item[1].n_tok is 0 when there is one
+};
 
 // tokens of an item's first or second row tile, and of an item
 __host__ __device__ inline int tile_tokens(int group) { return kTileRows / group; }
 
 struct Args {
-    const Item *items;
-    const int32_t *units;
+    const Unit *units;
     const int32_t *counters;
     int32_t *tickets;  // [0] units taken beyond each CTA's first, [1] CTAs done; zero between calls
     int32_t *status;

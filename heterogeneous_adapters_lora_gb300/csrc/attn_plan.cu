@@ -18,7 +18,8 @@ struct PlanArgs {
     int tpi;      // tokens of an item
     int hkv, causal;
     Item *items;
-    int32_t *units, *tiles, *token_tiles, *joins, *first_tile, *counters;
+    attn::Unit *units;
+    int32_t *tiles, *token_tiles, *joins, *first_tile, *counters;
     int max_tokens;
 };
 
@@ -242,18 +243,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                               2LL * (attn::kOneBlock * range_one + attn::kOneItem));
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = 0;
     __syncthreads();
-    auto unit = [&](int u, int *word) {
+    auto unit = [&](int u, int *first, bool *both) {
         const int at = u < pairs ? u : pairs + (u - pairs) * per;
         const bool two = u >= pairs && per == 2 && at + 1 < pairs + singles;
-        *word = (at << 2) | (u < pairs ? attn::kPair : two ? attn::kTwo : attn::kOne);
+        *first = at;
+        *both = two;
         auto blocks = [&](int i) { return (long long)(p.items[i].blk1 - p.items[i].blk0); };
         const long long time = u < pairs ? attn::kPairBlock * blocks(at) + attn::kPairItem
                                          : attn::kOneBlock * (blocks(at) + (two ? blocks(at + 1) : 0)) +
                                                attn::kOneItem * (two ? 2 : 1);
         return (int)min((long long)kBuckets - 1, time * (kBuckets - 1) / top);
     };
-    int word;
-    for (int u = tid; u < n_units; u += kPlanThreads) atomicAdd(&hist[0][unit(u, &word)], 1);
+    int first;
+    bool both;
+    for (int u = tid; u < n_units; u += kPlanThreads) atomicAdd(&hist[0][unit(u, &first, &both)], 1);
     __syncthreads();
     {
         int sum;
@@ -263,8 +266,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     __syncthreads();
     for (int u = tid; u < n_units; u += kPlanThreads) {
-        const int b = unit(u, &word);
-        p.units[atomicAdd(&hist[0][b], 1)] = word;
+        const int b = unit(u, &first, &both);
+        const int4 *from = (const int4 *)(p.items + first);
+        int4 *to = (int4 *)(p.units + atomicAdd(&hist[0][b], 1));
+        to[0] = from[0];
+        to[1] = from[1];
+        to[2] = both ? from[2] : make_int4(0, 0, 0, 0);
+        to[3] = both ? from[3] : make_int4(0, 0, 0, 0);
     }
     // the tokens with partial results
     int n_joins = 0;
@@ -435,7 +443,7 @@ Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
-    return align16((size_t)c.items * sizeof(Item)) + align16((size_t)c.items * 4) + align16((size_t)c.tiles * 16) +
+    return align16((size_t)c.items * sizeof(Item)) + (size_t)c.items * sizeof(attn::Unit) + align16((size_t)c.tiles * 16) +
            align16((size_t)tokens * 8) + align16((size_t)tokens * 4) + align16((size_t)(seqs + groups) * 4) + 32;
 }
 
@@ -493,8 +501,7 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     cudaStream_t s = (cudaStream_t)stream;
     attn::Args a;
     memset(&a, 0, sizeof(a));
-    a.items = (const Item *)plan->items;
-    a.units = plan->units;
+    a.units = (const attn::Unit *)plan->units;
     a.counters = plan->counters;
     a.tickets = (int32_t *)workspace;
     a.status = plan->counters + attn::kStatus;
@@ -523,7 +530,7 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     a.part_lse = (float *)((char *)workspace + kWsHead +
                            align16((size_t)plan->max_part * d.n_q_heads * d.head_dim * 4));
     const Caps c = caps(d, plan->total_q, plan->n_seqs, plan->n_groups);
-    const lora_status_t st = lora_attn_launch(a, (int)c.items, s);
+    const lora_status_t st = lora_attn_launch(a, (int)c.items, s);  // no more units than items
     if (st != LORA_OK) return st;
     // without prefixes, tiles of up to kMinBlocks blocks are never split
     if (!prefix && plan->max_kv_len <= attn::kMinBlocks * attn::kBlock) return LORA_OK;
@@ -584,7 +591,7 @@ extern "C" lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_
     plan->items = (int32_t *)at;
     at += align16((size_t)c.items * sizeof(Item));
     plan->units = (int32_t *)at;
-    at += align16((size_t)c.items * 4);
+    at += (size_t)c.items * sizeof(attn::Unit);
     plan->tiles = (int32_t *)at;
     at += align16((size_t)c.tiles * 16);
     plan->token_tiles = (int32_t *)at;
@@ -624,7 +631,7 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
     p.hkv = plan->desc.n_kv_heads;
     p.causal = plan->desc.causal;
     p.items = (Item *)plan->items;
-    p.units = plan->units;
+    p.units = (attn::Unit *)plan->units;
     p.tiles = plan->tiles;
     p.token_tiles = plan->token_tiles;
     p.joins = plan->joins;

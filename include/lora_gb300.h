@@ -488,7 +488,8 @@ typedef struct {
  * same.  Caller-owned device memory, bound with lora_attn_plan_bind.
  *   items[max_items][8]  tiles of queries x ranges of keys: those of two row tiles,
  *                        then those of one, each the longest first
- *   units[max_items]     items that a CTA works on together, the longest first
+ *   units[max_items][16] the one or two items that a CTA works on together, the
+ *                        longest first
  *   tiles[max_tiles][4]  tiles of queries and where their partial results lie
  *   token_tiles[2][max_tokens]  each token's own tile and prefix tile (-1: none
  *                        that has to be joined)
