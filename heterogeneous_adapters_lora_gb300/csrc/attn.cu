@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const int ask = max(-1, k.n - 3);
 #pragma unroll 1
                 for (int j = -1; j < k.n; ++j) {
-                    if (!half && j == ask && lane == 0) taken = (int)gridDim.x + atomicAdd(p.a.tickets, 1);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         if (j >= 0 && j < nb[c]) load(&p.tv, k.kvh, row[c]);
@@ -429,8 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                             load(&p.tk, k.kvh, row[c]);
                         }
                     }
+                    if (!half && j == ask && lane == 0) taken = atomicAdd(p.a.tickets, 1);
                 }
-                w = __shfl_sync(0xffffffffu, taken, 0);
+                w = __shfl_sync(0xffffffffu, taken, 0) + (int)gridDim.x;
                 ok = all(ok);
             }
             if (!half) {
@@ -617,10 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     if (key0 + attn::kBlock > min_lim) {
                         const int rel = lim - key0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 4; ++c) {
+                            if (key0 + c * 32 + 32 <= min_lim) continue;  // seen whole by all rows
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (c * 32 + i >= rel) x[c][i] = 0xff800000u;
+                        }
                     }
                     float mx[4];
 #pragma unroll

@@ -165,11 +165,12 @@ def ptr(obj):
     """Raw address of a torch tensor, numpy array, int or None."""
     if obj is None:
         return None
+    try:
+        return obj.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(obj, int):
         return obj
-    data_ptr = getattr(obj, "data_ptr", None)
-    if data_ptr is not None:
-        return data_ptr()
     if hasattr(obj, "ctypes"):
         return obj.ctypes.data
     raise TypeError(type(obj))
