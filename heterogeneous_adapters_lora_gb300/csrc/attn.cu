@@ -19,6 +19,15 @@
 // Tensor memory (512 columns): S of slot 0, 1 (128 columns each, P as bf16 in
 // the first half of its S), O of slot 0, 1.
 //
+// What bounds it: the products of two full slots take 2048 cycles a block, the
+// two softmaxes (512 cycles of exponentials each and about 300 other
+// instructions) run under them, and a slot's own chain (S there, softmax 1100
+// to 1400 cycles, 250 to the MMA warp, 1024 of products) just fits: one prompt
+// of 7995 tokens, 32 heads of 128 over 8: 300 us, 1.75 PFLOP/s, tensor pipe 76%
+// active.  One-tile items of decode batches are bound by HBM (64 single tokens
+// over up to 4000 keys: 90 us, 5.9 TB/s).  Short units pay about 5000 cycles
+// beside their blocks: the first softmax, the stores, code fetched once.
+//
 // Orders that no barrier of its own is needed for: a slot's QK of block j + 1
 // is issued after its PV of block j, so "S is there" also says that O holds
 // block j; a slot's PV of a unit's first block waits for P, which the same
@@ -216,9 +225,14 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// The products with the upper halves of the descriptors as immediates: only
-// start addresses change from one to the next.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // see tc::desc_sw128
+// The products with the upper halves of the shared-memory descriptors as
+// immediates: only start addresses change from one to the next (computing whole
+// descriptors in a lane-0 branch issued a product every 110 cycles, this one
+// every 68).  128-byte swizzle, 8 rows of 128 bytes to a group of 1024 bytes.
+// Q and K lie with k contiguous.  V's rows are its k, its N elements are
+// contiguous in chunks of 64, and the leading byte offset is the way to the
+// next chunk; a K step of 16 rows advances the start address by 2048 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // as tc::desc_sw128 has them
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
@@ -228,6 +242,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
         "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHi)
         : "memory");
 }
+// A from tensor memory: row r in lane r, two bf16 of consecutive k per column.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"

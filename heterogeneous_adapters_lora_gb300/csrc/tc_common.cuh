@@ -105,17 +105,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem desc]: A holds row r in lane r, two bf16 of
-// consecutive k per 32-bit column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread completes.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -178,19 +167,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t smem_addr) {
     d |= (uint64_t)(1024 >> 4) << 32;             // stride byte offset: 8 rows x 128 B
     d |= (uint64_t)1 << 46;                       // descriptor version for tcgen05
     d |= (uint64_t)2 << 61;                       // 128-byte swizzle
-    return d;
-}
-// The same swizzle with rows along k: an operand whose M/N elements are
-// contiguous, in chunks of 64 (rows of 128 bytes, one per k); the chunks of
-// 64 are chunk_bytes apart.  A K step of 16 rows advances the start address
-// by 2048 bytes.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t smem_addr, uint32_t chunk_bytes) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(chunk_bytes >> 4) << 16;      // leading byte offset: the next 64 of M/N
-    d |= (uint64_t)(1024 >> 4) << 32;             // stride byte offset: the next 8 of K
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
     return d;
 }
 // Instruction descriptor of kind::f16: bf16 A and B, fp32 D, both K-major.
