@@ -12,14 +12,28 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;  // of the sort of items by length
 
+// A token with partial results: first those of its own tile, then its prefix's.
+struct Parts {
+    int base, nt;      // first token row of its slot in the first of them, tokens of the slot
+    int at;            // which of the slot's tokens it is
+    int apart, n;      // token rows from one to the next, and how many there are
+};
+struct Join {
+    int token;
+    Parts part[2];
+    int unused;
+};
+static_assert(sizeof(Join) == 48, "joins are 12 words");
+
 struct PlanArgs {
     const int32_t *cu_q, *kv_len, *group_start, *prefix_len;
     int n_seqs, n_groups, T, max_kv, max_prefix;
     int tpi;      // tokens of an item
-    int hkv, causal;
+    int hkv, causal, tpt;
     Item *items;
     attn::Unit *units;
-    int32_t *tiles, *token_tiles, *joins, *first_tile, *counters;
+    int32_t *tiles, *token_tiles, *first_tile, *counters;
+    Join *joins;
     int max_tokens;
 };
 
@@ -281,7 +295,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int has = t < p.T && (p.token_tiles[t] >= 0 || p.token_tiles[p.max_tokens + t] >= 0);
         int sum;
         const int at = block_scan(has, &sum);
-        if (has) p.joins[n_joins + at] = t;
+        if (has) {
+            Join r;
+            r.token = t;
+            r.unused = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int tile = p.token_tiles[k * p.max_tokens + t];
+                r.part[k] = {0, 1, 0, 0, 0};
+                if (tile < 0) continue;
+                const int4 e = *(const int4 *)(p.tiles + 4 * (long long)tile);
+                const int i = t - e.z, slot = i / p.tpt;  // slots of tpt tokens, the last one of what is left
+                r.part[k] = {e.x + slot * p.tpt, min(p.tpt, e.w - slot * p.tpt), i - slot * p.tpt, e.w, e.y};
+            }
+            p.joins[n_joins + at] = r;
+        }
         n_joins += sum;
     }
     if (tid == 0) {
@@ -297,78 +325,80 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // ---------------------------------------------------------------- join
 
 struct JoinArgs {
-    const int32_t *tiles, *token_tiles, *joins, *counters;
-    int max_tokens, T, hq, hkv, G, D, tpt;
+    const Join *joins;
+    const int32_t *counters;
+    int hq, hkv, G, D;
     const float *part_o, *part_lse;
     uint16_t *out;
     long long ldo;
 };
 
 constexpr int kJoinThreads = 128;
-constexpr int kJoinCtas = 3 * attn::kSms;  // what the registers let be resident
-constexpr int kJoinAhead = 4;  // parts that it reads together
 constexpr int kJoinHeads = 4;  // query heads of a key/value head that a warp has in hand
 
 // out[t][h] = sum_s 2^lse_s o_s / sum_s 2^lse_s over the partial results of
 // the token's own tile and of its prefix tile, in that order (so the result
 // does not depend on which item ended first).  A warp takes a token and
 // kJoinHeads heads of one key/value head: their rows are neighbours in a
-// partial result, so each line that a lane (four elements of a head) fetches
-// serves all of them.
+// partial result, so the 64 bytes that a lane (four elements of a head) reads
+// lie side by side, kAhead parts at a time.  With few tokens the chain of
+// reads after the item kernel counts (about 4 us of a call, whose largest
+// step is one read of what other SMs wrote) and four parts at once are best;
+// with many the warps in flight do, of which three parts leave room for more
+// (256 tokens behind one prefix 93 -> 90 us, 4 tokens 14.6 -> 15.1).
+template <int kAhead>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs p) {
     // The plan was complete before the item kernel began, which lets this one
     // start: only the partial results are waited for.
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31;
     const int per = (p.G + kJoinHeads - 1) / kJoinHeads * p.hkv;  // warps of a token
+    const int step = gridDim.x * (kJoinThreads / 32);
+    int w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    auto entry = [&](int i) {
+        Join r;
+        const int4 *at = (const int4 *)(p.joins + i);
+        *(int4 *)&r.token = __ldg(at);
+        *((int4 *)&r.token + 1) = __ldg(at + 1);
+        *((int4 *)&r.token + 2) = __ldg(at + 2);
+        return r;
+    };
     const long long n = (long long)__ldg(p.counters + attn::kJoins) * per;
-    const long long step = (long long)gridDim.x * (kJoinThreads / 32);
     bool waited = false;
-    for (long long w = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); w < n; w += step) {
-        const int t = __ldg(p.joins + w / per), kvh = (int)(w % per) % p.hkv, g0 = (int)(w % per) / p.hkv * kJoinHeads;
-        // the token's parts, first its own tile's, then its prefix's: the row in the
-        // first of them, rows of a part, how far apart they are, and how many
-        long long first[2], apart[2];
-        int parts[2], rows[2], at[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int tile = __ldg(p.token_tiles + k * p.max_tokens + t);
-            parts[k] = rows[k] = at[k] = 0;
-            first[k] = apart[k] = 0;
-            if (tile < 0) continue;
-            const int4 e = __ldg((const int4 *)(p.tiles + 4 * (long long)tile));
-            const int i = t - e.z, slot = i / p.tpt;  // slots of tpt tokens, the last one of what is left
-            rows[k] = min(p.tpt, e.w - slot * p.tpt) * p.G;
-            at[k] = (i - slot * p.tpt) * p.G + g0;
-            first[k] = (long long)(e.x + slot * p.tpt) * p.hq + (long long)kvh * rows[k];
-            apart[k] = (long long)e.w * p.hq;
-            parts[k] = e.y;
-        }
-        const int all = parts[0] + parts[1];
+#pragma unroll 1
+    for (; w < n; w += step) {
+        const Join r = entry(w / per);
+        const int kvh = (w % per) % p.hkv, g0 = (w % per) / p.hkv * kJoinHeads;
+        const int heads = min(kJoinHeads, p.G - g0), all = r.part[0].n + r.part[1].n;
+        const int n0 = r.part[0].n, rows0 = r.part[0].nt * p.G, rows1 = r.part[1].nt * p.G;
+        const int at0 = r.part[0].at * p.G + g0, at1 = r.part[1].at * p.G + g0;
+        const long long first0 = (long long)r.part[0].base * p.hq + kvh * rows0, apart0 = (long long)r.part[0].apart * p.hq;
+        const long long first1 = (long long)r.part[1].base * p.hq + kvh * rows1, apart1 = (long long)r.part[1].apart * p.hq;
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
         waited = true;
-        const int heads = min(kJoinHeads, p.G - g0);
         float top[kJoinHeads], sum[kJoinHeads], acc[kJoinHeads][4];
 #pragma unroll
         for (int u = 0; u < kJoinHeads; ++u) {
             top[u] = -INFINITY;
             sum[u] = acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
         }
-        // kJoinAhead parts at a time, their loads together; the sums so far are
+        // kAhead parts at a time, their loads together; the sums so far are
         // rescaled when a part's maximum is above theirs
-        for (int s0 = 0; s0 < all; s0 += kJoinAhead) {
-            float lse[kJoinAhead][kJoinHeads];
-            float4 v[kJoinAhead][kJoinHeads];
+#pragma unroll 1
+        for (int s0 = 0; s0 < all; s0 += kAhead) {
+            float lse[kAhead][kJoinHeads];
+            float4 v[kAhead][kJoinHeads];
 #pragma unroll
-            for (int a = 0; a < kJoinAhead; ++a) {
-                const int s = s0 + a, k = s >= parts[0] ? 1 : 0;
-                const long long row = k ? first[1] + (s - parts[0]) * apart[1] : first[0] + s * apart[0];
-                const long long one = row + (k ? at[1] : at[0]);
-                const float *o = p.part_o + row * p.D + ((long long)lane * (k ? rows[1] : rows[0]) + (k ? at[1] : at[0])) * 4;
+            for (int a = 0; a < kAhead; ++a) {
+                const int s = s0 + a;
+                const bool second = s >= n0;
+                const int rows = second ? rows1 : rows0, at = second ? at1 : at0;
+                const long long first = second ? first1 + (s - n0) * apart1 : first0 + s * apart0;
+                const float *o = p.part_o + first * p.D + (lane * rows + at) * 4;
 #pragma unroll
                 for (int u = 0; u < kJoinHeads; ++u) {
                     const bool is = s < all && u < heads;
-                    lse[a][u] = is ? p.part_lse[one + u] : -INFINITY;
+                    lse[a][u] = is ? p.part_lse[first + at + u] : -INFINITY;
                     v[a][u] = is && 4 * lane < p.D ? *(const float4 *)(o + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
@@ -376,13 +406,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             for (int u = 0; u < kJoinHeads; ++u) {
                 float m = top[u];
 #pragma unroll
-                for (int a = 0; a < kJoinAhead; ++a) m = fmaxf(m, lse[a][u]);
+                for (int a = 0; a < kAhead; ++a) m = fmaxf(m, lse[a][u]);
                 const float base = m == -INFINITY ? 0.f : m, old = exp2f(top[u] - base);
                 top[u] = m;
                 sum[u] *= old;
                 acc[u][0] *= old; acc[u][1] *= old; acc[u][2] *= old; acc[u][3] *= old;
 #pragma unroll
-                for (int a = 0; a < kJoinAhead; ++a) {
+                for (int a = 0; a < kAhead; ++a) {
                     // a part without keys weighs nothing; a NaN or infinite score makes its weight NaN
                     const float x = exp2f(lse[a][u] - base);
                     if (x == 0.f) continue;
@@ -395,10 +425,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
         for (int u = 0; u < kJoinHeads; ++u) {
             if (u >= heads || 4 * lane >= p.D) continue;
-            const float r = sum[u] == 0.f ? 0.f : 1.f / sum[u];
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[u][0] * r, acc[u][1] * r);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[u][2] * r, acc[u][3] * r);
-            *(uint2 *)(p.out + (long long)t * p.ldo + (long long)(kvh * p.G + g0 + u) * p.D + 4 * lane) =
+            const float f = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[u][0] * f, acc[u][1] * f);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[u][2] * f, acc[u][3] * f);
+            *(uint2 *)(p.out + (long long)r.token * p.ldo + (long long)(kvh * p.G + g0 + u) * p.D + 4 * lane) =
                 make_uint2(*(const uint32_t *)&x, *(const uint32_t *)&y);
         }
     }
@@ -444,14 +474,14 @@ size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
     return align16((size_t)c.items * sizeof(Item)) + (size_t)c.items * sizeof(attn::Unit) + align16((size_t)c.tiles * 16) +
-           align16((size_t)tokens * 8) + align16((size_t)tokens * 4) + align16((size_t)(seqs + groups) * 4) + 32;
+           align16((size_t)tokens * 8) + (size_t)tokens * sizeof(Join) + align16((size_t)(seqs + groups) * 4) + 32;
 }
 
 bool caps_ok(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs, int32_t max_groups, Caps *c) {
     if (!desc || !desc_ok(*desc) || max_tokens < 1 || max_seqs < 1 || max_groups < 0 || max_groups > max_seqs)
         return false;
     *c = caps(*desc, max_tokens, max_seqs, max_groups);
-    return c->items * desc->n_kv_heads <= 0x7fffffffLL && c->part <= 0x7fffffffLL && c->tiles <= 0x1fffffffLL;
+    return c->items * desc->n_kv_heads <= 0x7fffffffLL && (long long)max_tokens * desc->n_q_heads <= 0x3fffffffLL && c->part <= 0x7fffffffLL && c->tiles <= 0x1fffffffLL;
 }
 
 size_t part_bytes(const lora_attn_plan_t &p) {
@@ -536,27 +566,23 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     if (!prefix && plan->max_kv_len <= attn::kMinBlocks * attn::kBlock) return LORA_OK;
     JoinArgs j;
     memset(&j, 0, sizeof(j));
-    j.tiles = plan->tiles;
-    j.token_tiles = plan->token_tiles;
-    j.joins = plan->joins;
+    j.joins = (const Join *)plan->joins;
     j.counters = plan->counters;
-    j.max_tokens = plan->max_tokens;
-    j.T = plan->total_q;
     j.hq = d.n_q_heads;
     j.hkv = d.n_kv_heads;
     j.G = a.G;
     j.D = d.head_dim;
-    j.tpt = attn::tile_tokens(a.G);
     j.part_o = a.part_o;
     j.part_lse = a.part_lse;
     j.out = a.out;
     j.ldo = ldo;
     const long long warps = (long long)plan->total_q * ((a.G + kJoinHeads - 1) / kJoinHeads * d.n_kv_heads);
-    long long grid = (warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-    if (grid > kJoinCtas) grid = kJoinCtas;
+    const long long ctas = (warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+    // as many CTAs as the registers let be resident: 3 per SM with four parts at a time, 4 with three
+    const bool few = ctas <= 3 * attn::kSms;
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = config((int)grid, kJoinThreads, s, at);
-    LORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, join_kernel, j));
+    cudaLaunchConfig_t cfg = config((int)(ctas < 4 * attn::kSms ? ctas : 4 * attn::kSms), kJoinThreads, s, at);
+    LORA_CUDA_TRY(few ? cudaLaunchKernelEx(&cfg, join_kernel<4>, j) : cudaLaunchKernelEx(&cfg, join_kernel<3>, j));
     lora_note_launch();
     return LORA_OK;
 }
@@ -597,7 +623,7 @@ extern "C" lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_
     plan->token_tiles = (int32_t *)at;
     at += align16((size_t)max_tokens * 8);
     plan->joins = (int32_t *)at;
-    at += align16((size_t)max_tokens * 4);
+    at += (size_t)max_tokens * sizeof(Join);
     plan->first_tile = (int32_t *)at;
     return LORA_OK;
 }
@@ -634,7 +660,8 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
     p.units = (attn::Unit *)plan->units;
     p.tiles = plan->tiles;
     p.token_tiles = plan->token_tiles;
-    p.joins = plan->joins;
+    p.joins = (Join *)plan->joins;
+    p.tpt = attn::tile_tokens(plan->desc.n_q_heads / plan->desc.n_kv_heads);
     p.first_tile = plan->first_tile;
     p.counters = plan->counters;
     p.max_tokens = plan->max_tokens;
