@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 return (int)x;
             };
             auto load = [&](const CUtensorMap *map, int kvh, int row) {
-                if (fill >= kNS) ok &= wait(&bars->kv_empty[st], par, bars, status);
+                ok &= wait(&bars->kv_empty[st], par, bars, status);  // at once for a stage's first fill
                 if (ok) {
                     if (!half && lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
                     if (mine)
@@ -400,16 +400,16 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     k = *at;
                     done_work();
                 } else {
-                    if (round && w < n_work) k = work_of(p, w);
+                    if (round && (unsigned)w < (unsigned)n_work) k = work_of(p, w);
                     if (round >= kWorks)
                         ok = warp_wait<true>(&bars->work_empty[round % kWorks], (uint32_t)((round / kWorks - 1) & 1), bars, status);
                     if (lane == 0) {
-                        if (w < n_work) bars->work[round % kWorks] = k; else bars->work[round % kWorks].n = -1;
+                        if ((unsigned)w < (unsigned)n_work) bars->work[round % kWorks] = k; else bars->work[round % kWorks].n = -1;
                         tc::mbar_arrive(&bars->work_full[round % kWorks]);
                     }
                     __syncwarp();
                     ++round;
-                    if (w >= n_work) break;
+                    if ((unsigned)w >= (unsigned)n_work) break;
                 }
                 const int nb[2] = {k.shared ? k.n : k.s[0].nb, k.shared ? 0 : k.s[1].nb};
                 int row[2] = {oob, oob}, tab[2];

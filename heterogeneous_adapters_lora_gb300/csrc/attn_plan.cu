@@ -169,8 +169,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if ((tid & 31) == 0 && mine) atomicAdd(&total_time, mine);
     __syncthreads();
     const unsigned long long share = total_time * (unsigned long long)p.hkv / attn::kSms;
-    const int range_pair = (int)max((unsigned long long)attn::kMinBlocks, share / attn::kPairBlock + 1);
-    const int range_one = (int)max((unsigned long long)attn::kMinBlocks, share / (2 * attn::kOneBlock) + 1);
+    const unsigned long long share_pair = share / attn::kPairBlock + 1, share_one = share / (2 * attn::kOneBlock) + 1;
+    auto range_of = [&](bool prefix, int n_tok) {
+        const unsigned long long least = prefix ? attn::kMinPrefixBlocks : attn::kMinBlocks;
+        return (int)max(least, 2 * n_tok <= p.tpi ? share_one : share_pair);
+    };
     // items and partial rows of each tile; the histogram of item lengths
     int n_part = 0;
     for (int t0 = 0; t0 < n_tiles; t0 += kPlanThreads) {
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 }
                 ahead = __ldg(p.prefix_len + lo) > 0;
             }
-            range = 2 * n_tok <= p.tpi ? range_one : range_pair;
+            range = range_of(i < p.n_groups, n_tok);
             parts = (blocks + range - 1) / range;
             // no keys: zeros are written, unless a prefix has the tokens' result
             if (parts == 0 && !ahead) parts = 1;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int i = find_problem(p.first_tile, n, t);
         const Problem q = problem(p, i);
         const int j = t - p.first_tile[i], blocks = tile_blocks(q, j, p.tpi);
-        const int range = 2 * e.w <= p.tpi ? range_one : range_pair;
+        const int range = range_of(i < p.n_groups, e.w);
         for (int s = 0; s < e.y; ++s) {
             Item it;
             it.blk0 = s * range;
@@ -253,8 +256,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     // CTAs; all units by the time they take, the longest first
     const int per = (long long)singles * p.hkv > attn::kSms ? 2 : 1;
     const int n_units = pairs + (singles + per - 1) / per;
-    const long long top = max(attn::kPairBlock * (long long)range_pair + attn::kPairItem,
-                              2LL * (attn::kOneBlock * range_one + attn::kOneItem));
+    const long long top = max(attn::kPairBlock * (long long)range_of(false, p.tpi) + attn::kPairItem,
+                              2LL * (attn::kOneBlock * range_of(false, 0) + attn::kOneItem));
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = 0;
     __syncthreads();
     auto unit = [&](int u, int *first, bool *both) {
@@ -481,7 +484,8 @@ bool caps_ok(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs,
     if (!desc || !desc_ok(*desc) || max_tokens < 1 || max_seqs < 1 || max_groups < 0 || max_groups > max_seqs)
         return false;
     *c = caps(*desc, max_tokens, max_seqs, max_groups);
-    return c->items * desc->n_kv_heads <= 0x7fffffffLL && (long long)max_tokens * desc->n_q_heads <= 0x3fffffffLL && c->part <= 0x7fffffffLL && c->tiles <= 0x1fffffffLL;
+    return c->items * desc->n_kv_heads <= 0x7fffffffLL && (long long)max_tokens * desc->n_q_heads <= 0x3fffffffLL &&
+           c->part <= 0x7fffffffLL && c->tiles <= 0x1fffffffLL;
 }
 
 size_t part_bytes(const lora_attn_plan_t &p) {
@@ -513,7 +517,7 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     const lora_attn_desc_t &d = plan->desc;
     const int64_t qc = (int64_t)d.n_q_heads * d.head_dim, kc = (int64_t)d.n_kv_heads * d.head_dim;
     if (ldq < qc || ldq % 8 || ldk < kc || ldk % 8 || ldv < kc || ldv % 8 || ldo < qc || ldo % 8 || n_rows < 0 ||
-        n_rows > 0x7fffffffLL)
+        n_rows > attn::kMostRows)
         return LORA_ERR_INVALID_ARG;
     const int64_t page = d.page_size;
     if (plan->max_kv_len > 0 &&
