@@ -25,8 +25,10 @@
 // to 1400 cycles, 250 to the MMA warp, 1024 of products) just fits: one prompt
 // of 7995 tokens, 32 heads of 128 over 8: 300 us, 1.75 PFLOP/s, tensor pipe 76%
 // active.  One-tile items of decode batches are bound by HBM (64 single tokens
-// over up to 4000 keys: 90 us, 5.9 TB/s).  Short units pay about 5000 cycles
-// beside their blocks: the first softmax, the stores, code fetched once.
+// over up to 4000 keys: 89 us, 6.0 TB/s).  Short units are bound by chains of
+// dependent steps in single warps: one of two one-key items takes 8600 cycles,
+// of which reading the unit and its table and issuing four stages' copies is
+// one chain of 7000, a softmax, its wait for O and the stores another.
 //
 // Orders that no barrier of its own is needed for: a slot's QK of block j + 1
 // is issued after its PV of block j, so "S is there" also says that O holds
