@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const int rows = k.nt * p.a.G;
                 const long long prow = (long long)k.part * p.a.hq + (long long)kvh * rows;
                 uint16_t *out = p.a.out + (long long)(k.tok0 + e) * p.a.ldo + (long long)(kvh * p.a.G + g) * p.a.D;
-                float *part = p.a.part_o + prow * p.a.D + 4 * row;
+                float *part = p.a.part_o + prow * p.a.D + 8 * row;
                 // a loop, though of few rounds: code that a unit runs once comes from beyond
                 // the instruction cache, and unrolled this took longer than its work
 #pragma unroll 1
@@ -752,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                     for (int i = 0; i < 32; ++i) o[i] = some ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
                     if (k.part >= 0) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (c + 4 * i < p.a.D) *(uint4 *)part = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                            part += 4 * rows;
+                        for (int i = 0; i < 4; ++i) {
+                            if (c + 8 * i < p.a.D) st_global32(part, o + 8 * i);
+                            part += 8 * rows;
                         }
                         continue;
                     }

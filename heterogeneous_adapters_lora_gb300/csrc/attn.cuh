@@ -32,8 +32,8 @@ constexpr int kPairBlock = 18, kPairItem = 20, kOneBlock = 16, kOneItem = 10;
 // a two-tile item takes at most one SM's share, one of a one-tile item, whose
 // partial results are small, half of it.  None has less than kMinBlocks blocks
 // unless its tile has no more; or kMinPrefixBlocks of a prefix, whose results
-// are joined in any case, and with an own one are then read in one go (4 tokens
-// behind a prefix of 1000: 14.8 us with 4 blocks, 14.1 with 3, 14.3 with 2).
+// are joined in any case (4 tokens behind a prefix of 1000: 12.6 us with 4
+// blocks, 11.4 with 3, 10.6 with 2; behind one of 8000 20.0, 18.8, 21.0).
 constexpr int kMinBlocks = 4;
 constexpr int kMinPrefixBlocks = 3;
 
@@ -75,8 +75,8 @@ struct Args {
     long long ld_table, ld_ptable;
     uint16_t *out;
     // Partial results: a slot of nt tokens has, per key/value head, nt * G rows from
-    // row part * hq + head * nt * G on; its outputs lie as [D / 4][rows][4], so that
-    // the warps, with a row per lane, store them in one piece.
+    // row part * hq + head * nt * G on; its outputs lie as [D / 8][rows][8], so that
+    // the warps, with a row per lane, store them in one piece and heads are read side by side.
     float *part_o;
     float *part_lse;
 };

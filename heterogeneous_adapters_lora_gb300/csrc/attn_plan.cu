@@ -337,25 +337,32 @@ struct JoinArgs {
 };
 
 constexpr int kJoinThreads = 128;
-constexpr int kJoinHeads = 4;  // query heads of a key/value head that a warp has in hand
+
+__device__ __forceinline__ void ld_global32(float *v, const float *p) {
+    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
 
 // out[t][h] = sum_s 2^lse_s o_s / sum_s 2^lse_s over the partial results of
 // the token's own tile and of its prefix tile, in that order (so the result
-// does not depend on which item ended first).  A warp takes a token and
-// kJoinHeads heads of one key/value head: their rows are neighbours in a
-// partial result, so the 64 bytes that a lane (four elements of a head) reads
-// lie side by side, kAhead parts at a time.  With few tokens the chain of
-// reads after the item kernel counts (about 4 us of a call, whose largest
-// step is one read of what other SMs wrote) and four parts at once are best;
-// with many the warps in flight do, of which three parts leave room for more
-// (256 tokens behind one prefix 93 -> 90 us, 4 tokens 14.6 -> 15.1).
-template <int kAhead>
+// does not depend on which item ended first).  A warp takes a token and kHeads
+// heads of one key/value head, whose rows are neighbours in a partial result:
+// eight lanes have a head, a lane 8 of its elements and the 8 that lie 64 on.
+// The 4 / kHeads groups of eight lanes that share a head share its parts out,
+// and are added up in the end.  Bound by latency with few tokens (about 2.5 us
+// of a call, most of it one read of what other SMs wrote), by L2 with many.
+// With elements of four heads in a lane, 16 bytes each, it read half sectors,
+// a line per lane: 889 tokens of 28 heads in two to three parts 16 us, now 6.
+template <int kHeads, int kAhead>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs p) {
+    constexpr int kSlices = 4 / kHeads;
     // The plan was complete before the item kernel began, which lets this one
     // start: only the partial results are waited for.
     asm volatile("griddepcontrol.launch_dependents;");
-    const int lane = threadIdx.x & 31;
-    const int per = (p.G + kJoinHeads - 1) / kJoinHeads * p.hkv;  // warps of a token
+    const int lane = threadIdx.x & 31, c0 = lane & 7, u = (lane >> 3) % kHeads, slice = (lane >> 3) / kHeads;
+    const int per = (p.G + kHeads - 1) / kHeads * p.hkv;  // warps of a token
     const int step = gridDim.x * (kJoinThreads / 32);
     int w = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
     auto entry = [&](int i) {
@@ -371,68 +378,84 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll 1
     for (; w < n; w += step) {
         const Join r = entry(w / per);
-        const int kvh = (w % per) % p.hkv, g0 = (w % per) / p.hkv * kJoinHeads;
-        const int heads = min(kJoinHeads, p.G - g0), all = r.part[0].n + r.part[1].n;
-        const int n0 = r.part[0].n, rows0 = r.part[0].nt * p.G, rows1 = r.part[1].nt * p.G;
-        const int at0 = r.part[0].at * p.G + g0, at1 = r.part[1].at * p.G + g0;
+        const int kvh = (w % per) % p.hkv, g = (w % per) / p.hkv * kHeads + u;
+        const int all = r.part[0].n + r.part[1].n, n0 = r.part[0].n;
+        const int rows0 = r.part[0].nt * p.G, rows1 = r.part[1].nt * p.G;
+        const int at0 = r.part[0].at * p.G + g, at1 = r.part[1].at * p.G + g;
         const long long first0 = (long long)r.part[0].base * p.hq + kvh * rows0, apart0 = (long long)r.part[0].apart * p.hq;
         const long long first1 = (long long)r.part[1].base * p.hq + kvh * rows1, apart1 = (long long)r.part[1].apart * p.hq;
+        const int mine = g < p.G ? all : 0;  // parts that there are for this lane
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
         waited = true;
-        float top[kJoinHeads], sum[kJoinHeads], acc[kJoinHeads][4];
+        float top = -INFINITY, sum = 0.f, acc[16];
 #pragma unroll
-        for (int u = 0; u < kJoinHeads; ++u) {
-            top[u] = -INFINITY;
-            sum[u] = acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
-        }
+        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
         // kAhead parts at a time, their loads together; the sums so far are
         // rescaled when a part's maximum is above theirs
 #pragma unroll 1
-        for (int s0 = 0; s0 < all; s0 += kAhead) {
-            float lse[kAhead][kJoinHeads];
-            float4 v[kAhead][kJoinHeads];
+        for (int s0 = slice; s0 < all; s0 += kAhead * kSlices) {
+            float lse[kAhead], v[kAhead][16];
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
-                const int s = s0 + a;
+                const int s = s0 + a * kSlices;
                 const bool second = s >= n0;
                 const int rows = second ? rows1 : rows0, at = second ? at1 : at0;
                 const long long first = second ? first1 + (s - n0) * apart1 : first0 + s * apart0;
-                const float *o = p.part_o + first * p.D + (lane * rows + at) * 4;
+                const float *o = p.part_o + first * p.D + (c0 * rows + at) * 8;
+                lse[a] = s < mine ? p.part_lse[first + at] : -INFINITY;
 #pragma unroll
-                for (int u = 0; u < kJoinHeads; ++u) {
-                    const bool is = s < all && u < heads;
-                    lse[a][u] = is ? p.part_lse[first + at + u] : -INFINITY;
-                    v[a][u] = is && 4 * lane < p.D ? *(const float4 *)(o + 4 * u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int h = 0; h < 2; ++h) {
+                    if (s < mine && 8 * c0 + 64 * h < p.D) {
+                        ld_global32(v[a] + 8 * h, o + 64 * h * rows);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[a][8 * h + i] = 0.f;
+                    }
                 }
             }
+            float m = top;
 #pragma unroll
-            for (int u = 0; u < kJoinHeads; ++u) {
-                float m = top[u];
+            for (int a = 0; a < kAhead; ++a) m = fmaxf(m, lse[a]);
+            const float base = m == -INFINITY ? 0.f : m, old = exp2f(top - base);
+            top = m;
+            sum *= old;
 #pragma unroll
-                for (int a = 0; a < kAhead; ++a) m = fmaxf(m, lse[a][u]);
-                const float base = m == -INFINITY ? 0.f : m, old = exp2f(top[u] - base);
-                top[u] = m;
-                sum[u] *= old;
-                acc[u][0] *= old; acc[u][1] *= old; acc[u][2] *= old; acc[u][3] *= old;
+            for (int i = 0; i < 16; ++i) acc[i] *= old;
 #pragma unroll
-                for (int a = 0; a < kAhead; ++a) {
-                    // a part without keys weighs nothing; a NaN or infinite score makes its weight NaN
-                    const float x = exp2f(lse[a][u] - base);
-                    if (x == 0.f) continue;
-                    sum[u] += x;
-                    acc[u][0] += x * v[a][u].x; acc[u][1] += x * v[a][u].y;
-                    acc[u][2] += x * v[a][u].z; acc[u][3] += x * v[a][u].w;
-                }
+            for (int a = 0; a < kAhead; ++a) {
+                // a part without keys weighs nothing; a NaN or infinite score makes its weight NaN
+                const float x = exp2f(lse[a] - base);
+                if (x == 0.f) continue;
+                sum += x;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] += x * v[a][i];
             }
         }
 #pragma unroll
-        for (int u = 0; u < kJoinHeads; ++u) {
-            if (u >= heads || 4 * lane >= p.D) continue;
-            const float f = sum[u] == 0.f ? 0.f : 1.f / sum[u];
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[u][0] * f, acc[u][1] * f);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(acc[u][2] * f, acc[u][3] * f);
-            *(uint2 *)(p.out + (long long)r.token * p.ldo + (long long)(kvh * p.G + g0 + u) * p.D + 4 * lane) =
-                make_uint2(*(const uint32_t *)&x, *(const uint32_t *)&y);
+        for (int o = 8 * kHeads; o < 32; o <<= 1) {
+            const float m = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float x = exp2f(top - (m == -INFINITY ? 0.f : m));
+            top = m;
+            sum *= x;
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                acc[i] *= x;
+                acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            }
+        }
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t *out = p.out + (long long)r.token * p.ldo + (long long)(kvh * p.G + g) * p.D + 8 * c0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (slice || g >= p.G || 8 * c0 + 64 * h >= p.D) continue;
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(acc[8 * h + 2 * i] * f, acc[8 * h + 2 * i + 1] * f);
+                x[i] = *(const uint32_t *)&y;
+            }
+            *(uint4 *)(out + 64 * h) = make_uint4(x[0], x[1], x[2], x[3]);
         }
     }
     // a kernel after this one must not start on what the item kernel still writes
@@ -489,8 +512,7 @@ bool caps_ok(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs,
 }
 
 size_t part_bytes(const lora_attn_plan_t &p) {
-    return align16((size_t)p.max_part * p.desc.n_q_heads * p.desc.head_dim * 4) +
-           align16((size_t)p.max_part * p.desc.n_q_heads * 4);
+    return (size_t)p.max_part * p.desc.n_q_heads * (p.desc.head_dim + 1) * 4 + 32;  // the first on 32 bytes
 }
 
 constexpr size_t kWsHead = 256;  // control words at the start of a workspace
@@ -506,6 +528,19 @@ cudaLaunchConfig_t config(int grid, int threads, cudaStream_t s, cudaLaunchAttri
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.stream = s;
     return cfg;
+}
+
+// CTAs of the join with so many heads to a warp, were each warp to take one token.
+long long join_ctas(const attn::Args &a, int heads) {
+    const long long warps = (long long)a.T * ((a.G + heads - 1) / heads * a.hkv);
+    return (warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+}
+
+template <int kHeads, int kAhead>
+cudaError_t join_launch(const JoinArgs &j, long long ctas, int per_sm, cudaStream_t s) {
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = config((int)(ctas < per_sm * attn::kSms ? ctas : per_sm * attn::kSms), kJoinThreads, s, at);
+    return cudaLaunchKernelEx(&cfg, join_kernel<kHeads, kAhead>, j);
 }
 
 lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k, int64_t ldk,
@@ -560,9 +595,8 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     a.ld_table = ld_table;
     a.ld_ptable = ld_ptable;
     a.out = (uint16_t *)out;
-    a.part_o = (float *)((char *)workspace + kWsHead);
-    a.part_lse = (float *)((char *)workspace + kWsHead +
-                           align16((size_t)plan->max_part * d.n_q_heads * d.head_dim * 4));
+    a.part_o = (float *)(((uintptr_t)workspace + kWsHead + 31) & ~(uintptr_t)31);
+    a.part_lse = a.part_o + (size_t)plan->max_part * d.n_q_heads * d.head_dim;
     const Caps c = caps(d, plan->total_q, plan->n_seqs, plan->n_groups);
     const lora_status_t st = lora_attn_launch(a, (int)c.items, s);  // no more units than items
     if (st != LORA_OK) return st;
@@ -580,13 +614,16 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     j.part_lse = a.part_lse;
     j.out = a.out;
     j.ldo = ldo;
-    const long long warps = (long long)plan->total_q * ((a.G + kJoinHeads - 1) / kJoinHeads * d.n_kv_heads);
-    const long long ctas = (warps + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-    // as many CTAs as the registers let be resident: 3 per SM with four parts at a time, 4 with three
-    const bool few = ctas <= 3 * attn::kSms;
-    cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = config((int)(ctas < 4 * attn::kSms ? ctas : 4 * attn::kSms), kJoinThreads, s, at);
-    LORA_CUDA_TRY(few ? cudaLaunchKernelEx(&cfg, join_kernel<4>, j) : cudaLaunchKernelEx(&cfg, join_kernel<3>, j));
+    // One head to a warp while all its warps fit the SMs at once (their registers let two
+    // CTAs be resident), then two, then four: 16 tokens behind a prefix of 8000 20 us against
+    // 28 with four heads, 64 tokens over 4000 keys 17.9 with two against 18.9 with four and
+    // 19.9 with one, 256 tokens behind 8190 86 with four against 98 with one.
+    const long long one = join_ctas(a, 1), two = join_ctas(a, 2), all = join_ctas(a, 4);
+    cudaError_t e;
+    if (one <= 2 * attn::kSms) e = join_launch<1, 8>(j, one, 2, s);
+    else if (two <= 3 * attn::kSms) e = join_launch<2, 4>(j, two, 3, s);
+    else e = join_launch<4, 3>(j, all, 4, s);
+    LORA_CUDA_TRY(e);
     lora_note_launch();
     return LORA_OK;
 }

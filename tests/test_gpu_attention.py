@@ -124,6 +124,21 @@ def test_split_over_keys_and_repeatable():
     b.check()
 
 
+@pytest.mark.parametrize("heads", [(7, 1, 128), (14, 2, 72), (3, 3, 24), (12, 2, 64)])
+@pytest.mark.parametrize("tokens", [3, 100, 300])
+def test_joins_of_few_and_many_tokens(heads, tokens):
+    """Partial results of every batch size, in a workspace that begins on 16 bytes and ends where it says."""
+    b = Batch([1] * (tokens - 2) + [2], [i % 50 for i in range(tokens - 1)], heads=heads, page=16,
+              groups=[0, tokens - 1], prefix_lens=[4500 if tokens == 3 else 900], seed=tokens).upload()
+    whole = torch.full((b.ws_bytes + 16 + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    whole[16:16 + b.ws_bytes] = 0
+    b.ws = whole[16:16 + b.ws_bytes]
+    assert b.ws.data_ptr() % 32 == 16
+    b.run()
+    b.check()
+    assert torch.all(whole[:16] == 0xA5) and torch.all(whole[16 + b.ws_bytes:] == 0xA5)
+
+
 def test_long_prompt():
     b = Batch([1500], [1500], heads=(4, 1, 128), seed=13).upload()
     b.run()
