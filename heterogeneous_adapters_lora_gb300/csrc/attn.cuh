@@ -31,11 +31,14 @@ constexpr int kPairBlock = 18, kPairItem = 20, kOneBlock = 16, kOneItem = 10;
 // Ranges of keys: with the batch's time spread evenly over the SMs, a range of
 // a two-tile item takes at most one SM's share, one of a one-tile item, whose
 // partial results are small, half of it.  None has less than kMinBlocks blocks
-// unless its tile has no more; or kMinPrefixBlocks of a prefix, whose results
-// are joined in any case (4 tokens behind a prefix of 1000: 12.6 us with 4
-// blocks, 11.4 with 3, 10.6 with 2; behind one of 8000 20.0, 18.8, 21.0).
+// unless its tile has no more, a prefix's one less.  But when ranges no longer
+// than kMostFit leave every CTA at most one unit, the shortest such ranges are
+// taken, of kMinOwnBlocks or, for prefixes, whose results are joined in any
+// case, kMinPrefixBlocks at least (a token behind a prefix of 8000: 18.3 us in
+// 21 ranges of 3 blocks, 176 units, 15.7 in 16 of 4; 4 tokens behind one of 1000:
+// 11.4 in ranges of 3, 10.6 of 2; 16 tokens over 4000 keys 14.3 of 4, 13.5 of 3).
 constexpr int kMinBlocks = 4;
-constexpr int kMinPrefixBlocks = 3;
+constexpr int kMostFit = 16, kMinOwnBlocks = 3, kMinPrefixBlocks = 2;
 
 // One item of a plan (8 words).  The items of two row tiles come first, then
 // those of one, each kind longest first.

@@ -107,6 +107,7 @@ __device__ __forceinline__ int find_problem(const int32_t *first, int n, int til
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanArgs p) {
     __shared__ int hist[2][kBuckets];  // items of two tiles, of one
     __shared__ unsigned long long total_time;
+    __shared__ int fit[attn::kMostFit + 1];  // units, were no range longer
     __shared__ int bad;
     const int tid = threadIdx.x;
     const int n = p.n_groups + p.n_seqs;
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         bad = 0;
     }
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = hist[1][i] = 0;
+    if (tid <= attn::kMostFit) fit[tid] = 0;
     __syncthreads();
     // the lengths keep to the rules, or the plan is empty
     for (int b = tid; b < p.n_seqs; b += kPlanThreads) {
@@ -163,6 +165,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const unsigned long long b = tile_blocks(q, j, p.tpi);
         mine += 2 * min(p.tpi, q.n_tok - j * p.tpi) <= p.tpi ? attn::kOneBlock * b + attn::kOneItem
                                                              : attn::kPairBlock * b + attn::kPairItem;
+        if (n_tiles > attn::kSms) continue;
+        for (int r = attn::kMinPrefixBlocks; r <= attn::kMostFit; ++r)
+            atomicAdd(&fit[r], i >= p.n_groups && b <= attn::kMinBlocks ? 1 : max(1, (int)((b + r - 1) / r)));
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -170,9 +175,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __syncthreads();
     const unsigned long long share = total_time * (unsigned long long)p.hkv / attn::kSms;
     const unsigned long long share_pair = share / attn::kPairBlock + 1, share_one = share / (2 * attn::kOneBlock) + 1;
+    int fits = attn::kMinPrefixBlocks;
+    while (fits <= attn::kMostFit && (n_tiles > attn::kSms || fit[fits] * p.hkv > attn::kSms)) ++fits;
     auto range_of = [&](bool prefix, int n_tok) {
-        const unsigned long long least = prefix ? attn::kMinPrefixBlocks : attn::kMinBlocks;
-        return (int)max(least, 2 * n_tok <= p.tpi ? share_one : share_pair);
+        const int least = fits > attn::kMostFit ? attn::kMinBlocks - prefix
+                                                : max(fits, prefix ? attn::kMinPrefixBlocks : attn::kMinOwnBlocks);
+        return (int)max((unsigned long long)least, 2 * n_tok <= p.tpi ? share_one : share_pair);
     };
     // items and partial rows of each tile; the histogram of item lengths
     int n_part = 0;
@@ -198,6 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 ahead = __ldg(p.prefix_len + lo) > 0;
             }
             range = range_of(i < p.n_groups, n_tok);
+            if (i >= p.n_groups && blocks <= attn::kMinBlocks) range = attn::kMinBlocks;
             parts = (blocks + range - 1) / range;
             // no keys: zeros are written, unless a prefix has the tokens' result
             if (parts == 0 && !ahead) parts = 1;
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int i = find_problem(p.first_tile, n, t);
         const Problem q = problem(p, i);
         const int j = t - p.first_tile[i], blocks = tile_blocks(q, j, p.tpi);
-        const int range = range_of(i < p.n_groups, e.w);
+        const int range = e.y == 1 ? max(1, blocks) : range_of(i < p.n_groups, e.w);
         for (int s = 0; s < e.y; ++s) {
             Item it;
             it.blk0 = s * range;
