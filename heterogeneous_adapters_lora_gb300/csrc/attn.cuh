@@ -40,6 +40,14 @@ constexpr int kPairBlock = 18, kPairItem = 20, kOneBlock = 16, kOneItem = 10;
 constexpr int kMinBlocks = 4;
 constexpr int kMostFit = 16, kMinOwnBlocks = 3, kMinPrefixBlocks = 2;
 
+// In batches with prefixes, own keys of a sequence of one token that are no
+// more than this need no item, nearly empty tiles that cost a CTA 4 us a pair:
+// the join takes them as it does partial results, a dependent round of three
+// keys after another (256 tokens behind a prefix of 500: up to 10 own keys 41 us
+// with items, 18 without; up to 60 own keys 41 and 40; of up to 24 or 32 keys it
+// is slower where few tokens have so few, 32 prefixes 111 and 113 against 108).
+constexpr int kShortKeys = 16;
+
 // One item of a plan (8 words).  The items of two row tiles come first, then
 // those of one, each kind longest first.
 struct Item {

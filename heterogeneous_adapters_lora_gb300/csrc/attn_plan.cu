@@ -12,7 +12,8 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;  // of the sort of items by length
 
-// A token with partial results: first those of its own tile, then its prefix's.
+// A token with partial results: first those of its own tile, then its prefix's;
+// or with own keys that no item covers, of sequence part[0].base.
 struct Parts {
     int base, nt;      // first token row of its slot in the first of them, tokens of the slot
     int at;            // which of the slot's tokens it is
@@ -21,7 +22,7 @@ struct Parts {
 struct Join {
     int token;
     Parts part[2];
-    int unused;
+    int keys;
 };
 static_assert(sizeof(Join) == 48, "joins are 12 words");
 
@@ -94,6 +95,11 @@ __device__ __forceinline__ int tile_blocks(const Problem &q, int j, int tpi) {
     return lim <= 0 ? 0 : (int)((lim + attn::kBlock - 1) / attn::kBlock);
 }
 
+// Own keys of a single token that the join takes.
+__device__ __forceinline__ bool is_short(const PlanArgs &p, const Problem &q, int i) {
+    return i >= p.n_groups && p.n_groups && q.n_tok == 1 && q.len <= attn::kShortKeys;
+}
+
 // The problem of a tile: the last one whose first tile is at or before it.
 __device__ __forceinline__ int find_problem(const int32_t *first, int n, int tile) {
     int lo = 0, hi = n - 1;
@@ -162,6 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     for (int t = tid; t < n_tiles; t += kPlanThreads) {
         const int i = find_problem(p.first_tile, n, t), j = t - p.first_tile[i];
         const Problem q = problem(p, i);
+        if (is_short(p, q, i)) continue;
         const unsigned long long b = tile_blocks(q, j, p.tpi);
         mine += 2 * min(p.tpi, q.n_tok - j * p.tpi) <= p.tpi ? attn::kOneBlock * b + attn::kOneItem
                                                              : attn::kPairBlock * b + attn::kPairItem;
@@ -205,11 +212,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
                 }
                 ahead = __ldg(p.prefix_len + lo) > 0;
             }
+            const bool few = is_short(p, q, i);
+            if (few) p.token_tiles[tok0] = -2 - (i - p.n_groups);
             range = range_of(i < p.n_groups, n_tok);
             if (i >= p.n_groups && blocks <= attn::kMinBlocks) range = attn::kMinBlocks;
-            parts = (blocks + range - 1) / range;
+            parts = few ? 0 : (blocks + range - 1) / range;
             // no keys: zeros are written, unless a prefix has the tokens' result
-            if (parts == 0 && !ahead) parts = 1;
+            if (parts == 0 && !ahead && !few) parts = 1;
             joined = parts > 1 || ahead;
             if (joined) rows = parts * n_tok;
         }
@@ -300,29 +309,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         to[2] = both ? from[2] : make_int4(0, 0, 0, 0);
         to[3] = both ? from[3] : make_int4(0, 0, 0, 0);
     }
-    // the tokens with partial results
+    // the tokens with own keys for the join, which can begin with them while the
+    // last items are still computed, then those that have only partial results
     int n_joins = 0;
-    for (int t0 = 0; n_part && t0 < p.T; t0 += kPlanThreads) {
-        const int t = t0 + tid;
-        const int has = t < p.T && (p.token_tiles[t] >= 0 || p.token_tiles[p.max_tokens + t] >= 0);
-        int sum;
-        const int at = block_scan(has, &sum);
-        if (has) {
-            Join r;
-            r.token = t;
-            r.unused = 0;
+    for (int keys = 1; keys >= 0; --keys) {
+        for (int t0 = 0; t0 < p.T && (keys ? p.n_groups : n_part); t0 += kPlanThreads) {
+            const int t = t0 + tid;
+            const int own = t < p.T ? p.token_tiles[t] : -1;
+            const int has = keys ? own < -1 : own >= 0 || (own == -1 && t < p.T && p.token_tiles[p.max_tokens + t] >= 0);
+            int sum;
+            const int at = block_scan(has, &sum);
+            if (has) {
+                Join r;
+                r.token = t;
+                r.keys = 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int tile = p.token_tiles[k * p.max_tokens + t];
-                r.part[k] = {0, 1, 0, 0, 0};
-                if (tile < 0) continue;
-                const int4 e = *(const int4 *)(p.tiles + 4 * (long long)tile);
-                const int i = t - e.z, slot = i / p.tpt;  // slots of tpt tokens, the last one of what is left
-                r.part[k] = {e.x + slot * p.tpt, min(p.tpt, e.w - slot * p.tpt), i - slot * p.tpt, e.w, e.y};
+                for (int k = 0; k < 2; ++k) {
+                    const int tile = p.token_tiles[k * p.max_tokens + t];
+                    r.part[k] = {0, 1, 0, 0, 0};
+                    if (tile < -1) {
+                        r.part[k].base = -2 - tile;
+                        r.keys = __ldg(p.kv_len + r.part[k].base);
+                    }
+                    if (tile < 0) continue;
+                    const int4 e = *(const int4 *)(p.tiles + 4 * (long long)tile);
+                    const int i = t - e.z, slot = i / p.tpt;  // slots of tpt tokens, the last one of what is left
+                    r.part[k] = {e.x + slot * p.tpt, min(p.tpt, e.w - slot * p.tpt), i - slot * p.tpt, e.w, e.y};
+                }
+                p.joins[n_joins + at] = r;
             }
-            p.joins[n_joins + at] = r;
+            n_joins += sum;
         }
-        n_joins += sum;
     }
     if (tid == 0) {
         p.counters[attn::kJoins] = n_joins;
@@ -343,6 +360,13 @@ struct JoinArgs {
     const float *part_o, *part_lse;
     uint16_t *out;
     long long ldo;
+    // for the tokens whose own keys no item covers
+    const uint16_t *q, *k, *v;
+    long long ldq, ldk, ldv, n_rows, ld_table;
+    const int32_t *table;
+    int32_t *status;
+    int page, page_shift;  // page_shift: log2 of the page, -1 if it is no power of two
+    float scale_log2;
 };
 
 constexpr int kJoinThreads = 128;
@@ -352,6 +376,21 @@ __device__ __forceinline__ void ld_global32(float *v, const float *p) {
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "l"(p)
                  : "memory");
+}
+
+// 8 bf16 as floats.
+__device__ __forceinline__ void floats(float *y, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(w[i] << 16);
+        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load16(float *y, const uint16_t *x, const bool (&in)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        floats(y + 8 * h, in[h] ? *(const uint4 *)(x + 64 * h) : make_uint4(0, 0, 0, 0));
 }
 
 // out[t][h] = sum_s 2^lse_s o_s / sum_s 2^lse_s over the partial results of
@@ -364,8 +403,11 @@ __device__ __forceinline__ void ld_global32(float *v, const float *p) {
 // of a call, most of it one read of what other SMs wrote), by L2 with many.
 // With elements of four heads in a lane, 16 bytes each, it read half sectors,
 // a line per lane: 889 tokens of 28 heads in two to three parts 16 us, now 6.
-template <int kHeads, int kAhead>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs p) {
+// Own keys that no item covers are taken like partial results of one key, whose
+// outputs are the rows of V and whose statistics the scores, here a dot product
+// over the eight lanes of a head.
+template <int kHeads, int kAhead, bool kOwn>
+__global__ void __launch_bounds__(kJoinThreads, kHeads == 4 ? 4 : 1) join_kernel(const __grid_constant__ JoinArgs p) {
     constexpr int kSlices = 4 / kHeads;
     // The plan was complete before the item kernel began, which lets this one
     // start: only the partial results are waited for.
@@ -394,11 +436,93 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const long long first0 = (long long)r.part[0].base * p.hq + kvh * rows0, apart0 = (long long)r.part[0].apart * p.hq;
         const long long first1 = (long long)r.part[1].base * p.hq + kvh * rows1, apart1 = (long long)r.part[1].apart * p.hq;
         const int mine = g < p.G ? all : 0;  // parts that there are for this lane
-        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-        waited = true;
         float top = -INFINITY, sum = 0.f, acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+        // to the maximum m: what the sums so far are rescaled by is made theirs
+        auto raise = [&](float m) {
+            const float base = m == -INFINITY ? 0.f : m, old = exp2f(top - base);
+            top = m;
+            sum *= old;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i] *= old;
+            return base;
+        };
+        if (kOwn) {
+            const int keys = r.keys;
+            const long long head = (long long)kvh * p.D + 8 * c0;
+            const bool in[2] = {g < p.G && 8 * c0 < p.D, g < p.G && 8 * c0 + 64 < p.D};
+            float q[16];
+            if (keys) load16(q, p.q + r.token * p.ldq + ((long long)kvh * p.G + g) * p.D + 8 * c0, in);
+#pragma unroll 1
+            for (int key0 = 0; key0 < keys; key0 += 32) {
+                // the rows of 32 keys, a lane's each; -1: outside the cache, zeros
+                long long row = -1;
+                if (key0 + lane < keys) {
+                    const int key = key0 + lane;
+                    const int at = !p.page ? 0 : p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
+                    const long long tab = __ldg(p.table + (long long)r.part[0].base * p.ld_table + at);
+                    row = p.page ? tab * p.page + (key - at * p.page) : tab + key;
+                    if (row < 0 || row >= p.n_rows) {
+                        atomicExch(p.status, (int)LORA_ERR_DEVICE_INDEX);
+                        row = -1;
+                    }
+                }
+                const int end = min(32, keys - key0);
+                if (row >= 0) {  // all of them asked for at once
+                    const uint16_t *kr = p.k + row * p.ldk + (long long)kvh * p.D, *vr = p.v + row * p.ldv + (long long)kvh * p.D;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(kr));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(vr));
+                    if (p.D > 64) {
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(kr + 64));
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(vr + 64));
+                    }
+                }
+#pragma unroll 1
+                for (int i0 = 0; i0 < end; i0 += kAhead * kSlices) {
+                    uint4 k[kAhead][2], v[kAhead][2];
+                    float score[kAhead];
+#pragma unroll
+                    for (int a = 0; a < kAhead; ++a) {
+                        const int i = i0 + a * kSlices + slice;
+                        const int x = __shfl_sync(0xffffffffu, (int)row, i & 31);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const bool is = in[h] && i < end && x >= 0;
+                            k[a][h] = is ? *(const uint4 *)(p.k + x * p.ldk + head + 64 * h) : make_uint4(0, 0, 0, 0);
+                            v[a][h] = is ? *(const uint4 *)(p.v + x * p.ldv + head + 64 * h) : make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    float m = top;
+#pragma unroll
+                    for (int a = 0; a < kAhead; ++a) {
+                        float y[16], d = 0.f;
+                        floats(y, k[a][0]);
+                        floats(y + 8, k[a][1]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) d += q[i] * y[i];
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                        score[a] = i0 + a * kSlices + slice < end ? d * p.scale_log2 : -INFINITY;
+                        m = fmaxf(m, score[a]);
+                    }
+                    const float base = raise(m);
+#pragma unroll
+                    for (int a = 0; a < kAhead; ++a) {
+                        const float x = exp2f(score[a] - base);
+                        if (x == 0.f) continue;
+                        float y[16];
+                        floats(y, v[a][0]);
+                        floats(y + 8, v[a][1]);
+                        sum += x;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[i] += x * y[i];
+                    }
+                }
+            }
+        }
+        if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
         // kAhead parts at a time, their loads together; the sums so far are
         // rescaled when a part's maximum is above theirs
 #pragma unroll 1
@@ -425,11 +549,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             float m = top;
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) m = fmaxf(m, lse[a]);
-            const float base = m == -INFINITY ? 0.f : m, old = exp2f(top - base);
-            top = m;
-            sum *= old;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] *= old;
+            const float base = raise(m);
 #pragma unroll
             for (int a = 0; a < kAhead; ++a) {
                 // a part without keys weighs nothing; a NaN or infinite score makes its weight NaN
@@ -546,10 +666,11 @@ long long join_ctas(const attn::Args &a, int heads) {
 }
 
 template <int kHeads, int kAhead>
-cudaError_t join_launch(const JoinArgs &j, long long ctas, int per_sm, cudaStream_t s) {
+cudaError_t join_launch(const JoinArgs &j, bool own, long long ctas, int per_sm, cudaStream_t s) {
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = config((int)(ctas < per_sm * attn::kSms ? ctas : per_sm * attn::kSms), kJoinThreads, s, at);
-    return cudaLaunchKernelEx(&cfg, join_kernel<kHeads, kAhead>, j);
+    return own ? cudaLaunchKernelEx(&cfg, join_kernel<kHeads, kAhead, true>, j)
+               : cudaLaunchKernelEx(&cfg, join_kernel<kHeads, kAhead, false>, j);
 }
 
 lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq, const void *k, int64_t ldk,
@@ -623,15 +744,31 @@ lora_status_t attention(const lora_attn_plan_t *plan, const void *q, int64_t ldq
     j.part_lse = a.part_lse;
     j.out = a.out;
     j.ldo = ldo;
+    j.q = a.q;
+    j.k = a.k;
+    j.v = a.v;
+    j.ldq = ldq;
+    j.ldk = ldk;
+    j.ldv = ldv;
+    j.n_rows = n_rows;
+    j.table = table;
+    j.ld_table = ld_table;
+    j.status = a.status;
+    j.page = d.page_size;
+    for (j.page_shift = 0; j.page_shift < 31 && 1 << j.page_shift < d.page_size;) ++j.page_shift;
+    if (1 << j.page_shift != d.page_size) j.page_shift = -1;
+    j.scale_log2 = a.scale_log2;
     // One head to a warp while all its warps fit the SMs at once (their registers let two
-    // CTAs be resident), then two, then four: 16 tokens behind a prefix of 8000 20 us against
-    // 28 with four heads, 64 tokens over 4000 keys 17.9 with two against 18.9 with four and
-    // 19.9 with one, 256 tokens behind 8190 86 with four against 98 with one.
+    // CTAs be resident) or where no heads share keys, then two, then four: 16 tokens behind a
+    // prefix of 8000 20 us against 28 with four heads, 64 tokens over 4000 keys 17.9 with two
+    // against 18.9 with four and 19.9 with one, 256 tokens behind 8190 86 with four against 98
+    // with one; 240 tokens of 16 heads of their own 67 with one against 75 with four.
     const long long one = join_ctas(a, 1), two = join_ctas(a, 2), all = join_ctas(a, 4);
     cudaError_t e;
-    if (one <= 2 * attn::kSms) e = join_launch<1, 8>(j, one, 2, s);
-    else if (two <= 3 * attn::kSms) e = join_launch<2, 4>(j, two, 3, s);
-    else e = join_launch<4, 3>(j, all, 4, s);
+    if (one <= 2 * attn::kSms) e = join_launch<1, 8>(j, prefix, one, 2, s);
+    else if (a.G == 1) e = join_launch<1, 4>(j, prefix, one, 3, s);
+    else if (two <= 3 * attn::kSms) e = join_launch<2, 4>(j, prefix, two, 3, s);
+    else e = join_launch<4, 3>(j, prefix, all, 4, s);
     LORA_CUDA_TRY(e);
     lora_note_launch();
     return LORA_OK;

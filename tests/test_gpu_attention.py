@@ -124,7 +124,7 @@ def test_split_over_keys_and_repeatable():
     b.check()
 
 
-@pytest.mark.parametrize("heads", [(7, 1, 128), (14, 2, 72), (3, 3, 24), (12, 2, 64)])
+@pytest.mark.parametrize("heads", [(7, 1, 128), (14, 2, 72), (3, 3, 24), (12, 2, 64), (8, 8, 64)])
 @pytest.mark.parametrize("tokens", [3, 100, 300])
 def test_joins_of_few_and_many_tokens(heads, tokens):
     """Partial results of every batch size, in a workspace that begins on 16 bytes and ends where it says."""
@@ -250,6 +250,35 @@ def test_table_entries_outside_the_cache(page, wild):
     ref0, mag0 = z.reference()
     assert torch.all((got[0] - ref0[0]).abs() <= 2.0 ** -7 * mag0[0] + 2.0 ** -8 * ref0[0].abs() + 1e-30)
     assert torch.all((got[1] - ref[0][1]).abs() <= 2.0 ** -7 * ref[1][1] + 2.0 ** -8 * ref[0][1].abs())
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("wild", [-5, 1 << 30, 2147483647, -2147483648])
+def test_own_keys_outside_the_cache(page, wild):
+    """The same for the few own keys of single tokens behind a prefix: the first sequence's all lie outside."""
+    kw = dict(heads=(4, 2, 64), page=page, groups=[0, 2], prefix_lens=[30], seed=22, poison=0.5)
+    b = Batch([1, 1], [9, 9], **kw).upload()
+    ref = b.reference()
+    b.dtable[0, 0] = wild if page or wild > 0 else -40
+    b.run()
+    assert L.lora_attn_get_status(b.plan) == L.CODE["LORA_ERR_DEVICE_INDEX"]
+    got = b.out.float().cpu().double().view(2, 4, 64)
+    z = Batch([1, 1], [9, 9], **kw)
+    z.k[z.place[0]], z.v[z.place[0]] = 0, 0
+    ref0, mag0 = z.reference()
+    assert torch.all((got[0] - ref0[0]).abs() <= 2.0 ** -7 * mag0[0] + 2.0 ** -8 * ref0[0].abs() + 1e-30)
+    assert torch.all((got[1] - ref[0][1]).abs() <= 2.0 ** -7 * ref[1][1] + 2.0 ** -8 * ref[0][1].abs())
+
+
+@pytest.mark.parametrize("page", [0, 24, 64])
+@pytest.mark.parametrize("heads", [(5, 1, 128), (8, 8, 64), (14, 2, 40), (2, 1, 8)])
+@pytest.mark.parametrize("tokens", [5, 400])
+def test_single_tokens_with_few_own_keys(tokens, heads, page):
+    """Lengths around the number of own keys that need no item, with and without a prefix before them."""
+    own = [(0, 1, 2, 7, 8, 15, 16, 17, 18, 31, 33)[i % 11] for i in range(tokens - 1)]
+    b = go([1] * (tokens - 2) + [3, 1], own[:-1] + [3, 16], heads=heads, page=page,
+           groups=[0, tokens // 2, tokens // 2, tokens], prefix_lens=[0, 5, 40], seed=tokens, q_pad=8, kv_pad=16, out_pad=8)
+    assert torch.all(b.out[0, :heads[0] * heads[2]] == 0)  # no key at all
 
 
 def refused(code, f):
