@@ -492,7 +492,8 @@ typedef struct {
  *                        longest first
  *   tiles[max_tiles][4]  tiles of queries and where their partial results lie
  *   token_tiles[2][max_tokens]  each token's own tile and prefix tile (-1: none
- *                        that has to be joined)
+ *                        that has to be joined, -2 - b: own keys of sequence b
+ *                        without an item)
  *   joins[max_tokens][12] the tokens that have partial results, and where those lie,
  *                         or a few own keys that no item covers
  *   counters[8]          items, partial token rows, tiles, status word, units, joins
