@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const long long x = p.a.page ? (long long)tab * p.a.page + in : (long long)tab + in;
                 if (x < 0 || x + min(p.box_rows, k.kv_len - key) > p.a.n_rows) {
                     atomicExch(status, (int)LORA_ERR_DEVICE_INDEX);
-                    if (x < -(long long)p.box_rows || x > p.a.n_rows) return oob;
+                    // a cache of no rows has none to read (its maps have one, as maps need)
+                    if (!p.a.n_rows || x < -(long long)p.box_rows || x > p.a.n_rows) return oob;
                 }
                 return (int)x;
             };
