@@ -629,6 +629,7 @@ extern "C" int32_t lora_last_cuda_error(void) { return g_last_cuda_error.load(st
 extern "C" void lora_set_kernel_policy(int32_t policy) { g_lora_kernel_policy = policy; }
 
 extern "C" void lora_set_spin_limit(int32_t max_polls) { g_spin_limit = max_polls; }
+int lora_spin_limit() { return g_spin_limit; }
 
 bool lora_ws_data(void *workspace, size_t ws_bytes, char **data, size_t *data_bytes) {
     Carve cv;

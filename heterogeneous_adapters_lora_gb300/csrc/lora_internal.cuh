@@ -147,6 +147,7 @@ void lora_note_launch();
 // kernel only; 2 = cluster kernel preferred; 3 = automatic without the fused
 // decode kernel).
 extern int g_lora_kernel_policy;
+int lora_spin_limit();  // as lora_set_spin_limit left it
 
 // 2D bf16 tensor map over rows x cols (row stride in elements), optional
 // 128-byte swizzle (sgmv.cu).

@@ -32,7 +32,7 @@ constexpr int kRowThreads = 128;
 constexpr int kRowStages = 3;
 constexpr int kRowSmem = 224 * 1024;  // of an SM, for row buffers
 constexpr int kRowCtas = 8;           // per SM at most
-constexpr int kRowPolls = 1 << 25;
+constexpr int kRowLand = 1 << 12;     // polls (about 1.5 us each) for a copy in flight to land
 
 __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(tc::smem_u32(src)),
@@ -56,6 +56,7 @@ struct RopeArgs {
     int lw_log;  // log2 of the lanes of a group
     int chunks;  // head chunks of a token
     int row_bytes;  // of a row buffer
+    int spin_limit;
 };
 
 // A lane's piece of V elements (4 or 8) as it lies in memory.
@@ -279,8 +280,9 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
     int t = blockIdx.x;
     places(t);
     angles<V>(p, in_tables(p, npos, nslot) ? npos : 0, l, rotated, nco, nsi);
-    bool ok = true;
-    for (int i = 0; t < p.T; ++i, t += step) {
+    int i = 0;
+    bool gave_up = false;
+    for (; t < p.T; ++i, t += step) {
         const int st = i % kRowStages;
         pos = npos;
         slot = nslot;
@@ -293,8 +295,9 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
         places(t + step);
         const bool good = in_tables(p, pos, slot);
         if (!good && threadIdx.x == 0 && p.status) atomicExch(p.status, (int)LORA_ERR_DEVICE_INDEX);
-        ok = tc::mbar_wait(&full[st], (uint32_t)((i / kRowStages) & 1), kRowPolls);
-        if (__syncthreads_or(!ok)) {
+        const bool ok = tc::mbar_wait(&full[st], (uint32_t)((i / kRowStages) & 1), p.spin_limit);
+        gave_up = __syncthreads_or(!ok);
+        if (gave_up) {
             if (threadIdx.x == 0 && p.status) atomicExch(p.status, (int)LORA_ERR_TIMEOUT);
             break;
         }
@@ -339,8 +342,10 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
         }
     }
     if (threadIdx.x == 0) {
-        // after a wait that gave up the other copies are given time to land
-        for (int st = 0; !ok && st < kRowStages; ++st) tc::mbar_wait(&full[st], 0, 1 << 12);
+        // after a wait that gave up, this token's row and the one fetched ahead of it
+        // land before the CTA ends, each waited for in its own phase
+        for (int j = i; gave_up && j < i + kRowStages - 1 && t < p.T; ++j, t += step)
+            tc::mbar_wait(&full[j % kRowStages], (uint32_t)((j / kRowStages) & 1), kRowLand);
         tc::bulk_wait0();
     }
 }
@@ -431,6 +436,7 @@ extern "C" lora_status_t lora_qk_norm_rope(const lora_rope_desc_t *desc, const v
     p.slots = slots;
     p.n_rows = n_rows;
     p.status = status;
+    p.spin_limit = lora_spin_limit();
     if ((long long)T * p.heads > 0x7fffffffLL) return LORA_ERR_INVALID_ARG;
     int dev = 0;
     LORA_CUDA_TRY(cudaGetDevice(&dev));
