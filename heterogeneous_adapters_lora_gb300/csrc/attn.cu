@@ -46,7 +46,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kChunkBytes = attn::kBlock * 128;  // 128 rows of 64 bf16
-constexpr int kMaxPolls = 1 << 25;               // of a wait (seconds)
+constexpr int kLand = 1 << 13;                   // polls (about 1.5 us each) for what is in flight to end
 constexpr float kLag = 8.f;                      // the maximum in use may lag by 2^8
 constexpr float kExactBase = 1048576.f;          // up to here the rounding of the maximum is small against 1
 
@@ -58,6 +58,7 @@ struct KArgs {
     int tpt;       // tokens of a slot's tile
     int q_bytes;   // bytes of a Q tile's copies
     int out32;     // output rows of a head begin on 32-byte boundaries, in pieces of 32
+    int spin_limit;
 };
 
 // A slot's part of a unit.
@@ -84,7 +85,7 @@ struct Bars {
     uint64_t work_full[kWorks], work_empty[kWorks];
     Work work[kWorks];
     uint32_t tmem;
-    int abort;
+    int abort, spin_limit;  // next to each other: a wait that lasts reads both
 };
 
 template <int NCH>
@@ -98,11 +99,12 @@ struct Shape {
 
 // Bounded wait; false when it gave up here or somewhere else in the CTA.
 // The lanes of a warp may differ: callers vote before they leave a loop.
+// abort points at a Bars' abort and spin_limit.
 __device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status) {
 #pragma unroll 1
     for (int polls = 0; !tc::mbar_try_wait(bar, parity); ++polls) {
         if ((polls & 1023) == 0 && *abort) return false;
-        if (polls > kMaxPolls) {
+        if (polls > abort[1]) {
             *abort = 1;
             atomicExch(status, (int)LORA_ERR_TIMEOUT);
             return false;
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
             tc::mbar_init(&bars->turn[i], 1);
         }
         bars->abort = 0;
+        bars->spin_limit = p.spin_limit;
         for (int i = 0; i < kWorks; ++i) {
             tc::mbar_init(&bars->work_full[i], 1);
             tc::mbar_init(&bars->work_empty[i], kThreads / 32 - 1);
@@ -362,7 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 return (int)x;
             };
             auto load = [&](const CUtensorMap *map, int kvh, int row) {
+                // After a wait somewhere in the CTA gave up no more copies are issued, also where
+                // stages still come back: the other warp's half of one, or the bytes that it is
+                // to expect, may be missing, and a barrier counts bytes only so far.
+                const int gone = *(volatile int *)&bars->abort;
                 ok &= wait(&bars->kv_empty[st], par, bars, status);  // at once for a stage's first fill
+                ok &= !gone;
                 if (ok) {
                     if (!half && lane == 0) tc::mbar_expect_tx(&bars->kv_full[st], Sh::kStage);
                     if (mine)
@@ -464,13 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 const int last = fill - 1 - ((fill - 1 - s) % kNS);
                 int polls = 0;
 #pragma unroll 1
-                while (!tc::mbar_try_wait(&bars->kv_full[s], (uint32_t)((last / kNS) & 1)) && ++polls < (1 << 16)) {}
+                while (!tc::mbar_try_wait(&bars->kv_full[s], (uint32_t)((last / kNS) & 1)) && ++polls < kLand) {}
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 int polls = 0;
 #pragma unroll 1
-                while (nq[s] && !tc::mbar_try_wait(&bars->q_full[s], (uint32_t)((nq[s] - 1) & 1)) && ++polls < (1 << 16)) {}
+                while (nq[s] && !tc::mbar_try_wait(&bars->q_full[s], (uint32_t)((nq[s] - 1) & 1)) && ++polls < kLand) {}
             }
         } else {
             // ---- MMA issue of one slot
@@ -593,12 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1) item_kernel(const __grid_constant
                 ok = all(ok);
                 done_work();
             }
-            // all products are done before tensor memory is given back
-            if (lane == 0) tc::mma_commit(&bars->fin[s]);
+            // all products are done before tensor memory is given back, also those of a unit
+            // that was given up (a commit counts the products of the lane that issues it)
+            if (elect_one()) tc::mma_commit(&bars->fin[s]);
             __syncwarp();
             int polls = 0;
 #pragma unroll 1
-            while (!tc::mbar_try_wait(&bars->fin[s], 0) && ++polls < (1 << 20)) {}
+            while (!tc::mbar_try_wait(&bars->fin[s], 0) && ++polls < kLand) {}
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -822,6 +831,7 @@ lora_status_t lora_attn_launch(const attn::Args &a, int max_items, cudaStream_t 
     KArgs p;
     memset(&p, 0, sizeof(p));
     p.a = a;
+    p.spin_limit = lora_spin_limit();
     p.tpt = attn::tile_tokens(a.G);
     p.box_rows = attn::kBlock;
     if (a.page)

@@ -383,11 +383,15 @@ LORA_API lora_status_t lora_get_device_status(const lora_pool_t *pool, void *str
 
 /* Bound on the polls of every cross-CTA wait of lora_apply_slices and
  * lora_moe_apply (default 1 << 20, each poll sleeps up to ~64 ns), and of the
- * waits for copies of lora_qk_norm_rope (each poll up to ~1.5 us).  When a wait
- * gives up, the device status (of lora_qk_norm_rope: its status word) becomes
- * LORA_ERR_TIMEOUT and that work item is skipped (of lora_qk_norm_rope: the
- * tokens that the CTA has left, of which nothing is written).  A negative value makes every wait that is not already satisfied
- * give up at once (to exercise the error path).  Process-wide. */
+ * waits for copies of lora_qk_norm_rope and those of the attention calls (each
+ * poll up to ~1.5 us).  When a wait gives up, the device status (of
+ * lora_qk_norm_rope: its status word; of the attention calls: the plan's)
+ * becomes LORA_ERR_TIMEOUT and that work item is skipped (of lora_qk_norm_rope:
+ * the tokens that the CTA has left, of which nothing is written; of the
+ * attention calls: the output is not to be used, the next call is whole).  A
+ * negative value makes every wait that is not already satisfied give up at once
+ * (to exercise the error path; of the last three calls, one that is not within a
+ * poll or two).  Process-wide. */
 LORA_API void lora_set_spin_limit(int32_t max_polls);
 
 /* The full LoRA linear layer of a dense pool (vLLM LoRA layer pages,
