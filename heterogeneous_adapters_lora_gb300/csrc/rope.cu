@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_con
         places(t + step);
         const bool good = in_tables(p, pos, slot);
         if (!good && threadIdx.x == 0 && p.status) atomicExch(p.status, (int)LORA_ERR_DEVICE_INDEX);
-        const bool ok = tc::mbar_wait(&full[st], (uint32_t)((i / kRowStages) & 1), p.spin_limit);
+        const uint32_t parity = (uint32_t)((i / kRowStages) & 1);
+        const bool ok = p.spin_limit < 0 ? tc::mbar_test_wait(&full[st], parity)
+                                         : tc::mbar_wait(&full[st], parity, p.spin_limit);
         gave_up = __syncthreads_or(!ok);
         if (gave_up) {
             if (threadIdx.x == 0 && p.status) atomicExch(p.status, (int)LORA_ERR_TIMEOUT);

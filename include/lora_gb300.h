@@ -390,7 +390,7 @@ LORA_API lora_status_t lora_get_device_status(const lora_pool_t *pool, void *str
  * the tokens that the CTA has left, of which nothing is written; of the
  * attention calls: the output is not to be used, the next call is whole).  A
  * negative value makes every wait that is not already satisfied give up at once
- * (to exercise the error path; of the last three calls, one that is not within a
+ * (to exercise the error path; of the attention calls, one that is not within a
  * poll or two).  Process-wide. */
 LORA_API void lora_set_spin_limit(int32_t max_polls);
 

@@ -33,3 +33,25 @@ def test_waits_that_give_up(limit, heads):
     status.zero_()
     c.run(status).check()
     assert int(status) == 0
+
+
+def test_waits_that_give_up_at_once():
+    """With no poll at all some rows are not there yet when their CTA asks for them."""
+    c = Case(4000, heads=(32, 8, 128), max_pos=500, seed=13)
+    want = c.run().q.clone()
+    c.check()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    times = 0
+    for _ in range(10):
+        status.zero_()
+        L.lora_set_spin_limit(-1)
+        try:
+            c.run(status)
+        finally:
+            L.lora_set_spin_limit(1 << 20)
+        kept = torch.all(c.q == 7.0, 1)
+        assert int(status) == (L.CODE["LORA_ERR_TIMEOUT"] if kept.any() else 0)
+        assert torch.equal(c.q[~kept], want[~kept])
+        times += bool(kept.any())
+        assert torch.equal(c.run().q, want)
+    assert times
