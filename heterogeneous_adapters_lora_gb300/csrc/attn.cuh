@@ -60,8 +60,8 @@ struct Item {
 };
 static_assert(sizeof(Item) == 32, "plan items are 8 words");
 
-// counters[] of a plan
-enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4, kJoins = 5 };
+// counters[] of a plan; at kBinding (8 bytes) the binding that the status word belongs to
+enum { kItems = 0, kPartTokens = 1, kTiles = 2, kStatus = 3, kUnits = 4, kJoins = 5, kBinding = 6 };
 
 // A unit is what a CTA works on at a time, for one key/value head: an item of
 // two row tiles, or one or two items of one tile.  Units come the longest

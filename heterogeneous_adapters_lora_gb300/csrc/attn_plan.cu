@@ -3,6 +3,9 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+#include <chrono>
+
 #include "attn.cuh"
 
 using attn::Item;
@@ -36,6 +39,7 @@ struct PlanArgs {
     int32_t *tiles, *token_tiles, *first_tile, *counters;
     Join *joins;
     int max_tokens;
+    unsigned long long binding;
 };
 
 struct Problem {
@@ -122,6 +126,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (tid == 0) {
         total_time = 0;
         bad = 0;
+        // The status word stays as calls left it until it is read.  Only the first build of a
+        // binding clears it, also when a captured build is replayed.
+        unsigned long long *binding = (unsigned long long *)(p.counters + attn::kBinding);
+        if (*binding != p.binding) {
+            *binding = p.binding;
+            p.counters[attn::kStatus] = LORA_OK;
+        }
     }
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = hist[1][i] = 0;
     if (tid <= attn::kMostFit) fit[tid] = 0;
@@ -145,7 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (tid == 0) {
             p.counters[attn::kItems] = p.counters[attn::kUnits] = 0;
             p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = p.counters[attn::kJoins] = 0;
-            p.counters[attn::kStatus] = LORA_ERR_DEVICE_INDEX;
+            atomicExch(p.counters + attn::kStatus, (int)LORA_ERR_DEVICE_INDEX);
         }
         return;
     }
@@ -347,7 +358,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         p.counters[attn::kUnits] = n_units;
         p.counters[attn::kPartTokens] = n_part;
         p.counters[attn::kTiles] = n_tiles;
-        p.counters[attn::kStatus] = LORA_OK;
     }
 }
 
@@ -625,6 +635,15 @@ Caps caps(const lora_attn_desc_t &d, long long tokens, long long seqs, long long
     return c;
 }
 
+// A number for each binding of a plan, which memory that another one left does not hold by
+// chance: the time of the first binding, spread over 64 bits by an odd factor, and a count.
+uint64_t next_binding() {
+    static const uint64_t first =
+        (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() * 0x9e3779b97f4a7c15ull;
+    static std::atomic<uint64_t> n{0};
+    return first + n.fetch_add(1, std::memory_order_relaxed);
+}
+
 size_t align16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long groups) {
@@ -798,6 +817,7 @@ extern "C" lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_
     plan->max_tiles = (int32_t)c.tiles;
     plan->max_part = (int32_t)c.part;
     plan->n_seqs = plan->total_q = -1;  // nothing built yet
+    plan->binding = next_binding();
     char *at = (char *)d_buf;
     plan->counters = (int32_t *)at;
     at += 32;
@@ -852,6 +872,7 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
     p.first_tile = plan->first_tile;
     p.counters = plan->counters;
     p.max_tokens = plan->max_tokens;
+    p.binding = plan->binding;
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = config(1, kPlanThreads, (cudaStream_t)stream, at);
     LORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, plan_kernel, p));
@@ -889,9 +910,14 @@ extern "C" lora_status_t lora_prefix_attention(const lora_attn_plan_t *plan, con
 extern "C" lora_status_t lora_attn_get_status(const lora_attn_plan_t *plan, void *stream) {
     if (!plan || !plan->counters) return LORA_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
-    int32_t v = 0;
-    LORA_CUDA_TRY(cudaMemcpyAsync(&v, plan->counters + attn::kStatus, 4, cudaMemcpyDeviceToHost, s));
+    int32_t c[8];
+    LORA_CUDA_TRY(cudaMemcpyAsync(c, plan->counters, sizeof(c), cudaMemcpyDeviceToHost, s));
+    LORA_CUDA_TRY(cudaStreamSynchronize(s));
+    uint64_t binding;
+    memcpy(&binding, c + attn::kBinding, sizeof(binding));
+    // memory that no build of this binding has reached yet says nothing
+    if (binding != plan->binding || c[attn::kStatus] == LORA_OK) return LORA_OK;
     LORA_CUDA_TRY(cudaMemsetAsync(plan->counters + attn::kStatus, 0, 4, s));
     LORA_CUDA_TRY(cudaStreamSynchronize(s));
-    return (lora_status_t)v;
+    return (lora_status_t)c[attn::kStatus];
 }

@@ -65,7 +65,7 @@ class AttnPlan(ctypes.Structure):
                 ("max_items", c_i32), ("max_tiles", c_i32), ("max_part", c_i32), ("n_seqs", c_i32),
                 ("total_q", c_i32), ("n_groups", c_i32), ("max_kv_len", c_i32), ("max_prefix_len", c_i32),
                 ("items", c_vp), ("units", c_vp), ("tiles", c_vp), ("token_tiles", c_vp), ("joins", c_vp),
-                ("first_tile", c_vp), ("counters", c_vp)]
+                ("first_tile", c_vp), ("counters", c_vp), ("binding", ctypes.c_uint64)]
 
 
 class LoraError(RuntimeError):

@@ -19,10 +19,10 @@
  *
  * Conventions common to every entry point
  *  - Every call is asynchronous on `stream` (a cudaStream_t, NULL = the legacy
- *    default stream).  Only lora_get_device_status and lora_pool_destroy
- *    synchronise.  Calls that take only device pointers launch kernels and
- *    cudaMemsetAsync/cudaMemcpyAsync only, so they can be captured in a CUDA
- *    graph.
+ *    default stream).  Only lora_get_device_status, lora_attn_get_status and
+ *    lora_pool_destroy synchronise.  Calls that take only device pointers launch
+ *    kernels and cudaMemsetAsync/cudaMemcpyAsync only, so they can be captured in
+ *    a CUDA graph.
  *  - bf16 tensors are passed as `void *` (2-byte elements, row-major).  All
  *    device tensors given to compute calls must be 16-byte aligned and their
  *    leading dimensions (in elements) multiples of 8.
@@ -30,7 +30,8 @@
  *    No call throws, traps or asserts on the device.  Bad adapter indices seen
  *    on the device set the pool's status word (LORA_ERR_DEVICE_INDEX) and the
  *    row is treated as idx -1; a cross-CTA wait that runs out of iterations
- *    sets LORA_ERR_TIMEOUT.  Read and clear it with lora_get_device_status.
+ *    sets LORA_ERR_TIMEOUT.  Read and clear it with lora_get_device_status (an
+ *    attention plan has a word of its own: lora_attn_get_status).
  *  - A row is *active* when 0 <= idx < max_loras, the slot is enabled and its
  *    rank is > 0 (and, for MoE, its expert id is in range).  Inactive rows of
  *    y / ic1 / ic3 are left bit-identical.
@@ -502,7 +503,8 @@ typedef struct {
  *                        without an item)
  *   joins[max_tokens][12] the tokens that have partial results, and where those lie,
  *                         or a few own keys that no item covers
- *   counters[8]          items, partial token rows, tiles, status word, units, joins
+ *   counters[8]          items, partial token rows, tiles, status word, units, joins,
+ *                        the binding that the status word belongs to (8 bytes)
  * The host fields n_seqs .. max_prefix_len record the last build. */
 typedef struct {
     lora_attn_desc_t desc;
@@ -515,6 +517,7 @@ typedef struct {
     int32_t *joins;
     int32_t *first_tile;
     int32_t *counters;
+    uint64_t binding;  /* a number of its own for each lora_attn_plan_bind */
 } lora_attn_plan_t;
 
 /* Device bytes lora_attn_plan_bind needs (0 if the descriptor or a capacity
@@ -536,7 +539,8 @@ LORA_API lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_at
  * (d_group_start [n_groups + 1] int32, from 0 to n_seqs), which share
  * prefix_len[g] keys (d_prefix_len [n_groups] int32, 0..max_prefix_len) ahead
  * of their own.  Lengths that break these rules make an empty plan (calls with
- * it write nothing) and set the plan's status to LORA_ERR_DEVICE_INDEX.
+ * it write nothing) and set the plan's status to LORA_ERR_DEVICE_INDEX.  A
+ * build clears no status: what earlier steps set stays until it is read.
  * max_kv_len and max_prefix_len are at most 2^30.
  * Errors: LORA_ERR_INVALID_ARG, LORA_ERR_CAPACITY. */
 LORA_API lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_seqs, int32_t total_q,
@@ -590,7 +594,8 @@ LORA_API lora_status_t lora_prefix_attention(const lora_attn_plan_t *plan, const
                                              size_t ws_bytes, void *stream);
 
 /* Synchronise `stream`, return the plan's status word (LORA_OK,
- * LORA_ERR_DEVICE_INDEX or LORA_ERR_TIMEOUT) and clear it. */
+ * LORA_ERR_DEVICE_INDEX or LORA_ERR_TIMEOUT) and clear it.  It holds the last
+ * error of all builds and calls since it was read, or since the plan was bound. */
 LORA_API lora_status_t lora_attn_get_status(const lora_attn_plan_t *plan, void *stream);
 
 /* Kernel selection for lora_apply_slices / lora_moe_apply (process-wide):
