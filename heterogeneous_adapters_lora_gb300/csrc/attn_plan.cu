@@ -652,7 +652,7 @@ size_t plan_bytes(const Caps &c, long long tokens, long long seqs, long long gro
 }
 
 bool caps_ok(const lora_attn_desc_t *desc, int32_t max_tokens, int32_t max_seqs, int32_t max_groups, Caps *c) {
-    if (!desc || !desc_ok(*desc) || max_tokens < 1 || max_seqs < 1 || max_groups < 0 || max_groups > max_seqs)
+    if (!desc || !desc_ok(*desc) || max_tokens < 1 || max_seqs < 1 || max_groups < 0)
         return false;
     *c = caps(*desc, max_tokens, max_seqs, max_groups);
     return c->items * desc->n_kv_heads <= 0x7fffffffLL && (long long)max_tokens * desc->n_q_heads <= 0x3fffffffLL &&
@@ -841,7 +841,7 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
                                               int32_t max_kv_len, int32_t max_prefix_len, void *stream) {
     if (!plan || !plan->counters || n_seqs < 0 || total_q < 0 || n_groups < 0 || max_kv_len < 0 ||
         max_prefix_len < 0 || max_kv_len > attn::kMostKeys || max_prefix_len > attn::kMostKeys ||
-        (n_groups > 0 && n_seqs == 0) || (n_seqs == 0 && total_q > 0))
+        (n_seqs == 0 && total_q > 0))
         return LORA_ERR_INVALID_ARG;
     if (n_seqs > plan->max_seqs || total_q > plan->max_tokens || n_groups > plan->max_groups) return LORA_ERR_CAPACITY;
     if (n_seqs > 0 && (!d_cu_q || !d_kv_len || ((uintptr_t)d_cu_q & 3) || ((uintptr_t)d_kv_len & 3)))
@@ -856,7 +856,7 @@ extern "C" lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_
     p.group_start = d_group_start;
     p.prefix_len = d_prefix_len;
     p.n_seqs = n_seqs;
-    p.n_groups = n_groups;
+    p.n_groups = n_seqs ? n_groups : 0;  // groups of no sequences at all: no lengths to read
     p.T = total_q;
     p.max_kv = max_kv_len;
     p.max_prefix = max_prefix_len;

@@ -538,7 +538,7 @@ LORA_API lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_at
  * is the sequences group_start[g] .. group_start[g+1] - 1
  * (d_group_start [n_groups + 1] int32, from 0 to n_seqs), which share
  * prefix_len[g] keys (d_prefix_len [n_groups] int32, 0..max_prefix_len) ahead
- * of their own.  Lengths that break these rules make an empty plan (calls with
+ * of their own; a group may have no sequences.  Lengths that break these rules make an empty plan (calls with
  * it write nothing) and set the plan's status to LORA_ERR_DEVICE_INDEX.  A
  * build clears no status: what earlier steps set stays until it is read.
  * max_kv_len and max_prefix_len are at most 2^30.
