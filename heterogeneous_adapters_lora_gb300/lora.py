@@ -163,17 +163,16 @@ def _check(code, where):
 
 def ptr(obj):
     """Raw address of a torch tensor, numpy array, int or None."""
-    if obj is None:
-        return None
+    if obj is None or isinstance(obj, int):
+        return obj
     try:
         return obj.data_ptr()
     except AttributeError:
         pass
-    if isinstance(obj, int):
-        return obj
-    if hasattr(obj, "ctypes"):
-        return obj.ctypes.data
-    raise TypeError(type(obj))
+    host = getattr(obj, "ctypes", None)
+    if host is None:
+        raise TypeError(type(obj))
+    return host.data
 
 
 def _current_stream():
