@@ -464,70 +464,68 @@ __global__ void __launch_bounds__(kJoinThreads, kHeads == 4 ? 4 : 1) join_kernel
             const bool in[2] = {g < p.G && 8 * c0 < p.D, g < p.G && 8 * c0 + 64 < p.D};
             float q[16];
             if (keys) load16(q, p.q + r.token * p.ldq + ((long long)kvh * p.G + g) * p.D + 8 * c0, in);
+            // the rows of the keys, a lane's each; -1: outside the cache, zeros
+            static_assert(attn::kShortKeys <= 32, "a lane for each own key");
+            long long row = -1;
+            if (lane < keys) {
+                const int at = !p.page ? 0 : p.page_shift >= 0 ? lane >> p.page_shift : lane / p.page;
+                const long long tab = __ldg(p.table + (long long)r.part[0].base * p.ld_table + at);
+                row = p.page ? tab * p.page + (lane - at * p.page) : tab + lane;
+                if (row < 0 || row >= p.n_rows) {
+                    atomicExch(p.status, (int)LORA_ERR_DEVICE_INDEX);
+                    row = -1;
+                }
+            }
+            if (row >= 0) {  // all of them asked for at once
+                const uint16_t *kr = p.k + row * p.ldk + (long long)kvh * p.D, *vr = p.v + row * p.ldv + (long long)kvh * p.D;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(kr));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(vr));
+                if (p.D > 64) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(kr + 64));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(vr + 64));
+                }
+            }
+            // no more at a time than there are
+            constexpr int kOwnAhead = kAhead * kSlices <= attn::kShortKeys ? kAhead : attn::kShortKeys / kSlices;
 #pragma unroll 1
-            for (int key0 = 0; key0 < keys; key0 += 32) {
-                // the rows of 32 keys, a lane's each; -1: outside the cache, zeros
-                long long row = -1;
-                if (key0 + lane < keys) {
-                    const int key = key0 + lane;
-                    const int at = !p.page ? 0 : p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
-                    const long long tab = __ldg(p.table + (long long)r.part[0].base * p.ld_table + at);
-                    row = p.page ? tab * p.page + (key - at * p.page) : tab + key;
-                    if (row < 0 || row >= p.n_rows) {
-                        atomicExch(p.status, (int)LORA_ERR_DEVICE_INDEX);
-                        row = -1;
+            for (int i0 = 0; i0 < keys; i0 += kOwnAhead * kSlices) {
+                uint4 k[kOwnAhead][2], v[kOwnAhead][2];
+                float score[kOwnAhead];
+#pragma unroll
+                for (int a = 0; a < kOwnAhead; ++a) {
+                    const int i = i0 + a * kSlices + slice;
+                    const int x = __shfl_sync(0xffffffffu, (int)row, i & 31);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool is = in[h] && i < keys && x >= 0;
+                        k[a][h] = is ? *(const uint4 *)(p.k + x * p.ldk + head + 64 * h) : make_uint4(0, 0, 0, 0);
+                        v[a][h] = is ? *(const uint4 *)(p.v + x * p.ldv + head + 64 * h) : make_uint4(0, 0, 0, 0);
                     }
                 }
-                const int end = min(32, keys - key0);
-                if (row >= 0) {  // all of them asked for at once
-                    const uint16_t *kr = p.k + row * p.ldk + (long long)kvh * p.D, *vr = p.v + row * p.ldv + (long long)kvh * p.D;
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(kr));
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(vr));
-                    if (p.D > 64) {
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(kr + 64));
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(vr + 64));
-                    }
+                float m = top;
+#pragma unroll
+                for (int a = 0; a < kOwnAhead; ++a) {
+                    float y[16], d = 0.f;
+                    floats(y, k[a][0]);
+                    floats(y + 8, k[a][1]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) d += q[i] * y[i];
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                    score[a] = i0 + a * kSlices + slice < keys ? d * p.scale_log2 : -INFINITY;
+                    m = fmaxf(m, score[a]);
                 }
-#pragma unroll 1
-                for (int i0 = 0; i0 < end; i0 += kAhead * kSlices) {
-                    uint4 k[kAhead][2], v[kAhead][2];
-                    float score[kAhead];
+                const float base = raise(m);
 #pragma unroll
-                    for (int a = 0; a < kAhead; ++a) {
-                        const int i = i0 + a * kSlices + slice;
-                        const int x = __shfl_sync(0xffffffffu, (int)row, i & 31);
+                for (int a = 0; a < kOwnAhead; ++a) {
+                    const float x = exp2f(score[a] - base);
+                    if (x == 0.f) continue;
+                    float y[16];
+                    floats(y, v[a][0]);
+                    floats(y + 8, v[a][1]);
+                    sum += x;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const bool is = in[h] && i < end && x >= 0;
-                            k[a][h] = is ? *(const uint4 *)(p.k + x * p.ldk + head + 64 * h) : make_uint4(0, 0, 0, 0);
-                            v[a][h] = is ? *(const uint4 *)(p.v + x * p.ldv + head + 64 * h) : make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    float m = top;
-#pragma unroll
-                    for (int a = 0; a < kAhead; ++a) {
-                        float y[16], d = 0.f;
-                        floats(y, k[a][0]);
-                        floats(y + 8, k[a][1]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) d += q[i] * y[i];
-#pragma unroll
-                        for (int o = 1; o < 8; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                        score[a] = i0 + a * kSlices + slice < end ? d * p.scale_log2 : -INFINITY;
-                        m = fmaxf(m, score[a]);
-                    }
-                    const float base = raise(m);
-#pragma unroll
-                    for (int a = 0; a < kAhead; ++a) {
-                        const float x = exp2f(score[a] - base);
-                        if (x == 0.f) continue;
-                        float y[16];
-                        floats(y, v[a][0]);
-                        floats(y + 8, v[a][1]);
-                        sum += x;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[i] += x * y[i];
-                    }
+                    for (int i = 0; i < 16; ++i) acc[i] += x * y[i];
                 }
             }
         }
