@@ -40,3 +40,11 @@ def test_an_integer_costs_no_exception():
 
     assert L.ptr(Counted(64)) == 64
     assert not seen
+
+
+def test_tensors_before_and_after_their_type_is_known(monkeypatch):
+    t, p = torch.zeros(3), torch.nn.Parameter(torch.zeros(2))
+    for known in (None, torch.Tensor):
+        monkeypatch.setattr(L, "_tensor", known)
+        assert L.ptr(t) == t.data_ptr() and L.ptr(p) == p.data_ptr()
+        assert L.ptr(None) is None and L.ptr(7) == 7 and L.ptr(t[1:]) == t.data_ptr() + 4
