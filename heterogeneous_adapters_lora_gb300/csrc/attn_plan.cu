@@ -126,14 +126,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     if (tid == 0) {
         total_time = 0;
         bad = 0;
-        // The status word stays as calls left it until it is read.  Only the first build of a
-        // binding clears it, also when a captured build is replayed.
-        unsigned long long *binding = (unsigned long long *)(p.counters + attn::kBinding);
-        if (*binding != p.binding) {
-            *binding = p.binding;
-            p.counters[attn::kStatus] = LORA_OK;
-        }
     }
+    // The status word stays as calls left it until it is read.  Only the first build of a
+    // binding clears it, also when a captured build is replayed.  Whose it is is asked for
+    // here and looked at in the end: waited for here, it would add 0.3 us.
+    unsigned long long *binding = (unsigned long long *)(p.counters + attn::kBinding);
+    const unsigned long long of = tid == 0 ? *(volatile unsigned long long *)binding : 0;
+    auto own_status = [&]() {
+        if (of == p.binding) return;
+        *binding = p.binding;
+        p.counters[attn::kStatus] = LORA_OK;
+    };
     for (int i = tid; i < kBuckets; i += kPlanThreads) hist[0][i] = hist[1][i] = 0;
     if (tid <= attn::kMostFit) fit[tid] = 0;
     __syncthreads();
@@ -156,6 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (tid == 0) {
             p.counters[attn::kItems] = p.counters[attn::kUnits] = 0;
             p.counters[attn::kPartTokens] = p.counters[attn::kTiles] = p.counters[attn::kJoins] = 0;
+            own_status();
             atomicExch(p.counters + attn::kStatus, (int)LORA_ERR_DEVICE_INDEX);
         }
         return;
@@ -358,6 +362,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         p.counters[attn::kUnits] = n_units;
         p.counters[attn::kPartTokens] = n_part;
         p.counters[attn::kTiles] = n_tiles;
+        own_status();
     }
 }
 
