@@ -23,12 +23,20 @@
 // two softmaxes (512 cycles of exponentials each and about 300 other
 // instructions) run under them, and a slot's own chain (S there, softmax 1100
 // to 1400 cycles, 250 to the MMA warp, 1024 of products) just fits: one prompt
-// of 7995 tokens, 32 heads of 128 over 8: 300 us, 1.75 PFLOP/s, tensor pipe 76%
-// active.  One-tile items of decode batches are bound by HBM (64 single tokens
-// over up to 4000 keys: 89 us, 6.0 TB/s).  Short units are bound by chains of
-// dependent steps in single warps: one of two one-key items takes 8600 cycles,
-// of which reading the unit and its table and issuing four stages' copies is
-// one chain of 7000, a softmax, its wait for O and the stores another.
+// of 7995 tokens, 32 heads of 128 over 8: 298 us in a burst of twelve calls,
+// 1.76 PFLOP/s, tensor pipe 76% active; 331 us, 1.58 PFLOP/s, in calls that go
+// on, whose clocks the power limit lowers.  One-tile items of decode batches are
+// bound by HBM (64 single tokens over up to 4000 keys: 89 us, 6.0 TB/s).  Short
+// units are bound by chains of dependent steps in single warps: one of two
+// one-key items takes 8600 cycles, of which reading the unit and its table and
+// issuing four stages' copies is one chain of 7000, a softmax, its wait for O
+// and the stores another.
+//
+// Roundings: scores, statistics, accumulators and partial results are fp32; P is
+// rounded to bf16 once, because the products take both operands in one 16-bit
+// type and V is bf16.  The sums l are of the weights before that, whose
+// roundings average out: against 64 bits the outputs are 1.7e-3 to 2.3e-3 off,
+// where rounding the exact ones to bf16 gives 1.5e-3 to 1.7e-3.
 //
 // Orders that no barrier of its own is needed for: a slot's QK of block j + 1
 // is issued after its PV of block j, so "S is there" also says that O holds

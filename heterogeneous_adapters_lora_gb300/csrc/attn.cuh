@@ -37,6 +37,10 @@ constexpr int kPairBlock = 18, kPairItem = 20, kOneBlock = 16, kOneItem = 10;
 // case, kMinPrefixBlocks at least (a token behind a prefix of 8000: 18.3 us in
 // 21 ranges of 3 blocks, 176 units, 15.7 in 16 of 4; 4 tokens behind one of 1000:
 // 11.4 in ranges of 3, 10.6 of 2; 16 tokens over 4000 keys 14.3 of 4, 13.5 of 3).
+// Batches of more tiles than SMs are not looked at, and tiles whose own keys the
+// join takes count: without them 152 to 256 tokens of up to 16 own keys behind a
+// prefix of 500 take 13.0 to 20.2 us instead of 13.9 to 20.0, but behind one of
+// 1000, where there is more to join, 19.7 to 23.5 instead of 15.0 to 22.9.
 constexpr int kMinBlocks = 4;
 constexpr int kMostFit = 16, kMinOwnBlocks = 3, kMinPrefixBlocks = 2;
 
@@ -44,7 +48,7 @@ constexpr int kMostFit = 16, kMinOwnBlocks = 3, kMinPrefixBlocks = 2;
 // more than this need no item, nearly empty tiles that cost a CTA 4 us a pair:
 // the join takes them as it does partial results, a dependent round of three
 // keys after another (256 tokens behind a prefix of 500: up to 10 own keys 41 us
-// with items, 18 without; up to 60 own keys 41 and 40; of up to 24 or 32 keys it
+// with items, 18 without; up to 60 own keys 41 and 37; of up to 24 or 32 keys it
 // is slower where few tokens have so few, 32 prefixes 111 and 113 against 108).
 constexpr int kShortKeys = 16;
 

@@ -10,11 +10,12 @@
 // when the head size and its rotated part are multiples of 16 elements, else 8.
 //
 // Few tokens: a warp does kU heads per group of one token (256 tokens of that
-// size: 3.1 us; one token: 2.2 us, of which a launch is most).  Many tokens:
-// resident CTAs pass their tokens' rows through shared memory by bulk copies,
-// which keeps three rows a CTA and six CTAs an SM in flight and writes whole
-// rows (7995 tokens: 35 us, 5.7 TB/s, against 47 us with a CTA per unit and
-// 39 us with four rows and four CTAs).
+// size: 3.1 us in a graph; one token: 2.2 us, of which a launch is most; calls
+// one by one take 6.6 to 7.7 us, the host's time).  Many tokens: resident CTAs
+// pass their tokens' rows through shared memory by bulk copies, which keeps
+// three rows a CTA and six CTAs an SM in flight and writes whole rows (7995
+// tokens: 35 us, 5.7 TB/s, against 47 us with a CTA per unit and 39 us with four
+// rows and four CTAs).
 #include <math.h>
 #include <string.h>
 

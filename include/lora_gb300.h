@@ -538,10 +538,10 @@ LORA_API lora_status_t lora_attn_plan_bind(lora_attn_plan_t *plan, const lora_at
  * is the sequences group_start[g] .. group_start[g+1] - 1
  * (d_group_start [n_groups + 1] int32, from 0 to n_seqs), which share
  * prefix_len[g] keys (d_prefix_len [n_groups] int32, 0..max_prefix_len) ahead
- * of their own; a group may have no sequences.  Lengths that break these rules make an empty plan (calls with
- * it write nothing) and set the plan's status to LORA_ERR_DEVICE_INDEX.  A
- * build clears no status: what earlier steps set stays until it is read.
- * max_kv_len and max_prefix_len are at most 2^30.
+ * of their own; a group may have no sequences.  Lengths that break these rules
+ * make an empty plan (calls with it write nothing) and set the plan's status to
+ * LORA_ERR_DEVICE_INDEX.  A build clears no status: what earlier steps set stays
+ * until it is read.  max_kv_len and max_prefix_len are at most 2^30.
  * Errors: LORA_ERR_INVALID_ARG, LORA_ERR_CAPACITY. */
 LORA_API lora_status_t lora_attn_build_plan(lora_attn_plan_t *plan, int32_t n_seqs, int32_t total_q,
                                             const int32_t *d_cu_q, const int32_t *d_kv_len, int32_t n_groups,
@@ -566,8 +566,9 @@ LORA_API size_t lora_attn_workspace_bytes(const lora_attn_plan_t *plan);
  * query of a sequence sees do not touch its results, whatever their rows
  * hold (but a value that is not finite makes NaN of the results of earlier
  * queries that share its block of 128 keys, as its product with a weight of
- * zero is NaN).  Rows that a table puts outside [0, n_rows) count as zero rows and set
- * the plan's status to LORA_ERR_DEVICE_INDEX.  Scores and sums are fp32; the
+ * zero is NaN).  Rows that a table puts outside [0, n_rows) count as zero rows
+ * and set the plan's status to LORA_ERR_DEVICE_INDEX; n_rows may be 0.  out must
+ * not overlap q, k or v.  Scores and sums are fp32; the
  * probabilities are rounded to bf16 for their product with v.
  * The result does not change from run to run.
  * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, leading dimension
