@@ -68,6 +68,15 @@ class AttnPlan(ctypes.Structure):
                 ("first_tile", c_vp), ("counters", c_vp), ("binding", ctypes.c_uint64)]
 
 
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("n_experts", c_i32), ("top_k", c_i32), ("scoring", c_i32), ("renormalize", c_i32),
+                ("logits_f32", c_i32), ("scale", ctypes.c_float)]
+
+
+class MoELayerDesc(ctypes.Structure):
+    _fields_ = [("n_experts", c_i32), ("top_k", c_i32), ("d_model", c_i32), ("d_mlp", c_i32), ("activation", c_i32)]
+
+
 class LoraError(RuntimeError):
     def __init__(self, code, where, cuda_error=None):
         self.code = int(code)
@@ -133,6 +142,11 @@ EXPORTS = {
     "lora_prefix_attention": (c_i32, [ctypes.POINTER(AttnPlan), c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_vp,
                                       c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_size, c_vp]),
     "lora_attn_get_status": (c_i32, [ctypes.POINTER(AttnPlan), c_vp]),
+    "lora_moe_route": (c_i32, [ctypes.POINTER(RouteDesc), c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp]),
+    "lora_moe_layer_workspace_bytes": (c_size, [ctypes.POINTER(MoELayerDesc), c_vp, c_i32]),
+    "lora_moe_layer": (c_i32, [ctypes.POINTER(MoELayerDesc), c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_i64,
+                               c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_size, c_vp]),
+    "lora_sample": (c_i32, [c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
 }
 
 
@@ -395,6 +409,30 @@ def lora_prefix_attention(plan: AttnPlan, q, ldq, k, ldk, v, ldv, n_rows, table,
 
 def lora_attn_get_status(plan: AttnPlan, stream=None) -> int:
     return int(lib().lora_attn_get_status(ctypes.byref(plan), stream_ptr(stream)))
+
+
+def lora_moe_route(desc: RouteDesc, logits, ld_logits, T, bias, topk_ids, topk_w, stream=None):
+    """The experts of every token and their weights from a router's logits."""
+    _check(lib().lora_moe_route(ctypes.byref(desc), ptr(logits), ld_logits, T, ptr(bias), ptr(topk_ids), ptr(topk_w),
+                                stream_ptr(stream)), "lora_moe_route")
+
+
+def lora_moe_layer_workspace_bytes(desc: MoELayerDesc, pool, max_tokens) -> int:
+    return int(lib().lora_moe_layer_workspace_bytes(ctypes.byref(desc), pool, max_tokens))
+
+
+def lora_moe_layer(desc: MoELayerDesc, pool, d_idx, x, ldx, T, topk_ids, topk_w, w13, ld_w13, w2, ld_w2, out, ld_out,
+                   status, ws, ws_bytes, stream=None):
+    """A whole layer of experts for a few tokens: base products, adapters' deltas, activation, weighted sum."""
+    _check(lib().lora_moe_layer(ctypes.byref(desc), pool, ptr(d_idx), ptr(x), ldx, T, ptr(topk_ids), ptr(topk_w),
+                                ptr(w13), ld_w13, ptr(w2), ld_w2, ptr(out), ld_out, ptr(status), ptr(ws), ws_bytes,
+                                stream_ptr(stream)), "lora_moe_layer")
+
+
+def lora_sample(logits, ld, T, vocab_size, temperature, top_k, top_p, min_p, uniform, tokens, logprobs, stream=None):
+    """The next token of every row of logits, and its log probability."""
+    _check(lib().lora_sample(ptr(logits), ld, T, vocab_size, ptr(temperature), ptr(top_k), ptr(top_p), ptr(min_p),
+                             ptr(uniform), ptr(tokens), ptr(logprobs), stream_ptr(stream)), "lora_sample")
 
 
 def lora_kernel_launch_count() -> int:

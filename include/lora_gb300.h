@@ -599,6 +599,120 @@ LORA_API lora_status_t lora_prefix_attention(const lora_attn_plan_t *plan, const
  * error of all builds and calls since it was read, or since the plan was bound. */
 LORA_API lora_status_t lora_attn_get_status(const lora_attn_plan_t *plan, void *stream);
 
+/* ------------------------------------------- a layer of experts for few tokens
+ *
+ * The rest of a decode step of a MoE model around its LoRA layers: the
+ * router's choice, the chosen experts with the adapters' deltas, and the next
+ * token from the logits that lora_logits_apply leaves. */
+
+#define LORA_ROUTE_MAX_EXPERTS 1024
+#define LORA_ROUTE_MAX_TOP_K 32
+#define LORA_MOE_LAYER_MAX_PAIRS 4096
+
+/* What a router does with its logits. */
+typedef struct {
+    int32_t n_experts;    /* 1..LORA_ROUTE_MAX_EXPERTS */
+    int32_t top_k;        /* 1..LORA_ROUTE_MAX_TOP_K, at most n_experts */
+    int32_t scoring;      /* 0: softmax over the token's experts; 1: 1 / (1 + exp(-logit)) */
+    int32_t renormalize;  /* 1: weights are divided by their sum over the chosen experts */
+    int32_t logits_f32;   /* 1: fp32 logits; 0: bf16 */
+    float scale;          /* factor of the weights, finite */
+} lora_route_desc_t;
+
+/* The experts of every token and their weights, as lora_build_meta,
+ * lora_moe_apply and lora_moe_layer take them: the top_k experts of the largest
+ * score + bias (bias: [n_experts] fp32 device, NULL = none), in that order, of
+ * equal ones the lower id first; weight = the score itself (without the bias),
+ * divided by the chosen scores' sum under renormalize (0 where that sum is 0),
+ * times scale.  logits: [T][ld_logits] device, aligned to its type, any
+ * ld_logits >= n_experts.  The order is that of the exact scores: where fp32
+ * cannot tell two biased scores apart they are taken again in 64 bits.  An
+ * expert whose logit or biased score is NaN or -inf is not chosen (and adds
+ * nothing to a softmax); a token with fewer than top_k others gets ids of -1 and
+ * weights of 0 in the last places.  A logit of +inf counts as the largest finite
+ * number.  topk_ids: [T][top_k] int32, topk_w: [T][top_k] fp32, device, not
+ * overlapping the inputs.
+ * Errors: LORA_ERR_INVALID_ARG (a null or misaligned pointer, T < 0, a field or
+ * ld_logits out of range). */
+LORA_API lora_status_t lora_moe_route(const lora_route_desc_t *desc, const void *logits, int64_t ld_logits, int32_t T,
+                                      const float *bias, int32_t *topk_ids, float *topk_w, void *stream);
+
+/* Shape of a layer of experts. */
+typedef struct {
+    int32_t n_experts;   /* 1..LORA_ROUTE_MAX_EXPERTS */
+    int32_t top_k;       /* 1..LORA_ROUTE_MAX_TOP_K */
+    int32_t d_model;     /* D: multiple of 8, 8..65536 */
+    int32_t d_mlp;       /* F: multiple of 8, 8..65536 */
+    int32_t activation;  /* act(g): 0 = g / (1 + exp(-g)); 1 = g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} lora_moe_layer_desc_t;
+
+/* Workspace bytes of lora_moe_layer for up to max_tokens tokens with this pool
+ * (0 if an argument is out of range, or the pool is not one the layer takes).
+ * The workspace must be zero before its first use (lora_workspace_init) and
+ * serve no other kind of call, nor layers of another shape or pool shape; calls
+ * that share one must not overlap on the device. */
+LORA_API size_t lora_moe_layer_workspace_bytes(const lora_moe_layer_desc_t *desc, const lora_pool_t *pool,
+                                               int32_t max_tokens);
+
+/* A whole layer of experts for a few tokens, base products and adapters'
+ * deltas together.  For token t with the experts e = topk_ids[t][k], their
+ * weights w_k = topk_w[t][k] and its adapter a = d_idx[t]:
+ *   g = W13[e][:F] x_t + scale[a] B13_gate[a][e] (A13_gate[a][e] x_t)      u likewise, rows F.. of W13
+ *   h = act(g) u
+ *   out[t] = sum_k w_k ( W2[e] h + scale[a] B2[a][e] (A2[a][e] h) )
+ * x: [T][ldx], out: [T][ld_out] bf16; w13: [n_experts][2F][ld_w13] (the gate's
+ * rows, then the up rows, of D elements), w2: [n_experts][D][ld_w2] (rows of F
+ * elements), bf16.  topk_ids: [T][top_k] int32; topk_w: [T][top_k] fp32, NULL =
+ * 1.  pool: a MoE pool of the same n_experts, d_model and d_mlp, gated (two w13
+ * slices of width F, or one of 2F), either layout; NULL = no adapters.  d_idx:
+ * [T] int32 slots, -1 = none; NULL exactly when pool is NULL.  No metadata are
+ * needed.  Rank and scale are read on the stream.
+ * Every chosen expert's weights are read once for up to 64 of its pairs; the
+ * call is meant for batches whose time is that of reading weights.
+ * Sums are fp32; h, which the second product takes in 16 bits, goes as the sum
+ * of two bf16; out is rounded once.  The result does not change from run to run.
+ * An id of -1 is no expert, and a token without experts gets zeros.  Other ids outside
+ * [0, n_experts) count as -1, slots outside [-1, max_loras) as no adapter, and both
+ * set *status (an int32 device word, may be NULL) to LORA_ERR_DEVICE_INDEX.  A wait that
+ * gives up (lora_set_spin_limit) sets it to LORA_ERR_TIMEOUT; out is not to be
+ * used then, the next call is whole.  out must overlap nothing else.
+ * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, a field or a leading
+ * dimension out of range, a pool of another device than the current one),
+ * LORA_ERR_SHAPE (the pool's sizes), LORA_ERR_UNSUPPORTED (a dense pool, one that is
+ * not gated), LORA_ERR_CAPACITY (the workspace, or T * top_k above
+ * LORA_MOE_LAYER_MAX_PAIRS). */
+LORA_API lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const lora_pool_t *pool, const int32_t *d_idx,
+                                      const void *x, int64_t ldx, int32_t T, const int32_t *topk_ids,
+                                      const float *topk_w, const void *w13, int64_t ld_w13, const void *w2,
+                                      int64_t ld_w2, void *out, int64_t ld_out, int32_t *status, void *workspace,
+                                      size_t ws_bytes, void *stream);
+
+/* The next token of every row of logits ([T][ld] bf16, vocab_size columns, as
+ * lora_logits_apply leaves them).  With temperature[t] > 0 the columns, ordered
+ * by logit (the largest first, of equal ones the lower index first), have the
+ * weights exp((logit - largest) / temperature[t]); kept are the first top_k[t] of
+ * them (all where top_k[t] < 1), of those the shortest beginning that holds
+ * top_p[t] of their weight (all where top_p[t] >= 1 or is NaN; at least one), and of those the ones
+ * of weight >= min_p[t] (at least one); the token is the first whose sum of
+ * weights up to it exceeds uniform[t] (in [0, 1); other numbers are moved into it, NaN
+ * to 0) times the weight of what is kept.  Otherwise the token is the first of the order.
+ * logprobs[t] (may be NULL) is the logarithm of the token's share of the
+ * weights of all columns (at temperature 1 where it is not > 0), whatever is kept.
+ * temperature, top_p, min_p and uniform are [T] fp32 and top_k [T] int32 device; NULL
+ * means 1, 1, 0, 0 and 0.  Logits of -inf or NaN take no part, +inf counts as the
+ * largest finite number; a row of which nothing is left gets token -1 and
+ * logprob -inf.  Weights and their sums are integers of 2^-62 of the largest
+ * weight, accurate to about 10^-14, so that sums do not depend on their order and the
+ * token is that of the exact formula but for numbers that close to a border.
+ * Rows whose logits that matter are 0 or of magnitudes in [2^-23, 2^9) are read twice;
+ * others up to 22 times.
+ * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, T < 0, ld < vocab_size or
+ * not a multiple of 8), LORA_ERR_SHAPE (vocab_size < 1 or > LORA_MAX_VOCAB). */
+LORA_API lora_status_t lora_sample(const void *logits, int64_t ld, int32_t T, int32_t vocab_size,
+                                   const float *temperature, const int32_t *top_k, const float *top_p,
+                                   const float *min_p, const float *uniform, int32_t *tokens, float *logprobs,
+                                   void *stream);
+
 /* Kernel selection for lora_apply_slices / lora_moe_apply (process-wide):
  * 0 = automatic (tcgen05 for long contiguous runs of a rank-64 dense pool;
  *     the fused decode kernel -- one thread-block cluster per adapter slot,
