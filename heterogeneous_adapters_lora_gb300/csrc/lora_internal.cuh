@@ -154,6 +154,11 @@ int lora_spin_limit();  // as lora_set_spin_limit left it
 bool lora_make_tmap_2d(CUtensorMap *m, const void *base, long long cols, long long rows, long long stride,
                        int box_cols, int box_rows, bool swizzle128);
 
+// 3D bf16 map over [depth][rows][cols] (strides in elements), boxes of one
+// depth in the 128-byte swizzle; elements outside read as zero (sgmv.cu).
+bool lora_make_tmap_3d(CUtensorMap *m, const void *base, long long cols, long long rows, long long depth, long long stride,
+                       long long depth_stride, int box_cols, int box_rows);
+
 // 3D bf16 tensor map over a row-major [rows][cols] matrix (cols % 64 == 0)
 // that lands a box of box_rows rows x box_chunks 128-byte column chunks in
 // shared memory chunk-major: for each chunk, the rows as 128-byte lines in

@@ -467,6 +467,19 @@ bool lora_make_tmap_heads(CUtensorMap *m, const void *base, int head_dim, int he
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool lora_make_tmap_3d(CUtensorMap *m, const void *base, long long cols, long long rows, long long depth, long long stride,
+                       long long depth_stride, int box_cols, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 f = encode_fn();
+    if (!f) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+    cuuint64_t strides[2] = {(cuuint64_t)stride * 2, (cuuint64_t)depth_stride * 2};
+    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool lora_sgmv_eligible(const lora_pool_t *pool) {
     const lora_pool_desc_t &d = pool->desc;
     if (pool->is_moe || !pool->d_bmaps || d.max_rank > 64) return false;
