@@ -10,7 +10,7 @@
 //
 //   shrink13   v[p] = scale A13 x        (with adapters; runs under the start of up)
 //   up         g, u = W13 x + B13 v; h = act(g) u; parts of A2 h      per 128 columns of h
-//   down       y[p] = w (W2 h + B2 (scale A2 h))                     per 256 rows of W2
+//   down       y[p] = w (W2 h + B2 (scale A2 h))                      per 256 rows of W2
 //   combine    out[t] = sum of y over the token's pairs, in their order, one rounding
 //
 // Work is cut by bytes, not by tiles.  A unit is 256 weight rows (128 of gate and 128
@@ -22,14 +22,21 @@
 // lower index are waited for, which have started earlier.  Every CTA finds its groups from
 // topk_ids by itself (a histogram and a scan in shared memory).
 //
-// Roles (320 threads): warp 0 issues the TMA copies, one lane the two weight boxes of a
-// block, the others four gathered rows each (tile::gather4 by token, or by pair); warp 1 issues the MMAs;
-// warps 2-9 are the epilogue, a row per thread, two warps per quarter of the accumulator's lanes
-// which take turns at four columns (pairs) each, under the next unit's MMAs (two accumulators).
+// Roles (352 threads): warp 0 issues the TMA copies, one lane the two weight boxes of a
+// block, others the pairs' rows (x by token, four rows to a tile::gather4; h, which up leaves in the order
+// of the groups, in boxes of eight); warp 1 issues the MMAs; warps 2-9 are the epilogue, a row per
+// thread, two warps per quarter of the accumulator's lanes which take four of eight columns (pairs) each, under
+// the next unit's MMAs (two accumulators); warp 10 says that a shared unit's sums are there (the
+// fence behind stores takes some 5 us while the memory is busy, which the epilogue would wait out).
 //
-// Roundings: sums are fp32 throughout (accumulators, v, parts, y).  h enters the second
-// product in 16 bits: as two bf16, h = hi + lo, in separate columns whose sums are
-// added (2^-17 of h instead of 2^-9; the weights' bytes bound the kernel, not its MMAs).
+// The adapters' part of eight pairs is small (256 rows of B, some ranks) and goes by m16n8k16
+// products in the epilogue's warps while a unit's weights are still on their way: the rows of
+// B, or of A2, come from global memory straight into registers, once per adapter among the eight, and the v of pairs
+// of other adapters count as zeros.
+//
+// Roundings: sums are fp32 throughout (accumulators, v, parts of A2 h, y).  h and v enter their
+// products in 16 bits: as two bf16, hi + lo, whose products are added (2^-17 of a
+// value instead of 2^-9; the weights' bytes bound the kernel, not its MMAs).
 #include <math.h>
 #include <stddef.h>
 #include <string.h>
@@ -37,6 +44,7 @@
 #include <atomic>
 
 #include "lora_internal.cuh"
+#include "mma_common.cuh"
 #include "tc_common.cuh"
 
 namespace {
@@ -48,7 +56,7 @@ constexpr int kGroup = 64;                    // pairs of a group
 constexpr int kRows = 256, kTile = 128;       // weight rows of a unit, of an MMA
 constexpr int kBK = 64;                       // columns of a block: one 128-byte swizzle row
 constexpr uint32_t kABytes = kRows * kBK * 2;
-constexpr int kStreamThreads = 320, kEpi0 = 2, kEpiThreads = 256;
+constexpr int kStreamThreads = 352, kEpi0 = 2, kEpiThreads = 256;
 constexpr int kSms = 152;                     // where no device answers
 constexpr int kLeast = 4;                     // fewest blocks worth a CTA
 
@@ -69,9 +77,10 @@ struct LayerArgs {
     int b_rows[3];                // rows of B per expert (0: one for all)
     const int32_t *rank, *enabled;
     const float *scale;
-    float *v13;                   // [P][2][R], scaled
-    uint16_t *h;                  // [2][P][F]: hi, lo
-    float *v2;                    // [P][ceil(F / 128)][R], parts of A2 h
+    int R8;
+    float *v13;                   // [P][2][R8], scaled (shared outer: by token), zeros past the adapter's rank
+    uint16_t *h;                  // [2][P][F]: hi, lo, in the order of the groups
+    float *v2;                    // [P][ceil(F / 128)][R8], parts of A2 h
     float *y;                     // [P][D], weighted
     float *part;                  // [CTA][2][kGroup][kTile] sums of shared units
     int *flags;                   // [2][CTA] part is there (up, down)
@@ -94,36 +103,95 @@ __device__ __forceinline__ int slot_of(const LayerArgs &p, int t, bool note) {
     return p.enabled[a] && p.rank[a] > 0 ? a : -1;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    return v;
+// A number as the sum of two bf16.
+__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
+    const __nv_bfloat16 a = __float2bfloat16_rn(v), b = __float2bfloat16_rn(v - __bfloat162float(a));
+    hi = *(const uint16_t *)&a;
+    lo = *(const uint16_t *)&b;
 }
-// products of 8 pairs of bf16
-__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
-    return bf16lo(a.x) * bf16lo(b.x) + bf16hi(a.x) * bf16hi(b.x) + bf16lo(a.y) * bf16lo(b.y) + bf16hi(a.y) * bf16hi(b.y) +
-           bf16lo(a.z) * bf16lo(b.z) + bf16hi(a.z) * bf16hi(b.z) + bf16lo(a.w) * bf16lo(b.w) + bf16hi(a.w) * bf16hi(b.w);
-}
-__device__ __forceinline__ float dot_bf16(const uint16_t *a, const uint16_t *b, int n, int lane) {
-    float s = 0.f;
-    for (int i = lane * 8; i < n; i += 256) s += dot8(__ldg((const uint4 *)(a + i)), __ldg((const uint4 *)(b + i)));
-    return warp_sum(s);
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = bgmv::pack_bf16x2(a, b);
+    lo = bgmv::pack_bf16x2(a - bf16lo(hi), b - bf16hi(hi));
 }
 
-// scale * A x of every pair: a warp per (pair, slice, rank row)
-__global__ void __launch_bounds__(kThreads) shrink13_kernel(const LayerArgs p) {
+// v = scale A13 x.  A CTA takes an expert (shared outer: the slots of one
+// remainder by the number of CTAs), a slice and 16 ranks.  It finds the expert's pairs (the slots'
+// tokens), sorts them by slot and reads an adapter's rows once for up to 8 of them: 16 ranks x 8
+// pairs is one m16n8k16 product, whose operands come from global memory straight into registers
+// (any order of k will do as long as both have the same), a warp per eighth of the columns.
+// Several CTAs (gridDim.z) share an expert's batches of 8.  Bound by the adapters' bytes for
+// many pairs, by its chain of dependent reads for few (ids and slots, ranks, rows).
+constexpr int kBatch = 8, kRanks = 16;
+__global__ void __launch_bounds__(kThreads, 4) shrink13_kernel(const LayerArgs p, int chunks) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ uint32_t found[kMaxP], key[kMaxP];  // slot << 12 | pair; sorted
+    __shared__ float sums[kWarps][kRanks][kBatch];
+    __shared__ int s_n;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int which = (int)blockIdx.y / chunks, r0 = (int)blockIdx.y % chunks * kRanks;
+    if (tid == 0) s_n = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    const long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (i >= (long long)p.P * 2 * p.R) return;
-    const int r = (int)(i % p.R), s = (int)(i / p.R % 2), pair = (int)(i / p.R / 2), t = pair / p.K;
-    const int e = expert_of(p, pair, false), a = slot_of(p, t, false);
-    if (e < 0 || a < 0 || r >= p.rank[a]) return;
-    const int n = p.n13 == 2 ? s : 0;
-    const uint16_t *A = p.A[n] + (long long)a * p.a_ss[n] + (long long)e * p.a_es[n] + (long long)r * p.D;
-    const float v = dot_bf16(A, p.x + t * p.ldx, p.D, lane);
-    if (lane == 0) p.v13[i] = v * p.scale[a];
+    __syncthreads();
+    const int count = p.shared ? p.T : p.P, sets = gridDim.x, me = blockIdx.x;
+#pragma unroll 4
+    for (int i = tid; i < count; i += kThreads) {
+        const int e = p.shared ? me : p.ids[i], a = p.idx[p.shared ? i : i / p.K];
+        if (e == me && a >= 0 && a < p.L && (!p.shared || a % sets == me)) found[atomicAdd(&s_n, 1)] = (uint32_t)a << 12 | (uint32_t)i;
+    }
+    __syncthreads();
+    const int n = s_n;
+    // in order, whatever order they were found in; those of slots without an adapter go unused
+    for (int i = tid; i < n; i += kThreads) {
+        const uint32_t mine = found[i];
+        int before = 0;
+        for (int j = 0; j < n; ++j) before += found[j] < mine;
+        key[before] = mine;
+    }
+    __syncthreads();
+    const int m = p.n13 == 2 ? which : 0;
+    const int g = lane >> 2, c0 = (lane & 3) * 8;  // row of the fragments, first of this lane's 8 columns of 32
+    for (int at = 0, b = 0; at < n; ++b) {
+        const int slot = (int)(key[at] >> 12);
+        int few = 1;
+        while (few < kBatch && at + few < n && (int)(key[at + few] >> 12) == slot) ++few;
+        const int first = at;
+        at += few;
+        if (b % (int)gridDim.z != (int)blockIdx.z) continue;
+        const int rank = p.enabled[slot] ? p.rank[slot] : 0;
+        const uint16_t *A = p.A[m] + (long long)slot * p.a_ss[m] + (p.shared ? 0 : (long long)me * p.a_es[m]);
+        const int i = (int)(key[first + min(g, few - 1)] & 0xfffu);
+        const uint16_t *x = p.x + (long long)(p.shared ? i : i / p.K) * p.ldx;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r0 < rank) {
+            const uint16_t *row0 = A + (long long)min(r0 + g, rank - 1) * p.D, *row1 = A + (long long)min(r0 + g + 8, rank - 1) * p.D;
+#pragma unroll 4
+            for (int c = warp * 32 + c0; c - c0 < p.D; c += kWarps * 32) {
+                uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0, v = a0;
+                if (c < p.D) {
+                    a0 = ldg_stream(row0 + c);
+                    a1 = ldg_stream(row1 + c);
+                    v = __ldg((const uint4 *)(x + c));
+                }
+                bgmv::mma16816(d, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+                bgmv::mma16816(d, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+            }
+        }
+        sums[warp][g][(lane & 3) * 2] = d[0];
+        sums[warp][g][(lane & 3) * 2 + 1] = d[1];
+        sums[warp][g + 8][(lane & 3) * 2] = d[2];
+        sums[warp][g + 8][(lane & 3) * 2 + 1] = d[3];
+        __syncthreads();
+        const int r = r0 + (tid & 15), j = tid >> 4;
+        if (j < few && r < p.R8 && rank > 0) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += sums[w][tid & 15][j];
+            v = r < rank ? v * p.scale[slot] : 0.f;  // ranks past the adapter's meet zeros: finite, whatever x is
+            p.v13[((long long)(key[first + j] & 0xfffu) * 2 + which) * p.R8 + r] = v;
+        }
+        __syncthreads();
+    }
 }
 
 __device__ __forceinline__ float activation(float g, int gelu) {
@@ -134,7 +202,7 @@ __device__ __forceinline__ float activation(float g, int gelu) {
 // ------------------------------------------------------------ streamed products
 
 struct StreamArgs {
-    CUtensorMap tm_w, tm_b;
+    CUtensorMap tm_w, tm_b;  // weights, the pairs' rows (x or h)
     LayerArgs a;
     int KB, MT;  // blocks of a unit, units of a group
 };
@@ -143,29 +211,41 @@ template <bool DOWN>
 struct Shape {
     static constexpr int kCols = DOWN ? 2 * kGroup : kGroup;  // accumulator columns of a tile (down: hi, then lo)
     static constexpr uint32_t kStage = kABytes + kCols * 128;
-    static constexpr int kStages = DOWN ? 4 : 5;
+    static constexpr int kStages = 3;
     static constexpr int kTmem = 4 * kCols;  // two tiles, two buffers
 };
 
-struct Shared {
-    uint64_t full[5], empty[5], accf[2], acce[2];
+constexpr int kBatchCols = 8;                // columns that the epilogue takes at a time
+constexpr int kDPitch = kRows + 4;           // of the adapters' part of a column: no two of a product's lanes on one bank
+constexpr int kVFloats = 8192;
+constexpr int kHPitch = kTile + 32;          // of a column of h: no two of 8 lanes' 16 bytes on one bank
+
+template <bool DOWN, bool ADAPT>
+struct SharedOf {
+    uint64_t full[3], empty[3], accf[2], acce[2];
     uint32_t tmem;
     int abort;
     uint16_t groups[kMaxE + 8], pairs[kMaxE + 8];  // groups and pairs of the experts before this one
     uint16_t list[kMaxP];                          // pairs of this CTA's experts, by expert
-    int slot[kGroup], rank[kGroup];                // of a unit's pairs: adapter slot (-1: none), its rank
-    float scale[kGroup], weight[kGroup];
-    union alignas(16) {
+    // of the pairs of a group, and of the next one
+    struct Pairs {
+        unsigned long long starts;       // columns where another adapter begins
+        int slot[kGroup], rank[kGroup];  // adapter (-1: none) and its rank
+        float weight[kGroup];
+    } of[2];
+    alignas(16) union {
         struct {
             int count[kMaxE];
-            uint16_t ids[kMaxP];
-        } g;                                                 // while groups are found
-        float h[2][2][4][kTile + 4];                         // up: four columns of h of each half of the warps, twice
-        float v2[2][4][LORA_MAX_RANK];                       // down: scale A2 h of four pairs
+            uint16_t ids[kMaxP], slots[ADAPT ? kMaxP : 1];
+        } g;  // while groups are found
+        struct {
+            float delta[kBatchCols][kDPitch];  // the adapters' part of eight columns
+            float v[ADAPT ? kVFloats : 1];     // scale A x or scale A2 h of some pairs
+            alignas(16) uint16_t h[ADAPT && !DOWN ? 2 : 1][ADAPT && !DOWN ? kGroup : 1][kHPitch];  // hi and lo of the unit's columns of h
+        } e;  // epilogue
     } u;
 };
-
-static_assert(offsetof(Shared, u) % 16 == 0 && sizeof(float[kTile + 4]) % 16 == 0, "columns of h are read 16 bytes at a time");
+static_assert(sizeof(float[kBatchCols][kDPitch]) % 16 == 0 && kHPitch % 8 == 0, "read 16 bytes at a time");
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -200,6 +280,21 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// A box of weights, which nobody reads again: L2 is to give their lines up first, and to keep
+// what is read often (instructions above all: a fetch from DRAM takes microseconds behind the weights).
+__device__ __forceinline__ uint64_t evict_first() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void tma_weights(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], "
+        "[%5], %6;" ::"r"(tc::smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&r)[4]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
@@ -207,11 +302,13 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&r)[4]) {
                  : "memory");
 }
 
+template <class Shared>
 __device__ __forceinline__ void note_timeout(const LayerArgs &p, Shared &s) {
     *(volatile int *)&s.abort = 1;
     if (p.status) atomicExch(p.status, (int)LORA_ERR_TIMEOUT);
 }
 // Waits for a phase of a barrier; false once any wait of the CTA has given up.
+template <class Shared>
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const LayerArgs &p, Shared &s) {
     int polls = 0;
     while (!tc::mbar_try_wait(bar, parity)) {
@@ -248,6 +345,7 @@ __device__ __forceinline__ bool bar_and(int id, int threads, bool ok) {
 }
 
 // The groups of the batch, as prefix sums over the experts.
+template <class Shared>
 __device__ int find_groups(const LayerArgs &p, Shared &s) {
     for (int i = threadIdx.x; i < p.E; i += kStreamThreads) s.u.g.count[i] = 0;
     __syncthreads();
@@ -255,6 +353,7 @@ __device__ int find_groups(const LayerArgs &p, Shared &s) {
         const int e = p.ids[i];
         const bool ok = e >= 0 && e < p.E;
         s.u.g.ids[i] = ok ? (uint16_t)e : 0xffffu;
+        if (sizeof(s.u.g.slots) > 2) s.u.g.slots[i] = (uint16_t)min((unsigned)p.idx[i / p.K], 0xffffu);
         if (ok) atomicAdd(&s.u.g.count[e], 1);
     }
     __syncthreads();
@@ -280,6 +379,7 @@ __device__ int find_groups(const LayerArgs &p, Shared &s) {
     __syncthreads();
     return s.groups[p.E];
 }
+template <class Shared>
 __device__ __forceinline__ int expert_of_group(const LayerArgs &p, const Shared &s, int g) {
     int lo = 0, hi = p.E;  // groups[lo] <= g < groups[hi]
     while (hi - lo > 1) {
@@ -289,17 +389,43 @@ __device__ __forceinline__ int expert_of_group(const LayerArgs &p, const Shared 
     }
     return lo;
 }
-// The pairs of experts e0..e1 in their order, each expert's by a warp.
+// The pairs of experts e0..e1, each expert's by a warp: in their order, with adapters those of a group by slot.
+template <class Shared>
 __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = e0 + warp; e <= e1; e += kStreamThreads / 32) {
-        int at = s.pairs[e] - s.pairs[e0];
-        if (s.pairs[e + 1] == s.pairs[e]) continue;
+        const int first = s.pairs[e] - s.pairs[e0], n = s.pairs[e + 1] - s.pairs[e];
+        if (n == 0) continue;
+        int at = first;
         for (int i = 0; i < p.P; i += 32) {
             const bool mine = i + lane < p.P && s.u.g.ids[i + lane] == e;
             const unsigned m = __ballot_sync(kAll, mine);
             if (mine) s.list[at + __popc(m & ((1u << lane) - 1))] = (uint16_t)(i + lane);
             at += __popc(m);
+        }
+        __syncwarp();
+        for (int g = first; sizeof(s.u.g.slots) > 2 && g < first + n; g += kGroup) {
+            const int few = min(kGroup, first + n - g);
+            // keys that are all different: the slot, then the place
+            uint16_t pair[2];
+            unsigned key[2];
+            int before[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = j * 32 + lane;
+                pair[j] = i < few ? s.list[g + i] : 0;
+                key[j] = (i < few ? (unsigned)s.u.g.slots[pair[j]] : 0xffffu) << 6 | (unsigned)i;
+            }
+            for (int j = 0; j < few; ++j) {
+                const unsigned other = __shfl_sync(kAll, j < 32 ? key[0] : key[1], j & 31);
+                before[0] += other < key[0];
+                before[1] += other < key[1];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (j * 32 + lane < few) s.list[g + before[j]] = pair[j];
+            __syncwarp();
         }
     }
 }
@@ -314,7 +440,9 @@ struct Range {
 struct Part {
     int k0, k1;        // blocks of the unit
     int e, m, n, at;   // expert, place in it, pairs, first of them in the list
+    int pos;           // ... and in the order of the groups
 };
+template <class Shared>
 __device__ __forceinline__ Part part_of(const StreamArgs &q, const Shared &s, const Range &r, int u, int e_first) {
     Part x;
     x.k0 = max(r.b0 - u * q.KB, 0);
@@ -324,38 +452,227 @@ __device__ __forceinline__ Part part_of(const StreamArgs &q, const Shared &s, co
     x.e = expert_of_group(q.a, s, g);
     const int first = s.pairs[x.e] + (g - s.groups[x.e]) * kGroup;
     x.n = min(kGroup, s.pairs[x.e + 1] - first);
+    x.pos = first;
     x.at = first - s.pairs[e_first];
     return x;
 }
 
-// sum_r b[r] v[r] of up to 4 rows of B (16 bytes each 8 ranks), v in shared or global memory
-template <int N>
-__device__ __forceinline__ void expand_rows(float (&acc)[N], const uint16_t *const (&b)[N], const float *const (&v)[N],
-                                            const int (&rank)[N], int most) {
-    for (int r = 0; r < most; r += 8) {
-        uint4 w[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) w[j] = r < rank[j] ? __ldg((const uint4 *)(b[j] + r)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (r >= rank[j]) continue;
-            const uint32_t c[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (r + i < rank[j]) acc[j] += (i & 1 ? bf16hi(c[i >> 1]) : bf16lo(c[i >> 1])) * v[j][r + i];
+__device__ __forceinline__ void prefetch_l2(const void *at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
+
+// What the epilogue does for adapters; all of its threads call these together.  The code is kept
+// small and in one place each: what a unit runs once comes from L2 instruction by instruction.
+template <bool DOWN, bool ADAPT>
+struct Epilogue {
+    typedef SharedOf<DOWN, ADAPT> Shared;
+    typedef typename Shared::Pairs Pairs;
+    const LayerArgs &p;
+    Shared &s;
+    const int tid, warp, lane, g, t4;  // g, t4: row and column of a product's fragments
+    const int per, lot;                // floats of v of a pair, pairs of them at a time
+
+    __device__ __forceinline__ Epilogue(const LayerArgs &p, Shared &s, int tid)
+        : p(p), s(s), tid(tid), warp(tid >> 5), lane(tid & 31), g((tid & 31) >> 2), t4(tid & 3),
+          per(ADAPT ? p.R8 * (DOWN ? 1 : p.n13) : 1), lot(kVFloats / per & ~(kBatchCols - 1)) {}
+
+    // The weights and adapters of a group's pairs.  A barrier has to follow.
+    __device__ __forceinline__ void note(const Part &x, Pairs &o) {
+        if (warp >= 2) return;
+        int slot = -1;
+        if (tid < x.n) {
+            const int pair = s.list[x.at + tid];
+            if (DOWN) o.weight[tid] = p.topk_w ? p.topk_w[pair] : 1.f;
+            if (ADAPT) slot = slot_of(p, pair / p.K, false);
+        }
+        if (!ADAPT) return;
+        o.slot[tid] = slot;
+        o.rank[tid] = slot >= 0 ? p.rank[slot] : 0;
+        int left = __shfl_up_sync(kAll, slot, 1);
+        if (lane == 0) left = -1;  // an adapter that goes on past column 32 begins there again
+        const unsigned starts = __ballot_sync(kAll, slot >= 0 && slot != left);
+        if (lane == 0) ((unsigned *)&o.starts)[warp] = starts;
+    }
+
+    // What a unit reads of the adapters, to L2 ahead of its use: rows of B, and of A2 two lines each.
+    __device__ __forceinline__ void prefetch(const Part &x, const Pairs &o) {
+        for (int k = warp; k < x.n; k += kEpiThreads / 32) {
+            if (!(o.starts >> k & 1)) continue;
+            const int slot = o.slot[k], rank = o.rank[k], rs = (rank + 7) & ~7;
+            for (int t = 0; t < (DOWN ? 1 : 2); ++t) {
+                const int which = DOWN ? 2 : t ? p.n13 - 1 : 0, row0 = x.m * (DOWN ? kRows : kTile);
+                const int there = min(DOWN ? kRows : kTile, (DOWN ? p.D : p.F) - row0);
+                const uint16_t *b = p.B[which] + (long long)slot * p.b_ss[which] +
+                                    ((long long)x.e * p.b_rows[which] + (t ? p.b_up : 0) + row0) * rs;
+                for (int at = lane * 64; at < there * rs; at += 32 * 64) prefetch_l2(b + at);
+            }
+            const int f0 = x.m * kTile + (lane & 1) * (kTile / 2);
+            if (!DOWN && f0 < p.F)
+                for (int r = lane >> 1; r < rank; r += 16)
+                    prefetch_l2(p.A[2] + (long long)slot * p.a_ss[2] + (long long)x.e * p.a_es[2] + (long long)r * p.F + f0);
         }
     }
-}
 
-template <bool DOWN>
+    // v of a lot of a group's pairs, to shared memory: scale A x as shrink13 left it (up), or scale A2 h, the sum of
+    // its parts, of which four lanes take one each in turn (down).  A barrier has to follow.
+    __device__ __forceinline__ void fill(const Part &x, const Pairs &o, int b0) {
+        const int n = min(lot, x.n - b0);
+        if (DOWN) {
+            const int parts = (p.F + kTile - 1) / kTile;
+            const unsigned quad = 0xfu << (lane & 28);
+#pragma unroll 2
+            for (int i = tid >> 2; i < n * per; i += kEpiThreads / 4) {
+                const int k = b0 + i / per, r = i - (k - b0) * per;
+                float sum = 0.f;
+                if (r < o.rank[k]) {
+                    const float *in = p.v2 + (long long)s.list[x.at + k] * parts * per + r;
+#pragma unroll 4
+                    for (int m = t4; m < parts; m += 4) sum += __ldcg(in + (long long)m * per);
+                    sum *= p.scale[o.slot[k]];
+                }
+                sum += __shfl_xor_sync(quad, sum, 1);
+                sum += __shfl_xor_sync(quad, sum, 2);
+                if (t4 == 0) s.u.e.v[i] = sum;
+            }
+        } else {
+            for (int i = tid * 4; i < n * per; i += kEpiThreads * 4) {
+                const int k = b0 + i / per, r = i - (k - b0) * per, pair = s.list[x.at + k];
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (o.slot[k] >= 0) f = __ldcg((const float4 *)(p.v13 + (long long)(p.shared ? pair / p.K : pair) * 2 * p.R8 + r));
+                *(float4 *)&s.u.e.v[i] = f;
+            }
+        }
+    }
+
+    // Rows of B for 16 ranks of an adapter, four such at a time, in the order of eight columns' adapters.
+    struct Rows {
+        uint2 w[4][4];
+        int run[4], r0[4];
+        int left, r;  // adapters to come (the first of them from rank r on)
+    };
+    __device__ __forceinline__ int runs(const Pairs &o, int b0) const {  // columns of eight where an adapter begins or goes on
+        return ((int)(o.starts >> b0) & 0xff) | (o.slot[b0] >= 0 ? 1 : 0);
+    }
+    __device__ __forceinline__ int tile() const { return DOWN ? 0 : warp >> 2; }
+    __device__ __forceinline__ void ask(Rows &q, const Part &x, const Pairs &o, int b0) {
+        const int which = DOWN ? 2 : tile() ? p.n13 - 1 : 0, rows = DOWN ? p.D : p.F;
+        const int row0 = x.m * (DOWN ? kRows : kTile) + (DOWN ? warp : warp & 3) * 32 + g;
+        const long long brow = (long long)x.e * p.b_rows[which] + (tile() ? p.b_up : 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            q.run[k] = -1;
+            q.r0[k] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q.w[k][j] = make_uint2(0, 0);
+            if (!q.left) continue;
+            const int run = __ffs(q.left) - 1, rank = o.rank[b0 + run], rs = (rank + 7) & ~7, r = q.r + t4 * 4;
+            const uint16_t *b = p.B[which] + (long long)o.slot[b0 + run] * p.b_ss[which] + brow * rs + r;
+            q.run[k] = run;
+            q.r0[k] = q.r;
+            if (r < rs)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q.w[k][j] = __ldg((const uint2 *)(b + (long long)min(row0 + j * 8, rows - 1) * rs));
+            q.r += 16;
+            if (q.r >= rank) {
+                q.r = 0;
+                q.left &= q.left - 1;
+            }
+        }
+    }
+    // B v of eight columns from b0 on for the unit's 256 rows, to s.u.e.delta: a warp takes 32 rows.  The
+    // first rows of B may have been asked for.  A barrier has to follow.
+    __device__ __forceinline__ void rows(Rows &q, bool asked, const Part &x, const Pairs &o, int b0) {
+        float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int col = b0 + g, all = runs(o, b0);
+        const int mine = col < x.n && o.slot[col] >= 0 ? 31 - __clz(all & ((2 << g) - 1)) : -2;  // the run of this lane's column
+        const float *v = s.u.e.v + col % lot * per + (p.n13 == 2 && tile() ? p.R8 : 0) + t4 * 4;
+        if (!asked) q.left = all, q.r = 0;
+#pragma unroll 1
+        for (;;) {
+            if (!asked) ask(q, x, o, b0);
+            asked = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (q.run[k] < 0) break;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q.run[k] == mine && q.r0[k] + t4 * 4 < p.R8) f = *(const float4 *)(v + q.r0[k]);
+                uint32_t hi[2], lo[2];
+                split(f.x, f.y, hi[0], lo[0]);
+                split(f.z, f.w, hi[1], lo[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    bgmv::mma16816(d[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, hi[0], hi[1]);
+                    bgmv::mma16816(d[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, lo[0], lo[1]);
+                }
+            }
+            if (!q.left) break;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s.u.e.delta[t4 * 2 + (k & 1)][warp * 32 + j * 16 + g + (k >> 1) * 8] = d[j][k];
+    }
+
+    // 16 ranks of an adapter's A2, this unit's columns of them: what a warp multiplies with h at a time (up).
+    struct Task {
+        uint4 w[4][2];
+        unsigned long long left;  // adapters from the task's on
+        int r0, rank, skip;       // skip: tasks from this one to the next of the warp
+    };
+    __device__ __forceinline__ bool next_task(Task &q, const Part &x, const Pairs &o) {
+        for (; q.left; q.left &= q.left - 1, q.r0 = 0) {
+            q.rank = o.rank[__ffsll(q.left) - 1];
+            const int tiles = (q.rank - q.r0 + 15) / 16;
+            if (q.skip < tiles) break;
+            q.skip -= tiles;
+        }
+        if (!q.left) return false;
+        q.r0 += q.skip * 16;
+        q.skip = kEpiThreads / 32;
+        const int f0 = x.m * kTile + t4 * 8;
+        const uint16_t *A = p.A[2] + (long long)o.slot[__ffsll(q.left) - 1] * p.a_ss[2] + (long long)x.e * p.a_es[2] + f0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                q.w[j][k] = f0 + j * 32 < p.F ? __ldg((const uint4 *)(A + (long long)min(q.r0 + k * 8 + g, q.rank - 1) * p.F + j * 32))
+                                              : make_uint4(0, 0, 0, 0);
+        return true;
+    }
+    __device__ __forceinline__ void run_task(const Task &q, const Part &x, const Pairs &o, int parts) {
+        const int run = __ffsll(q.left) - 1, slot = o.slot[run];
+        const unsigned long long next = q.left & (q.left - 1);
+        int end = next ? __ffsll(next) - 1 : x.n;
+        while (o.slot[end - 1] != slot) --end;  // pairs without an adapter come behind it
+#pragma unroll 1
+        for (int c = run; c < end; c += 8) {
+            float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const int col = min(c + g, kGroup - 1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 b = *(const uint4 *)&s.u.e.h[k][col][j * 32 + t4 * 8];
+                    bgmv::mma16816(d[k], q.w[j][0].x, q.w[j][1].x, q.w[j][0].y, q.w[j][1].y, b.x, b.y);
+                    bgmv::mma16816(d[k], q.w[j][0].z, q.w[j][1].z, q.w[j][0].w, q.w[j][1].w, b.z, b.w);
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int at = c + t4 * 2 + (k & 1), r = q.r0 + g + (k >> 1) * 8;
+                if (at < end && r < q.rank) p.v2[((long long)s.list[x.at + at] * parts + x.m) * p.R8 + r] = d[0][k] + d[1][k];
+            }
+        }
+    }
+};
+
+template <bool DOWN, bool ADAPT>
 constexpr size_t stream_smem() {
-    return 1024 + (size_t)Shape<DOWN>::kStages * Shape<DOWN>::kStage + sizeof(Shared);
+    return 1024 + (size_t)Shape<DOWN>::kStages * Shape<DOWN>::kStage + sizeof(SharedOf<DOWN, ADAPT>);
 }
-static_assert(stream_smem<false>() <= 227 * 1024 && stream_smem<true>() <= 227 * 1024, "shared memory of a CTA");
+static_assert(stream_smem<false, true>() <= 227 * 1024 && stream_smem<true, true>() <= 227 * 1024, "shared memory of a CTA");
 
-template <bool DOWN>
+template <bool DOWN, bool ADAPT>
 __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_constant__ StreamArgs q) {
     typedef Shape<DOWN> Sh;
+    typedef SharedOf<DOWN, ADAPT> Shared;
     extern __shared__ __align__(1024) char smem_raw[];
     char *ring = smem_raw + ((1024u - (smem_u32_of(smem_raw) & 1023u)) & 1023u);
     Shared &s = *(Shared *)(ring + (size_t)Sh::kStages * Sh::kStage);
@@ -364,7 +681,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
 
     // Without adapters the kernel before up is the caller's, which may have written
     // topk_ids; shrink13, and up before down, let this one start when those are complete.
-    if (!DOWN && !p.L) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!DOWN && !ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) {
         s.abort = 0;
@@ -399,23 +716,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
 
     if (warp == 0) {
         // ---- copies.  Weights are nobody's results: those of the first stages are asked for before
-        // the kernel before this one is complete, the gathered rows after it.
-        int done = 0;  // blocks asked for
+        // the kernel before this one is complete, the pairs' rows after it.
+        const uint64_t policy = evict_first();
         const auto weights = [&](const Part &x, int k, int st) {
             char *dst = ring + (size_t)st * Sh::kStage;
-            // rows of the expert's second tile that are there at all
-            const bool two = !DOWN || x.m * kRows + kTile < p.D;
-            const int n4 = (x.n + 3) & ~3;
-            tc::mbar_expect_tx(&s.full[st], (two ? kABytes : kABytes / 2) + (uint32_t)n4 * 128 * (DOWN ? 2 : 1));
             if (DOWN) {
-                tc::tma_load_3d(dst, &q.tm_w, k * kBK, x.m * kRows, x.e, &s.full[st]);
-                if (two) tc::tma_load_3d(dst + kABytes / 2, &q.tm_w, k * kBK, x.m * kRows + kTile, x.e, &s.full[st]);
+                const bool two = x.m * kRows + kTile < p.D;  // rows of the second tile that are there at all
+                tc::mbar_expect_tx(&s.full[st], (two ? kABytes : kABytes / 2) + (uint32_t)((x.n + 7) & ~7) * 128 * 2);
+                tma_weights(dst, &q.tm_w, k * kBK, x.m * kRows, x.e, &s.full[st], policy);
+                if (two) tma_weights(dst + kABytes / 2, &q.tm_w, k * kBK, x.m * kRows + kTile, x.e, &s.full[st], policy);
             } else {
-                tc::tma_load_3d(dst, &q.tm_w, k * kBK, x.m * kTile, 2 * x.e, &s.full[st]);
-                tc::tma_load_3d(dst + kABytes / 2, &q.tm_w, k * kBK, x.m * kTile, 2 * x.e + 1, &s.full[st]);
+                tc::mbar_expect_tx(&s.full[st], kABytes + (uint32_t)((x.n + 3) & ~3) * 128);
+                tma_weights(dst, &q.tm_w, k * kBK, x.m * kTile, 2 * x.e, &s.full[st], policy);
+                tma_weights(dst + kABytes / 2, &q.tm_w, k * kBK, x.m * kTile, 2 * x.e + 1, &s.full[st], policy);
             }
         };
-        int ahead = 0;
+        int done = 0, ahead = 0;  // blocks asked for; of the first ones the weights alone
         if (lane == 0) {
             tc::prefetch_tmap(&q.tm_w);
             tc::prefetch_tmap(&q.tm_b);
@@ -425,23 +741,23 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             }
         }
         ahead = __shfl_sync(kAll, ahead, 0);
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("fence.proxy.async.global;" ::: "memory");
+        if (DOWN) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+        }
         bool ok = true;
         for (int u = u_hi; u >= u_lo && ok; --u) {
             const Part x = part_of(q, s, r, u, e_first);
-            // this lane's four rows: of x by token, of h by pair (hi, in the upper lanes lo)
-            const int quad = DOWN ? lane & 15 : lane;
-            const bool mine = quad * 4 < x.n;
+            // this lane's rows: four of x by token, or eight of h (hi, in lanes 8-15 lo)
+            const bool mine = DOWN ? lane < 16 && (lane & 7) * 8 < x.n : lane * 4 < x.n;
+            const uint32_t off =
+                kABytes + (uint32_t)(DOWN ? (lane & 7) * 8 + (lane >> 3) * ((x.n + 7) & ~7) : lane * 4) * 128;
+            const int row = x.pos + (lane & 7) * 8 + (lane >> 3) * p.P;
             int4 rows = make_int4(0, 0, 0, 0);
-            if (mine) {
-                const auto row = [&](int i) {
-                    const int pair = s.list[x.at + min(quad * 4 + i, x.n - 1)];
-                    return DOWN ? pair + (lane >> 4) * p.P : pair / p.K;
-                };
-                rows = make_int4(row(0), row(1), row(2), row(3));
+            if (!DOWN && mine) {
+                const auto token = [&](int i) { return s.list[x.at + min(lane * 4 + i, x.n - 1)] / p.K; };
+                rows = make_int4(token(0), token(1), token(2), token(3));
             }
-            const uint32_t off = kABytes + (uint32_t)(quad * 4 + (DOWN ? (lane >> 4) * ((x.n + 7) & ~7) : 0)) * 128;
             for (int k = x.k0; k < x.k1; ++k) {
                 const int st = done % Sh::kStages;
                 if (done >= ahead) {
@@ -452,10 +768,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                     ok = __shfl_sync(kAll, (int)ok, 0);
                     if (!ok) break;
                 }
-                if (mine) tma_gather4(tc::smem_u32(ring) + st * Sh::kStage + off, &q.tm_b, k * kBK, rows, &s.full[st]);
+                char *dst = ring + (size_t)st * Sh::kStage + off;
+                if (mine) {
+                    if (DOWN) tc::tma_load_2d(dst, &q.tm_b, k * kBK, row, &s.full[st]);
+                    else tma_gather4(tc::smem_u32(dst), &q.tm_b, k * kBK, rows, &s.full[st]);
+                }
                 ++done;
             }
         }
+        if (!DOWN) asm volatile("griddepcontrol.wait;" ::: "memory");
         // every copy has landed before the CTA ends (given up or not: all that was asked for comes)
         if (lane == 0)
             for (int i = max(0, done - Sh::kStages); i < done; ++i)
@@ -473,7 +794,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             if (i >= 2) ok = __all_sync(kAll, wait(&s.acce[buf], (uint32_t)(((i >> 1) - 1) & 1), p, s));
             tc::tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(buf * 2 * Sh::kCols);
-            for (int k = x.k0; k < x.k1 && ok; ++k, ++done) {
+            for (int k = x.k0; k < x.k1 && ok; ++k) {
                 const int st = done % Sh::kStages;
                 ok = __all_sync(kAll, wait(&s.full[st], (uint32_t)((done / Sh::kStages) & 1), p, s));
                 if (!ok) break;
@@ -489,6 +810,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                     tc::mma_commit(&s.empty[st]);
                     if (k == x.k1 - 1) tc::mma_commit(&s.accf[buf]);
                 }
+                ++done;
             }
         }
         // products in flight read the ring and write tensor memory: the next stage's barrier tells their end
@@ -497,213 +819,195 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             land(&s.empty[last % Sh::kStages], (uint32_t)((last / Sh::kStages) & 1));
         }
         __syncwarp();
-    } else {
+    } else if (warp < kEpi0 + kEpiThreads / 32) {
         // ---- epilogue
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         const int tid = threadIdx.x - kEpi0 * 32;
         const int quarter = warp & 3, half = (warp - kEpi0) >> 2, row = quarter * 32 + lane;
-        const int htid = quarter * 32 + lane;  // thread of its half
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         float *const my_part = p.part + (size_t)c * 2 * kGroup * kTile;
         int *const flags = p.flags + (DOWN ? p.grid : 0);
+        typedef Epilogue<DOWN, ADAPT> Epi;
+        Epi epi(p, s, tid);
+        typename Epi::Rows rows;
+        typename Epi::Task task;
+        bool asked = false, waited = false;
+        int now = 0, noted = -1, filled = -1;  // of[now] is of this unit's group; `noted` is noted, `filled` the lot of v that is there
         int i = 0;
+        Part x = part_of(q, s, r, any ? u_hi : 0, e_first);
+        if ((DOWN || ADAPT) && any && x.k1 == q.KB) {
+            epi.note(x, s.of[0]);
+            noted = u_hi / q.MT;
+            bar_sync(1, kEpiThreads);
+            if (ADAPT) epi.prefetch(x, s.of[0]);
+        }
+        if (!ADAPT) asm volatile("griddepcontrol.wait;" ::: "memory");
         for (int u = u_hi; u >= u_lo; --u, ++i) {
-            const Part x = part_of(q, s, r, u, e_first);
             const int buf = i & 1;
-            const bool last = x.k1 == q.KB;
+            const bool last = x.k1 == q.KB, more = u > u_lo;
             const uint32_t acc = tmem + lanes + (uint32_t)(buf * 2 * Sh::kCols);
             const int lo_col = (x.n + 7) & ~7;
-            bar_sync(1, kEpiThreads);  // the last unit's slots are no longer read
-            if (last && tid < x.n) {
-                const int pair = s.list[x.at + tid], slot = slot_of(p, pair / p.K, false);
-                s.slot[tid] = slot;
-                s.rank[tid] = slot >= 0 ? p.rank[slot] : 0;
-                s.scale[tid] = slot >= 0 ? p.scale[slot] : 0.f;
-                s.weight[tid] = p.topk_w ? p.topk_w[pair] : 1.f;
+            const Part y = part_of(q, s, r, more ? u - 1 : u, e_first);  // the next unit
+            int next = now;
+            if (DOWN || ADAPT) {
+                bar_sync(1, kEpiThreads);  // nothing of the last unit is read any more
+                if (more && (u - 1) / q.MT != noted) {
+                    next ^= 1;
+                    noted = (u - 1) / q.MT;
+                    epi.note(y, s.of[next]);
+                }
             }
-            bool ok = wait(&s.accf[buf], (uint32_t)((i >> 1) & 1), p, s);
-            // sums that other CTAs have left of this unit
+            const typename Shared::Pairs &of = s.of[now];
+            bool any_delta = false, ok = true;
             int from = c;
-            if (last && x.k0 > 0) {
-                // the CTA that has the unit's first block: start(f) <= u KB < start(f + 1)
-                from = (int)((long long)u * q.KB * r.n / r.total);
-                while (r.start(from) > u * q.KB) --from;
-                while (r.start(from + 1) <= u * q.KB) ++from;
-                if (tid < c - from) {
-                    int polls = 0;
-                    while (ok && ld_acquire_gpu(flags + from + tid) == 0) {
-                        if (*(volatile int *)&s.abort) ok = false;
-                        else if (++polls > p.spin_limit) {
-                            note_timeout(p, s);
-                            ok = false;
-                        } else
-                            __nanosleep(64);
-                    }
-                }
-            }
-            // one wait that gave up ends the work of all
-            ok = bar_and(1, kEpiThreads, ok);
-            if (!ok) break;
-            tc::tc_fence_after();
-            int turn = 0;
 #pragma unroll 1
-            for (int col = half * 4; col < x.n; col += 8) {
-                float g[4], v[4];  // gate and up; or the two tiles' rows
-                tmem_ld4(acc + col, g);
-                tmem_ld4(acc + Sh::kCols + col, v);
-                if (DOWN) {
-                    float gl[4], vl[4];
-                    tmem_ld4(acc + lo_col + col, gl);
-                    tmem_ld4(acc + Sh::kCols + lo_col + col, vl);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) g[j] += gl[j], v[j] += vl[j];
-                } else {
-                    tc::tmem_wait_ld();
-                }
-                if (!last) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        __stcg(my_part + (size_t)(col + j) * kTile + row, g[j]);
-                        __stcg(my_part + (size_t)(kGroup + col + j) * kTile + row, v[j]);
-                    }
-                    continue;
-                }
-                for (int f = from; f < c; ++f) {
-                    const float *o = p.part + (size_t)f * 2 * kGroup * kTile;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        g[j] += __ldcg(o + (size_t)(col + j) * kTile + row);
-                        v[j] += __ldcg(o + (size_t)(kGroup + col + j) * kTile + row);
-                    }
-                }
-                int pair[4], slot[4], rank[4], most = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = min(col + j, x.n - 1);
-                    pair[j] = s.list[x.at + k];
-                    slot[j] = s.slot[k];
-                    rank[j] = col + j < x.n ? s.rank[k] : 0;
-                    most = max(most, rank[j]);
-                }
-                if (!DOWN) {
-                    const int f = x.m * kTile + row;
-                    const bool there = f < p.F;
-                    if (most && there) {
-                        const uint16_t *b[4];
-                        const float *vv[4];
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const int n = t ? p.n13 - 1 : 0, first = t ? p.b_up : 0;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int rs = (rank[j] + 7) & ~7;
-                                b[j] = p.B[n] + (long long)slot[j] * p.b_ss[n] + ((long long)x.e * p.b_rows[n] + first + f) * rs;
-                                vv[j] = p.v13 + ((long long)pair[j] * 2 + t) * p.R;
-                            }
-                            expand_rows<4>(t ? v : g, b, vv, rank, most);
+            for (int b0 = 0; b0 < x.n; b0 += kBatchCols) {
+                const bool end = b0 + kBatchCols >= x.n;
+                bool delta = false;
+                if (ADAPT) {
+                    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+                    waited = true;
+                    delta = last && epi.runs(of, b0);
+                    any_delta |= delta;
+                    if (delta) {
+                        const int lot = (u / q.MT) * kGroup + b0 / epi.lot;
+                        if (lot != filled) {
+                            epi.fill(x, of, b0 / epi.lot * epi.lot);
+                            bar_sync(1, kEpiThreads);
                         }
+                        filled = lot;
+                        epi.rows(rows, asked, x, of, b0);
+                        asked = false;
                     }
-                    float(*sh)[kTile + 4] = s.u.h[half][turn];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float h = there ? activation(g[j], p.gelu) * v[j] : 0.f;
-                        if (most) sh[j][row] = h;
-                        if (there && col + j < x.n) {
-                            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                            const __nv_bfloat16 lo = __float2bfloat16_rn(h - __bfloat162float(hi));
-                            p.h[(long long)pair[j] * p.F + f] = *(const uint16_t *)&hi;
-                            p.h[(long long)(p.P + pair[j]) * p.F + f] = *(const uint16_t *)&lo;
-                        }
+                    bar_sync(1, kEpiThreads);
+                    if (b0 == 0 && more) epi.prefetch(y, s.of[next]);
+                    // rows of B of the columns after these, and rows of A2, are on their way while these are worked on
+                    const Part &z = end ? y : x;
+                    const typename Shared::Pairs &oz = end ? s.of[next] : of;
+                    const int bz = end ? 0 : b0 + kBatchCols;
+                    if (end ? more : last) {
+                        rows.left = epi.runs(oz, bz);
+                        rows.r = 0;
+                        asked = rows.left != 0;
+                        if (asked) epi.ask(rows, z, oz, bz);
                     }
-                    if (most) {
-                        turn ^= 1;
-                        bar_sync(2 + half, kEpiThreads / 2);
-                        // this warp's pair: its column's part of A2 h
-                        const int j = quarter, k = min(col + j, x.n - 1), mine = col + j < x.n ? s.rank[k] : 0;
-                        if (mine) {
-                            const int f0 = x.m * kTile + lane * 4;
-                            const float4 h4 = *(const float4 *)&sh[j][lane * 4];
-                            const uint16_t *A = p.A[2] + (long long)s.slot[k] * p.a_ss[2] + (long long)x.e * p.a_es[2] + f0;
-                            float *out = p.v2 + ((long long)s.list[x.at + k] * q.MT + x.m) * p.R;
-                            for (int r0 = 0; r0 < mine; r0 += 8) {
-                                float d[8];
-#pragma unroll
-                                for (int t = 0; t < 8; ++t) {
-                                    uint2 w = make_uint2(0, 0);
-                                    if (r0 + t < mine && f0 < p.F) w = __ldg((const uint2 *)(A + (long long)(r0 + t) * p.F));
-                                    d[t] = bf16lo(w.x) * h4.x + bf16hi(w.x) * h4.y + bf16lo(w.y) * h4.z + bf16hi(w.y) * h4.w;
-                                }
-                                // eight sums over 32 lanes: halves of the values change lanes, so that 8 lanes end with one each
-#pragma unroll
-                                for (int t = 0; t < 4; ++t) {
-                                    const float give = lane & 16 ? d[t] : d[t + 4], keep = lane & 16 ? d[t + 4] : d[t];
-                                    d[t] = keep + __shfl_xor_sync(kAll, give, 16);
-                                }
-#pragma unroll
-                                for (int t = 0; t < 2; ++t) {
-                                    const float give = lane & 8 ? d[t] : d[t + 2], keep = lane & 8 ? d[t + 2] : d[t];
-                                    d[t] = keep + __shfl_xor_sync(kAll, give, 8);
-                                }
-                                {
-                                    const float give = lane & 4 ? d[0] : d[1], keep = lane & 4 ? d[1] : d[0];
-                                    d[0] = keep + __shfl_xor_sync(kAll, give, 4);
-                                }
-                                d[0] += __shfl_xor_sync(kAll, d[0], 2);
-                                d[0] += __shfl_xor_sync(kAll, d[0], 1);
-                                const int rr = r0 + (lane & 16 ? 4 : 0) + (lane & 8 ? 2 : 0) + (lane & 4 ? 1 : 0);
-                                if (!(lane & 3) && rr < mine) out[rr] = d[0];
+                    if (!DOWN && end && any_delta) {
+                        task.left = of.starts;
+                        task.r0 = 0;
+                        task.skip = tid >> 5;
+                        epi.next_task(task, x, of);
+                    }
+                }
+                if (b0 == 0) {
+                    ok = wait(&s.accf[buf], (uint32_t)((i >> 1) & 1), p, s);
+                    // sums that other CTAs have left of this unit
+                    if (last && x.k0 > 0) {
+                        // the CTA that has the unit's first block: start(f) <= u KB < start(f + 1)
+                        from = (int)((long long)u * q.KB * r.n / r.total);
+                        while (r.start(from) > u * q.KB) --from;
+                        while (r.start(from + 1) <= u * q.KB) ++from;
+                        if (tid < c - from) {
+                            int polls = 0;
+                            while (ok && ld_acquire_gpu(flags + from + tid) == 0) {
+                                if (*(volatile int *)&s.abort) ok = false;
+                                else if (++polls > p.spin_limit) {
+                                    note_timeout(p, s);
+                                    ok = false;
+                                } else
+                                    __nanosleep(64);
                             }
                         }
                     }
-                } else {
-                    float(*sv)[LORA_MAX_RANK] = s.u.v2[half];
-                    const int parts = (p.F + kTile - 1) / kTile;
-                    if (p.L) {
-                        bar_sync(2 + half, kEpiThreads / 2);  // the last four pairs' sums are no longer read
+                    // one wait that gave up ends the work of all
+                    ok = bar_and(1, kEpiThreads, ok);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                }
+                const int col = b0 + half * 4;
+                if (col < x.n) {
+                    float g[4], v[4];  // gate and up; or the two tiles' rows
+                    tmem_ld4(acc + col, g);
+                    tmem_ld4(acc + Sh::kCols + col, v);
+                    if (DOWN) {
+                        float gl[4], vl[4];
+                        tmem_ld4(acc + lo_col + col, gl);
+                        tmem_ld4(acc + Sh::kCols + lo_col + col, vl);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) g[j] += gl[j], v[j] += vl[j];
+                    } else {
+                        tc::tmem_wait_ld();
+                    }
+                    if (!last) {
+#pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int k = min(col + j, x.n - 1), mine = col + j < x.n ? s.rank[k] : 0;
-                            const float *in = p.v2 + (long long)s.list[x.at + k] * parts * p.R;
-                            for (int rr = htid; rr < mine; rr += kEpiThreads / 2) {
-                                float sum = 0.f;
-                                for (int m = 0; m < parts; ++m) sum += __ldcg(in + (long long)m * p.R + rr);
-                                sv[j][rr] = sum * s.scale[k];
-                            }
+                            __stcg(my_part + (size_t)(col + j) * kTile + row, g[j]);
+                            __stcg(my_part + (size_t)(kGroup + col + j) * kTile + row, v[j]);
                         }
-                        bar_sync(2 + half, kEpiThreads / 2);
-                    }
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int d = x.m * kRows + t * kTile + row;
-                        if (d >= p.D) continue;
-                        if (most) {
-                            const uint16_t *b[4];
-                            const float *vv[4];
+                    } else {
+                        for (int f = from; f < c; ++f) {
+                            const float *o = p.part + (size_t)f * 2 * kGroup * kTile;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const int rs = (rank[j] + 7) & ~7;
-                                b[j] = p.B[2] + (long long)slot[j] * p.b_ss[2] + ((long long)x.e * p.b_rows[2] + d) * rs;
-                                vv[j] = sv[j];
+                                g[j] += __ldcg(o + (size_t)(col + j) * kTile + row);
+                                v[j] += __ldcg(o + (size_t)(kGroup + col + j) * kTile + row);
                             }
-                            expand_rows<4>(t ? v : g, b, vv, rank, most);
                         }
+                        const int at = x.m * (DOWN ? kRows : kTile) + row;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (col + j < x.n) __stcg(p.y + (long long)pair[j] * p.D + d, (t ? v[j] : g[j]) * s.weight[col + j]);
+                        for (int j = 0; j < 4; ++j) {
+                            if (col + j >= x.n) break;
+                            if (delta) {
+                                g[j] += s.u.e.delta[half * 4 + j][row];
+                                v[j] += s.u.e.delta[half * 4 + j][kTile + row];
+                            }
+                            if (DOWN) {
+                                float *y = p.y + (long long)s.list[x.at + col + j] * p.D + at;
+                                const float w = of.weight[col + j];
+                                if (at < p.D) __stcg(y, g[j] * w);
+                                if (at + kTile < p.D) __stcg(y + kTile, v[j] * w);
+                            } else {
+                                uint16_t hi = 0, lo = 0;
+                                if (at < p.F) {
+                                    split(activation(g[j], p.gelu) * v[j], hi, lo);
+                                    p.h[(long long)(x.pos + col + j) * p.F + at] = hi;
+                                    p.h[(long long)(p.P + x.pos + col + j) * p.F + at] = lo;
+                                }
+                                if (ADAPT) {
+                                    s.u.e.h[0][col + j][row] = hi;
+                                    s.u.e.h[1][col + j][row] = lo;
+                                }
+                            }
+                        }
                     }
                 }
+                if (ADAPT && last) bar_sync(1, kEpiThreads);  // delta is no longer read; at the end, all of h is there
+            }
+            if (!ok) {
+                if (!last) asm volatile("bar.arrive 3, %0;" ::"r"(kEpiThreads + 32) : "memory");
+                break;
             }
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s.acce[buf]);
-            if (!last) {
-                __threadfence();
-                bar_sync(1, kEpiThreads);
-                if (tid == 0) {
-                    __threadfence();
-                    asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(flags + c), "r"(1) : "memory");
+            if (!last) asm volatile("bar.arrive 3, %0;" ::"r"(kEpiThreads + 32) : "memory");
+            if (ADAPT && !DOWN && any_delta) {
+#pragma unroll 1
+                while (task.left) {
+                    epi.run_task(task, x, of, q.MT);
+                    if (!epi.next_task(task, x, of)) break;
                 }
             }
+            x = y;
+            now = next;
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    } else {
+        // ---- whoever waits for this CTA's sums of a shared unit (its first one) is told
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (any && part_of(q, s, r, u_hi, e_first).k1 < q.KB) {
+            bar_sync(3, kEpiThreads + 32);
+            if (lane == 0)
+                asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p.flags + (DOWN ? p.grid : 0) + c), "r"(1) : "memory");
         }
     }
     tc::tc_fence_before();
@@ -760,7 +1064,7 @@ struct Carve {
     size_t flags, part, v13, h, v2, y, bytes;
 };
 Carve carve(const lora_moe_layer_desc_t &d, const lora_pool_t *pool, int64_t T, int sms) {
-    const size_t P = (size_t)T * d.top_k, R = pool ? pool->desc.max_rank : 0;
+    const size_t P = (size_t)T * d.top_k, R = pool ? pool->R8 : 0;
     Carve c;
     c.flags = 0;
     c.part = c.flags + align256((size_t)2 * sms * 4);
@@ -777,6 +1081,11 @@ struct Device {
 };
 Device g_devices[64];
 
+template <bool DOWN, bool ADAPT>
+cudaError_t set_smem() {
+    return cudaFuncSetAttribute(stream_kernel<DOWN, ADAPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stream_smem<DOWN, ADAPT>());
+}
+
 // SM count of the current device; the kernels' attributes are set on the way.
 cudaError_t device_sms(int &dev, int &sms) {
     cudaError_t e = cudaGetDevice(&dev);
@@ -785,17 +1094,15 @@ cudaError_t device_sms(int &dev, int &sms) {
     sms = g_devices[dev].sms.load(std::memory_order_acquire);
     if (sms) return cudaSuccess;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(stream_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stream_smem<false>())) !=
-            cudaSuccess ||
-        (e = cudaFuncSetAttribute(stream_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)stream_smem<true>())) !=
-            cudaSuccess)
+    if ((e = set_smem<false, false>()) != cudaSuccess || (e = set_smem<false, true>()) != cudaSuccess ||
+        (e = set_smem<true, false>()) != cudaSuccess || (e = set_smem<true, true>()) != cudaSuccess)
         return e;
     g_devices[dev].sms.store(sms, std::memory_order_release);
     return cudaSuccess;
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cudaLaunchAttribute at[1];
@@ -803,7 +1110,7 @@ cudaError_t launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -882,6 +1189,8 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
         const lora_pool_desc_t &q = pool->desc;
         p.L = q.max_loras;
         p.R = q.max_rank;
+        p.R8 = pool->R8;
+        p.shared = q.shared_outer;
         p.n13 = q.n_w13_slices;
         p.b_up = p.n13 == 2 ? 0 : d.d_mlp;
         p.rank = pool->d_rank;
@@ -908,13 +1217,24 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     if (!lora_make_tmap_3d(&up.tm_w, w13, d.d_model, d.d_mlp, 2LL * d.n_experts, ld_w13, (long long)d.d_mlp * ld_w13, kBK, kTile) ||
         !lora_make_tmap_2d(&up.tm_b, x, d.d_model, T, ldx, kBK, 1, true) ||
         !lora_make_tmap_3d(&down.tm_w, w2, d.d_mlp, d.d_model, d.n_experts, ld_w2, (long long)d.d_model * ld_w2, kBK, kTile) ||
-        !lora_make_tmap_2d(&down.tm_b, p.h, d.d_mlp, 2LL * p.P, d.d_mlp, kBK, 1, true))
+        !lora_make_tmap_2d(&down.tm_b, p.h, d.d_mlp, 2LL * p.P, d.d_mlp, kBK, 8, true))
         return LORA_ERR_UNSUPPORTED;
     up.a = down.a = p;
-    if (pool)
-        LORA_CUDA_TRY(launch(shrink13_kernel, (unsigned)lora_ceil_div((int64_t)p.P * 2 * p.R, kThreads / 32), kThreads, 0, s, p));
-    LORA_CUDA_TRY(launch(stream_kernel<false>, (unsigned)sms, kStreamThreads, stream_smem<false>(), s, up));
-    LORA_CUDA_TRY(launch(stream_kernel<true>, (unsigned)sms, kStreamThreads, stream_smem<true>(), s, down));
+    if (pool) {
+        // experts, or as many sets of slots as there can be; CTAs that share the batches of one
+        const int sets = !p.shared ? p.E : p.L < T ? p.L : T, chunks = lora_ceil_div(p.R, kRanks);
+        const int slots = 4 * sms / (sets * p.n13 * chunks), share = slots < 1 ? 1 : slots > 8 ? 8 : slots;
+        const dim3 grid((unsigned)sets, (unsigned)(p.n13 * chunks), (unsigned)(share < T ? share : T));
+        LORA_CUDA_TRY(launch(shrink13_kernel, grid, kThreads, 0, s, p, chunks));
+    }
+    const unsigned grid = (unsigned)sms;
+    if (pool) {
+        LORA_CUDA_TRY(launch(stream_kernel<false, true>, grid, kStreamThreads, stream_smem<false, true>(), s, up));
+        LORA_CUDA_TRY(launch(stream_kernel<true, true>, grid, kStreamThreads, stream_smem<true, true>(), s, down));
+    } else {
+        LORA_CUDA_TRY(launch(stream_kernel<false, false>, grid, kStreamThreads, stream_smem<false, false>(), s, up));
+        LORA_CUDA_TRY(launch(stream_kernel<true, false>, grid, kStreamThreads, stream_smem<true, false>(), s, down));
+    }
     const int64_t pieces = (int64_t)T * (d.d_model / 8), most = pieces > 2 * sms ? pieces : 2 * sms;
     LORA_CUDA_TRY(launch(combine_kernel, (unsigned)lora_ceil_div(most, kThreads), kThreads, 0, s, p));
     return LORA_OK;
