@@ -119,25 +119,35 @@ __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &
 // tokens), sorts them by slot and reads an adapter's rows once for up to 8 of them: 16 ranks x 8
 // pairs is one m16n8k16 product, whose operands come from global memory straight into registers
 // (any order of k will do as long as both have the same), a warp per eighth of the columns.
-// Several CTAs (gridDim.z) share an expert's batches of 8.  Bound by the adapters' bytes for
-// many pairs, by its chain of dependent reads for few (ids and slots, ranks, rows).
+// Several CTAs (gridDim.z) share an expert's batches of 8.  Bound by its chain of dependent reads (ids
+// and slots, then rows; rank and scale come with the rows, which are zeros past a rank) and by
+// the adapters' bytes.
 constexpr int kBatch = 8, kRanks = 16;
-__global__ void __launch_bounds__(kThreads, 4) shrink13_kernel(const LayerArgs p, int chunks) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ uint32_t found[kMaxP], key[kMaxP];  // slot << 12 | pair; sorted
-    __shared__ float sums[kWarps][kRanks][kBatch];
+__global__ void __launch_bounds__(kThreads, 3) shrink13_kernel(const LayerArgs p, int chunks) {
+    constexpr int kWarps = kThreads / 32, kAhead = 4;
+    extern __shared__ uint32_t found[];  // slot << 12 | pair; behind them in order
+    __shared__ float sums[2][kWarps][kRanks][kBatch];
     __shared__ int s_n;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int which = (int)blockIdx.y / chunks, r0 = (int)blockIdx.y % chunks * kRanks;
     if (tid == 0) s_n = 0;
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    __syncthreads();
     const int count = p.shared ? p.T : p.P, sets = gridDim.x, me = blockIdx.x;
-#pragma unroll 4
-    for (int i = tid; i < count; i += kThreads) {
-        const int e = p.shared ? me : p.ids[i], a = p.idx[p.shared ? i : i / p.K];
-        if (e == me && a >= 0 && a < p.L && (!p.shared || a % sets == me)) found[atomicAdd(&s_n, 1)] = (uint32_t)a << 12 | (uint32_t)i;
+    uint32_t *key = found + count;
+    for (int i0 = tid; i0 < count; i0 += kAhead * kThreads) {
+        int e[kAhead], a[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * kThreads;
+            e[j] = i >= count ? -1 : p.shared ? me : p.ids[i];
+            a[j] = i >= count ? -1 : p.idx[p.shared ? i : i / p.K];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (e[j] == me && a[j] >= 0 && a[j] < p.L && (!p.shared || a[j] % sets == me))
+                found[atomicAdd(&s_n, 1)] = (uint32_t)a[j] << 12 | (uint32_t)(i0 + j * kThreads);
     }
     __syncthreads();
     const int n = s_n;
@@ -151,46 +161,54 @@ __global__ void __launch_bounds__(kThreads, 4) shrink13_kernel(const LayerArgs p
     __syncthreads();
     const int m = p.n13 == 2 ? which : 0;
     const int g = lane >> 2, c0 = (lane & 3) * 8;  // row of the fragments, first of this lane's 8 columns of 32
-    for (int at = 0, b = 0; at < n; ++b) {
+    for (int at = 0, b = 0, turn = 0; at < n; ++b) {
         const int slot = (int)(key[at] >> 12);
         int few = 1;
         while (few < kBatch && at + few < n && (int)(key[at + few] >> 12) == slot) ++few;
         const int first = at;
         at += few;
         if (b % (int)gridDim.z != (int)blockIdx.z) continue;
-        const int rank = p.enabled[slot] ? p.rank[slot] : 0;
+        const int rank = p.rank[slot];
+        const float scale = p.scale[slot];
         const uint16_t *A = p.A[m] + (long long)slot * p.a_ss[m] + (p.shared ? 0 : (long long)me * p.a_es[m]);
         const int i = (int)(key[first + min(g, few - 1)] & 0xfffu);
-        const uint16_t *x = p.x + (long long)(p.shared ? i : i / p.K) * p.ldx;
+        const uint16_t *x = p.x + (long long)(p.shared ? i : i / p.K) * p.ldx + c0;
+        const uint16_t *row0 = A + (long long)min(r0 + g, p.R - 1) * p.D + c0, *row1 = A + (long long)min(r0 + g + 8, p.R - 1) * p.D + c0;
         float d[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r0 < rank) {
-            const uint16_t *row0 = A + (long long)min(r0 + g, rank - 1) * p.D, *row1 = A + (long long)min(r0 + g + 8, rank - 1) * p.D;
-#pragma unroll 4
-            for (int c = warp * 32 + c0; c - c0 < p.D; c += kWarps * 32) {
-                uint4 a0 = make_uint4(0, 0, 0, 0), a1 = a0, v = a0;
-                if (c < p.D) {
-                    a0 = ldg_stream(row0 + c);
-                    a1 = ldg_stream(row1 + c);
-                    v = __ldg((const uint4 *)(x + c));
+#pragma unroll 1
+        for (int c = warp * 32; c < p.D; c += kAhead * kWarps * 32) {
+            uint4 a0[kAhead], a1[kAhead], v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int k = c + j * kWarps * 32;
+                a0[j] = a1[j] = v[j] = make_uint4(0, 0, 0, 0);
+                if (k + c0 < p.D) {
+                    a0[j] = ldg_stream(row0 + k);
+                    a1[j] = ldg_stream(row1 + k);
+                    v[j] = __ldg((const uint4 *)(x + k));
                 }
-                bgmv::mma16816(d, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-                bgmv::mma16816(d, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                bgmv::mma16816(d, a0[j].x, a1[j].x, a0[j].y, a1[j].y, v[j].x, v[j].y);
+                bgmv::mma16816(d, a0[j].z, a1[j].z, a0[j].w, a1[j].w, v[j].z, v[j].w);
             }
         }
-        sums[warp][g][(lane & 3) * 2] = d[0];
-        sums[warp][g][(lane & 3) * 2 + 1] = d[1];
-        sums[warp][g + 8][(lane & 3) * 2] = d[2];
-        sums[warp][g + 8][(lane & 3) * 2 + 1] = d[3];
+        float(*sum)[kRanks][kBatch] = sums[turn];
+        turn ^= 1;
+        sum[warp][g][(lane & 3) * 2] = d[0];
+        sum[warp][g][(lane & 3) * 2 + 1] = d[1];
+        sum[warp][g + 8][(lane & 3) * 2] = d[2];
+        sum[warp][g + 8][(lane & 3) * 2 + 1] = d[3];
         __syncthreads();
         const int r = r0 + (tid & 15), j = tid >> 4;
-        if (j < few && r < p.R8 && rank > 0) {
+        if (j < few && r < p.R8) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += sums[w][tid & 15][j];
-            v = r < rank ? v * p.scale[slot] : 0.f;  // ranks past the adapter's meet zeros: finite, whatever x is
-            p.v13[((long long)(key[first + j] & 0xfffu) * 2 + which) * p.R8 + r] = v;
+            for (int w = 0; w < kWarps; ++w) v += sum[w][tid & 15][j];
+            // ranks past the adapter's meet zeros: finite, whatever x is
+            p.v13[((long long)(key[first + j] & 0xfffu) * 2 + which) * p.R8 + r] = r < rank ? v * scale : 0.f;
         }
-        __syncthreads();
     }
 }
 
@@ -1223,9 +1241,9 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     if (pool) {
         // experts, or as many sets of slots as there can be; CTAs that share the batches of one
         const int sets = !p.shared ? p.E : p.L < T ? p.L : T, chunks = lora_ceil_div(p.R, kRanks);
-        const int slots = 4 * sms / (sets * p.n13 * chunks), share = slots < 1 ? 1 : slots > 8 ? 8 : slots;
+        const int slots = 3 * sms / (sets * p.n13 * chunks), share = slots < 1 ? 1 : slots > 8 ? 8 : slots;
         const dim3 grid((unsigned)sets, (unsigned)(p.n13 * chunks), (unsigned)(share < T ? share : T));
-        LORA_CUDA_TRY(launch(shrink13_kernel, grid, kThreads, 0, s, p, chunks));
+        LORA_CUDA_TRY(launch(shrink13_kernel, grid, kThreads, (size_t)p.P * 8, s, p, chunks));
     }
     const unsigned grid = (unsigned)sms;
     if (pool) {
