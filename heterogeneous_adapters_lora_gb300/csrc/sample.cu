@@ -20,7 +20,7 @@
 //
 // Keys are bf16 bits mapped to integers that grow with the value.  A window is a
 // range of keys that is counted at once:
-//   one     the keys of 0 and of magnitudes in [2^-23, 2^9), 8193 bins: all that
+//   one     the keys of 0 and of magnitudes in (2^-55, 2^9), 16384 places: all that
 //           takes part in most rows
 //   many    otherwise 16 windows of 4096 keys each, in descending order, each
 //           counted when it is asked for, by the first CTA of the cluster alone
@@ -40,8 +40,10 @@ typedef unsigned __int128 u128;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kMagLo = 104 * 128, kMags = 32 * 128;  // magnitudes [2^-23, 2^9) as bf16 bits
-constexpr int kBins = 2 * kMags + 1;
+constexpr int kMagLo = 72 * 128, kMags = 64 * 128;  // magnitudes [2^-55, 2^9) as bf16 bits
+constexpr int kBins = 2 * kMags + 1;                // by magnitude, the sign above it, 0 last
+constexpr int kPlaces = 2 * kMags;                  // of the order; +2^-55 has none
+constexpr int kRounds = kPlaces / kThreads;         // of a place per thread
 constexpr int kMostCtas = 8;
 constexpr int kWinBins = 4096;
 constexpr int kWindows = 65536 / kWinBins;
@@ -71,17 +73,16 @@ __device__ __forceinline__ float value_of(unsigned key) {
 }
 
 // Places of the one window, in descending order of values: positive magnitudes, 0, negative ones.
-// Its bins lie by their bits instead: magnitude, the sign above it, 0 last.
 __device__ __forceinline__ int bin_of_place(int place) {
-    return place < kMags ? kMags - 1 - place : place == kMags ? 2 * kMags : place - 1;
+    return place < kMags - 1 ? kMags - 1 - place : place == kMags - 1 ? 2 * kMags : place;
 }
 __device__ __forceinline__ unsigned key_of_place(int place, int window) {
     if (window >= 0) return (unsigned)(window * kWinBins + kWinBins - 1 - place);
-    if (place == kMags) return 0x8000u;
-    return place < kMags ? 0x8000u | (unsigned)(kMagLo + kMags - 1 - place) : 0x7fffu - (unsigned)(kMagLo + place - kMags - 1);
+    if (place == kMags - 1) return 0x8000u;
+    return place < kMags ? 0x8000u | (unsigned)(kMagLo + kMags - 1 - place) : 0x7fffu - (unsigned)(kMagLo + place - kMags);
 }
 
-// 2^(-2^-j) for j = 1..18 in units of 2^-63, and ln 2 in units of 2^-64.
+// 2^(-2^-j) for j = 1..18 in units of 2^-63.
 __device__ const u64 kRoots[18] = {0x5a827999fcef3242ull, 0x6ba27e656b4eb57aull, 0x75606373ee921c97ull,
                                    0x7a92be8a92436616ull, 0x7d41d96db915019dull, 0x7e9f06067a4360baull,
                                    0x7f4f08ae3dc7c426ull, 0x7fa765aca88f6453ull, 0x7fd3ab290e46d769ull,
@@ -89,7 +90,6 @@ __device__ const u64 kRoots[18] = {0x5a827999fcef3242ull, 0x6ba27e656b4eb57aull,
                                    0x7ffd3a3f50020332ull, 0x7ffe9d1dbc0a75aaull, 0x7fff4e8e6306ed59ull,
                                    0x7fffa74712c3cdfdull, 0x7fffd3a381b1fa29ull, 0x7fffe9d1beed018aull};
 constexpr u64 kOne63 = 1ull << 63;
-constexpr u64 kLn2 = 0xb17217f7d1cf79acull;
 
 __device__ __forceinline__ u64 mul63(u64 a, u64 b) { return __umul64hi(a, b) << 1; }
 
@@ -110,22 +110,26 @@ struct Scale {
     float top;     // the largest logit, times up
 };
 
-// With c = log2(e) / temperature = m 2^e, m in [1, 2): logits times 2^e, and m.  Where that
-// would make the largest logit exceed 2^100, a smaller power does: distinct logits are then
-// at least 2^91 apart, and every weight but the largest is 0 whatever the factor.
+// With temperature = m 2^e, m in [0.5, 1): logits times 2^-e, and log2(e) / m, a quotient and
+// its remainder's.  Where the power would make the largest logit exceed 2^100, a smaller one does: distinct logits
+// are then at least 2^91 apart, and every weight but the largest is 0 whatever the factor.
 __device__ __forceinline__ Scale make_scale(float temperature, float top) {
+    constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kLog2e);
     Scale r;
     int s = -2;
-    double c = 0.0;
+    r.hi = r.lo = 0.f;
     if (temperature < INFINITY) {
-        c = 1.4426950408889634 / (double)temperature;
-        s = max(-126, min(126, ilogb(c)));
+        int e;
+        const float m = frexpf(temperature, &e);
+        s = max(-126, min(126, -e));
         if (top != 0.f) s = min(s, 100 - ilogbf(top));
-        c = fmin(ldexp(c, -s), 0x1p30);
+        r.hi = kLog2e / m;
+        r.lo = (fmaf(-r.hi, m, kLog2e) + kRest) / m;
+        const float rest = exp2f((float)min(-e - s, 30));
+        r.hi *= rest;
+        r.lo *= rest;
     }
     r.up = __int_as_float((s + 127) << 23);
-    r.hi = (float)c;
-    r.lo = (float)(c - (double)r.hi);
     r.top = top * r.up;
     return r;
 }
@@ -147,15 +151,18 @@ __device__ __forceinline__ u64 weight62(const Scale &c, float v, const u64 *pw) 
     float hi, lo;
     distance(c, v, hi, lo);
     if (!(hi < 62.f)) return 0ull;
-    long long y = __float2ll_rn(hi * 0x1p50f) + __float2ll_rn(lo * 0x1p50f);
+    // y in units of 2^-50: its multiple of 2^-24, and the rest, each a 32-bit conversion
+    const int whole = __float2int_rd(hi * 0x1p24f);
+    const int rest = __float2int_rn((lo + (hi - (float)whole * 0x1p-24f)) * 0x1p50f);
+    long long y = ((long long)whole << 26) + rest;
     y = y < 0 ? 0 : y;
-    const u64 f = (u64)y & ((1ull << 50) - 1);
-    const u64 q = __umul64hi((f & 0xffffffffull) << 14, kLn2);  // r ln 2 in units of 2^-64
-    u64 w = kOne63 - (q >> 1) + (__umul64hi(q, q) >> 2);
-    w = mul63(w, pw[f >> 44]);
-    w = mul63(w, pw[64 + ((f >> 38) & 63)]);
-    w = mul63(w, pw[128 + ((f >> 32) & 63)]);
-    return w >> (1 + (int)(y >> 50));
+    const unsigned low = (unsigned)y, high = (unsigned)((u64)y >> 32);  // r; i3 (6 bits), i2, i1, i
+    const unsigned q = __umulhi(low, 0xb17217f8u);                      // r ln 2 in units of 2^-50
+    u64 w = kOne63 - ((u64)q << 13) + (__umulhi(q, q) >> 6);
+    w = mul63(w, pw[high >> 12 & 63]);
+    w = mul63(w, pw[64 + (high >> 6 & 63)]);
+    w = mul63(w, pw[128 + (high & 63)]);
+    return w >> (1 + (high >> 18));
 }
 
 struct Found {
@@ -174,20 +181,20 @@ struct Told {
     int top;       // first place that is not empty
     unsigned low;  // largest key below the one window
     int odd;       // a key in the gaps of the one window, or above it
-    u64 lo, hi, least_lo, least_hi;  // weight of its slice, and of the weights of at least min_p in it
+    u64 lo, hi, least_lo, least_hi;  // weight of its slice, and of the beginning of at least min_p a column
     int n, least_n;
     int matches;   // columns of its part with the chosen key
 };
 
 struct Shared {
-    unsigned bins[kBins + 7];                   // by bits; or a window's in descending order
-    unsigned merged[(kBins / 2 + kThreads) / kThreads * kThreads + kThreads];  // a slice's counts of all CTAs, two CTAs at least
+    unsigned bins[kBins + 7];                         // by bits; or a window's in descending order
+    unsigned list[kPlaces / 2];                       // a slice's entries, where two CTAs or more share the row
     u64 pw[192];
     u64 warp_lo[kWarps], warp_hi[kWarps];  // 128-bit partial sums
-    int warp_n[kWarps];
+    int warp_n[kWarps], last;
     Told told;
     Told all[kMostCtas];  // of every CTA
-    Found found;
+    Found found[3];  // of each step
     Scale scale;
     // many windows
     int coarse[kWindows];
@@ -219,6 +226,7 @@ __device__ __forceinline__ Sums scan(Shared &s, Sums mine, Sums &total) {
     __syncthreads();
     Sums before = {0, 0};
     total = {0, 0};
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
         const u128 m = join(s.warp_hi[w], s.warp_lo[w]);
         if (w < warp) {
@@ -237,7 +245,7 @@ __device__ __forceinline__ Sums scan(Shared &s, Sums mine, Sums &total) {
 // those of a last vector that is not whole.
 template <typename F, typename G>
 __device__ __forceinline__ void each_vector(const uint16_t *row, int begin, int end, int at, int step, F f, G g) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 2;
     const int whole = begin + ((end - begin) & ~7);
     for (int i = begin + at * 8; i < whole; i += kAhead * step * 8) {
         uint4 v[kAhead];
@@ -251,65 +259,103 @@ __device__ __forceinline__ void each_vector(const uint16_t *row, int begin, int 
     if (at == 0)
         for (int i = whole; i < end; ++i) g(i, (unsigned)row[i]);
 }
+// (where time matters less than the size of the code)
 template <typename G>
-__device__ __forceinline__ void each_column(const uint16_t *row, int begin, int end, int at, int step, G g) {
-    each_vector(row, begin, end, at, step,
-                [&](int i, const uint4 &v) {
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void each_column(const uint16_t *row, int end, G g) {
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) g(i + k, u[k >> 1] >> (k & 1) * 16 & 0xffffu);
-                },
-                g);
+    for (int i = threadIdx.x; i < end; i += kThreads) g((unsigned)row[i]);
 }
 
-// Counts of a slice: places [first, first + per) are this thread's, in descending order.
-struct Slice {
-    const unsigned *counts;
-    int base, window;  // merged counts start at place `base`; -1: bins by bits
-    bool by_bits;
-    __device__ __forceinline__ unsigned count(int place) const {
-        if (!by_bits) return counts[place - base];
-        return place < kBins ? counts[bin_of_place(place)] : 0u;
-    }
-    __device__ __forceinline__ u64 weight(const Shared &s, int place) const {
-        return weight62(s.scale, value_of(key_of_place(place, window)), s.pw);
+// What a CTA has of the order: the places that are not empty, as place << 18 | columns (a row has
+// fewer than 2^18), `each` of them to a thread in a row.
+struct Entries {
+    const unsigned *list;
+    int n, each, window;  // window: -1, the one
+    Sums before, own;     // sums ahead of this thread's entries, and theirs
+    __device__ __forceinline__ u64 weight(const Shared &s, unsigned entry) const {
+        return weight62(s.scale, value_of(key_of_place((int)(entry >> 18), window)), s.pw);
     }
 };
+constexpr unsigned kColumns = (1u << 18) - 1;
+static_assert(LORA_MAX_VOCAB <= kColumns && kPlaces <= 1 << 14 && kWinBins <= 1 << 14, "an entry's parts");
 
-// Sums over a thread's places, and over those of them that weigh at least `least`.
-__device__ __forceinline__ void add_up(const Shared &s, const Slice &q, int first, int per, u64 least, Sums &sum, Sums &heavy) {
-    sum = heavy = {0, 0};
+// Writes the entries of places first + j * kThreads * .. : a warp has rounds * 32 places in a row, count(place)
+// columns each; `list` may be where the counts are.
+template <int MAX, typename F>
+__device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int first, int rounds, F count) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    first += warp * rounds * 32 + lane;
+    unsigned c[MAX];
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < MAX; ++j) {
+        c[j] = j < rounds ? count(first + j * 32) : 0u;
+        mine += c[j] != 0u;
+    }
+    mine = (int)__reduce_add_sync(kAll, (unsigned)mine);
+    if (lane == 0) s.warp_n[warp] = mine;
+    __syncthreads();  // (all counts have been read)
+    int at = 0, n = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        at += w < warp ? s.warp_n[w] : 0;
+        n += s.warp_n[w];
+    }
+#pragma unroll
+    for (int j = 0; j < MAX; ++j) {
+        const unsigned some = __ballot_sync(kAll, c[j] != 0u);
+        if (c[j]) list[at + __popc(some & ((1u << lane) - 1))] = (unsigned)(first + j * 32) << 18 | c[j];
+        at += __popc(some);
+    }
+    __syncthreads();
+    return n;
+}
+
+// Sums of the entries in `total`; of their beginning that weighs at least `least` a column in s.told.
+__device__ __forceinline__ void add_up(Shared &s, Entries &q, u64 least, Sums &total) {
+    Sums much = {0, 0};
+    q.own = {0, 0};
+    q.each = (q.n + kThreads - 1) / kThreads;
+    const int begin = min(q.n, (int)threadIdx.x * q.each), end = min(q.n, begin + q.each);
 #pragma unroll 1
-    for (int i = 0; i < per; ++i) {
-        const unsigned c = q.count(first + i);
-        if (!c) continue;
-        const u64 w = q.weight(s, first + i);
-        const u128 m = (u128)w * c;
-        sum.mass += m;
-        sum.n += (int)c;
-        if (w >= least) {
-            heavy.mass += m;
-            heavy.n += (int)c;
-        }
+    for (int i = begin; i < end; ++i) {
+        const unsigned entry = q.list[i];
+        const int c = (int)(entry & kColumns);
+        const u64 w = q.weight(s, entry);
+        q.own.mass += (u128)w * (unsigned)c;
+        q.own.n += c;
+        if (w >= least) much = q.own;
+    }
+    q.before = scan(s, q.own, total);
+    // the last thread that has some ends that beginning
+    if (threadIdx.x == 0) s.last = -1, s.told.least_n = 0, s.told.least_hi = 0, s.told.least_lo = 0;
+    __syncthreads();
+    const unsigned some = __ballot_sync(kAll, much.n > 0);
+    if (some && (threadIdx.x & 31) == 0) atomicMax(&s.last, (int)threadIdx.x + 31 - __clz(some));
+    __syncthreads();
+    if ((int)threadIdx.x == s.last) {
+        much.mass += q.before.mass;
+        much.n += q.before.n;
+        s.told.least_hi = (u64)(much.mass >> 64);
+        s.told.least_lo = (u64)much.mass;
+        s.told.least_n = much.n;
     }
 }
 
 // The first column of the order at which the sum of weights exceeds `mass`, or that is number `n`,
-// whichever comes first, if it lies within this thread's places (`before`: sums ahead of them,
-// `own`: theirs).  The thread's warp looks through its places, one a lane.
-__device__ __forceinline__ bool look(const Shared &s, const Slice &q, int first, int per, Sums before, const Sums &own, u128 mass, int n,
-                                     Found &out) {
+// whichever comes first, if it lies within the entries.  The warp whose thread has it looks through that
+// thread's entries, one a lane; the lane that has the column returns true.
+__device__ __forceinline__ bool look(const Shared &s, const Entries &q, u128 mass, int n, Found &out) {
     const int lane = threadIdx.x & 31;
-    const bool here = before.mass <= mass && before.n < n && (before.mass + own.mass > mass || before.n + own.n >= n);
+    const bool here = q.before.mass <= mass && q.before.n < n && (q.before.mass + q.own.mass > mass || q.before.n + q.own.n >= n);
     const unsigned who = __ballot_sync(kAll, here);
     if (!who) return false;
-    const int owner = __ffs(who) - 1;
-    first = __shfl_sync(kAll, first, owner);
-    const u64 hi = __shfl_sync(kAll, (u64)(before.mass >> 64), owner), lo = __shfl_sync(kAll, (u64)before.mass, owner);
-    const int n0 = __shfl_sync(kAll, before.n, owner);
-    const unsigned c = lane < per ? q.count(first + lane) : 0u;
-    const u64 w = c ? q.weight(s, first + lane) : 0ull;
-    Sums sum = {(u128)w * c, (int)c};
+    const int owner = __ffs(who) - 1, i = ((int)threadIdx.x - lane + owner) * q.each + lane;
+    const u64 hi = __shfl_sync(kAll, (u64)(q.before.mass >> 64), owner), lo = __shfl_sync(kAll, (u64)q.before.mass, owner);
+    const int n0 = __shfl_sync(kAll, q.before.n, owner);
+    const unsigned entry = lane < q.each && i < q.n ? q.list[i] : 0u;
+    const int c = (int)(entry & kColumns);
+    const u64 w = c ? q.weight(s, entry) : 0ull;
+    Sums sum = {(u128)w * (unsigned)c, c};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const u64 h = __shfl_up_sync(kAll, (u64)(sum.mass >> 64), o), l = __shfl_up_sync(kAll, (u64)sum.mass, o);
@@ -323,19 +369,22 @@ __device__ __forceinline__ bool look(const Shared &s, const Slice &q, int first,
     sum.n += n0;
     const unsigned past = __ballot_sync(kAll, c && (sum.mass > mass || sum.n >= n));
     if (lane != __ffs(past) - 1) return false;
-    const u128 m0 = sum.mass - (u128)w * c;
-    const int k0 = sum.n - (int)c;
-    // smallest r with m0 + (r + 1) w > mass, bounded by the number asked for
-    int a = 0, b = min((int)c, n - k0) - 1;
-    while (a < b) {
-        const int mid = (a + b) >> 1;
-        if (m0 + (u128)w * (unsigned)(mid + 1) > mass) b = mid;
-        else a = mid + 1;
+    const u128 m0 = sum.mass - (u128)w * (unsigned)c;
+    const int k0 = sum.n - c, last = min(c, n - k0) - 1;
+    // smallest r with m0 + (r + 1) w > mass, at most the number asked for: a quotient below 2^18, from fp32 to within one
+    int r = last;
+    if (sum.mass > mass) {
+        const u128 gap = mass - m0;
+        const int down = gap >> 64 ? 64 - __clzll((u64)(gap >> 64)) : 0;
+        const float quotient = (float)(u64)(gap >> down) / (float)w * exp2f((float)down);
+        r = quotient < (float)last ? (int)quotient : last;
+        while (r > 0 && m0 + (u128)w * (unsigned)r > mass) --r;
+        while (r < last && m0 + (u128)w * (unsigned)(r + 1) <= mass) ++r;
     }
-    const u128 m = m0 + (u128)w * (unsigned)(a + 1);
-    out.key = key_of_place(first + lane, q.window);
-    out.rank = a;
-    out.n = k0 + a + 1;
+    const u128 m = m0 + (u128)w * (unsigned)(r + 1);
+    out.key = key_of_place((int)(entry >> 18), q.window);
+    out.rank = r;
+    out.n = k0 + r + 1;
     out.hi = (u64)(m >> 64);
     out.lo = (u64)m;
     return true;
@@ -347,31 +396,39 @@ __device__ __noinline__ void count_window(Shared &s, const uint16_t *row, int V,
     __syncthreads();
     for (int i = threadIdx.x; i < kWinBins; i += kThreads) s.bins[i] = 0;
     __syncthreads();
-    each_column(row, 0, V, threadIdx.x, kThreads, [&](int, unsigned b) {
+    each_column(row, V, [&](unsigned b) {
         const unsigned k = key_of(b);
         if (k && (int)(k / kWinBins) == window) atomicAdd(&s.bins[kWinBins - 1 - (k % kWinBins)], 1u);
     });
     __syncthreads();
 }
 
-__device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, u64 least, Sums &total, Sums &heavy) {
+__device__ __noinline__ void window_entries(Shared &s, const uint16_t *row, int V, int window, u64 least, Entries &q, Sums &all) {
+    count_window(s, row, V, window);
     constexpr int kPer = kWinBins / kThreads;
+    q.list = s.bins;
+    q.window = window;
+    q.n = write_entries<kPer>(s, s.bins, 0, kPer, [&](int place) { return s.bins[place]; });
+    add_up(s, q, least, all);
+}
+
+__device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, u64 least, Sums &total, Sums &heavy) {
     if (threadIdx.x < kWindows) s.coarse[threadIdx.x] = 0;
     __syncthreads();
-    each_column(row, 0, V, threadIdx.x, kThreads, [&](int, unsigned b) {
+    each_column(row, V, [&](unsigned b) {
         const unsigned k = key_of(b);
         if (k) atomicAdd(&s.coarse[k / kWinBins], 1);
     });
     __syncthreads();
     total = heavy = {0, 0};
     for (int w = kWindows - 1; w >= 0; --w) {
-        Sums all = {0, 0}, some = {0, 0};
+        Sums all = {0, 0};
         if (s.coarse[w]) {
-            count_window(s, row, V, w);
-            Sums own, much;
-            add_up(s, {s.bins, 0, w, false}, threadIdx.x * kPer, kPer, least, own, much);
-            scan(s, own, all);
-            scan(s, much, some);
+            Entries q;
+            window_entries(s, row, V, w, least, q, all);
+            __syncthreads();
+            if (s.told.least_n) heavy = {total.mass + join(s.told.least_hi, s.told.least_lo), total.n + s.told.least_n};
+            __syncthreads();
         }
         if (threadIdx.x == 0) {
             s.win_hi[w] = (u64)(all.mass >> 64);
@@ -380,15 +437,13 @@ __device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, 
         }
         total.mass += all.mass;
         total.n += all.n;
-        heavy.mass += some.mass;
-        heavy.n += some.n;
     }
     __syncthreads();
 }
 
-__device__ __noinline__ void find_by_windows(Shared &s, const uint16_t *row, int V, u128 mass, int n) {
-    constexpr int kPer = kWinBins / kThreads;
-    Sums at = {0, 0};
+// The window where a sum passes a bound, and its entries.
+__device__ __noinline__ void window_of(Shared &s, const uint16_t *row, int V, u128 mass, int n, Entries &q) {
+    Sums at = {0, 0}, all;
     int w = kWindows - 1;
     for (; w > 0; --w) {
         const u128 m = at.mass + join(s.win_hi[w], s.win_lo[w]);
@@ -396,16 +451,9 @@ __device__ __noinline__ void find_by_windows(Shared &s, const uint16_t *row, int
         at.mass = m;
         at.n += s.win_n[w];
     }
-    count_window(s, row, V, w);
-    const Slice q = {s.bins, 0, w, false};
-    Sums own, unused, total;
-    add_up(s, q, threadIdx.x * kPer, kPer, 0, own, unused);
-    Sums before = scan(s, own, total);
-    before.mass += at.mass;
-    before.n += at.n;
-    Found f;
-    if (look(s, q, threadIdx.x * kPer, kPer, before, own, mass, n, f)) s.found = f;
-    __syncthreads();
+    window_entries(s, row, V, w, 0, q, all);
+    q.before.mass += at.mass;
+    q.before.n += at.n;
 }
 
 // ------------------------------------------------------------ clusters
@@ -425,7 +473,7 @@ __device__ __forceinline__ uint32_t peer_address(const void *local, int peer) {
 }
 __device__ __forceinline__ unsigned load_peer(uint32_t a) {
     unsigned v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ void store_peer(uint32_t a, unsigned v) {
@@ -460,35 +508,53 @@ struct Counter {
     __device__ __forceinline__ void add(unsigned address) {
         asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(address) : "memory");
     }
-    __device__ __forceinline__ void one(unsigned b) {
+    __device__ __forceinline__ void rare(unsigned b) {  // outside of the counted range
         const unsigned mag = b & 0x7fffu;
-        if (mag - kMagLo < (unsigned)kMags) atomicAdd(&bins[(mag - kMagLo) | (b >> 3 & 0x1000u)], 1u);
-        else if (mag == 0u) atomicAdd(&bins[2 * kMags], 1u);
+        if (mag == 0u) atomicAdd(&bins[2 * kMags], 1u);
         else if (mag > 0x7f80u || b == 0xff80u) return;  // NaN, -inf
         else if ((b & 0x8000u) && mag > kMagLo) low = max(low, key_of(b));
         else odd = 1;
     }
+    __device__ __forceinline__ void one(unsigned b) {
+        const unsigned mag = b & 0x7fffu;
+        if (mag - kMagLo < (unsigned)kMags) atomicAdd(&bins[(mag - kMagLo) | (b >> 2 & 0x2000u)], 1u);
+        else rare(b);
+    }
     __device__ __forceinline__ void eight(const uint4 &v) {
-        static_assert(kMagLo == 0x3400 && kMags == 0x1000, "the range ends at a multiple of its size with 0xc00 added");
+        static_assert(kMagLo == 0x2400 && kMags == 0x2000, "with 0x1c00 added the range is 0x4000 to 0x5fff");
         const unsigned base = smem_u32_of(bins);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t t[4], out = 0;
+        uint32_t t[4], out[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            t[k] = (w[k] & 0x7fff7fffu) + 0x0c000c00u;
-            out |= (t[k] ^ 0x40004000u) & 0x70007000u;
+            t[k] = (w[k] & 0x7fff7fffu) + 0x1c001c00u;
+            out[k] = (t[k] ^ 0x40004000u) & 0x60006000u;
         }
-        if (out) {
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) one(w[k >> 1] >> (k & 1) * 16 & 0xffffu);
+        // four times (magnitude | sign << 13)
+        const auto lower = [&](int k) { return base + ((t[k] << 2 & 0x7ffcu) | (w[k] & 0x8000u)); };
+        const auto upper = [&](int k) { return base + ((t[k] >> 14 & 0x7ffcu) | (w[k] >> 16 & 0x8000u)); };
+        if (!(out[0] | out[1] | out[2] | out[3])) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                add(lower(k));
+                add(upper(k));
+            }
             return;
         }
+        uint32_t odd_one = 0;  // halves outside of the range that are not -inf, as the halves' highest bits
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            // four times (magnitude | sign << 12)
-            add(base + ((t[k] << 2 & 0x3ffcu) | (w[k] >> 1 & 0x4000u)));
-            add(base + ((t[k] >> 14 & 0x3ffcu) | (w[k] >> 17 & 0x4000u)));
+            const uint32_t x = w[k] ^ 0xff80ff80u;
+            odd_one |= (out[k] + 0x60006000u) & (((x & 0x7fff7fffu) + 0x7fff7fffu) | x) & 0x80008000u;
+            if (!(out[k] & 0xffffu)) add(lower(k));
+            if (!(out[k] >> 16)) add(upper(k));
         }
+        if (odd_one)
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                const unsigned b = w[k >> 1] >> (k & 1) * 16 & 0xffffu;
+                if ((b & 0x7fffu) - kMagLo >= (unsigned)kMags) rare(b);
+            }
     }
 };
 
@@ -501,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     const uint16_t *row = p.logits + (long long)t * p.ld;
     asm volatile("griddepcontrol.launch_dependents;");
     fill_powers(s.pw);
-    if (tid == 0) s.told.low = 0, s.told.odd = 0, s.told.top = kBins;
+    if (tid == 0) s.told.low = 0, s.told.odd = 0, s.told.top = kPlaces;
     for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -515,8 +581,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     if (lane == 0 && low) atomicMax(&s.told.low, low);
     if (__any_sync(kAll, counter.odd) && lane == 0) s.told.odd = 1;
     __syncthreads();
-    int top = kBins;
-    for (int i = tid; i < kBins; i += kThreads)
+    if (tid == 0 && s.bins[0]) s.told.odd = 1;  // +2^-55
+    int top = kPlaces;
+    for (int i = tid; i < kPlaces; i += kThreads)
         if (s.bins[bin_of_place(i)]) {
             top = i;
             break;
@@ -531,28 +598,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     hear(s, C);
     unsigned lowest = 0;
     int odd = 0;
-    top = kBins;
+    top = kPlaces;
     for (int k = 0; k < C; ++k) {
         top = min(top, s.all[k].top);
         lowest = max(lowest, s.all[k].low);
         odd |= s.all[k].odd;
     }
     // The one window is enough if nothing lies outside of it but numbers too low to weigh anything.
-    bool one = !odd && top < kBins;
+    bool one = !odd && top < kPlaces;
     if (one) {
         if (tid == 0) s.scale = make_scale(greedy ? 1.f : temperature, value_of(key_of_place(top, -1)));
         __syncthreads();
         one = lowest == 0 || weight62(s.scale, value_of(lowest), s.pw) == 0;
     }
-    Sums total, heavy, own, before = {0, 0};
-    const int per = (kBins + C * kThreads - 1) / (C * kThreads), first = (c * kThreads + tid) * per;
-    const Slice slice = {C == 1 ? s.bins : s.merged, c * kThreads * per, -1, C == 1};
+    Sums total, heavy;
+    Entries entries;
     if (!one) {
         // the first CTA does the row alone
         cluster_sync(C);  // (and is no longer read by the others)
         if (c) return;
         unsigned key = 0;
-        each_column(row, 0, p.V, tid, kThreads, [&](int, unsigned b) { key = max(key, key_of(b)); });
+        each_column(row, p.V, [&](unsigned b) { key = max(key, key_of(b)); });
         key = __reduce_max_sync(kAll, key);
         if (lane == 0) s.warp_n[warp] = (int)key;
         __syncthreads();
@@ -567,118 +633,109 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         if (tid == 0) s.scale = make_scale(greedy ? 1.f : temperature, value_of(key));
         window_sums(s, row, p.V, least, total, heavy);
     } else {
-        if (C > 1) {
-            // the slice's counts in the parts of all
-            for (int i = 0; i < per; ++i) {
-                const int place = c * kThreads * per + i * kThreads + tid;
+        entries.window = -1;
+        const int rounds = kRounds / C, first = c * rounds * kThreads;
+        if (C == 1) {
+            entries.list = s.bins;
+            entries.n = write_entries<kRounds>(s, s.bins, 0, kRounds, [&](int place) { return s.bins[bin_of_place(place)]; });
+        } else {
+            // a slice's counts in the parts of all
+            entries.list = s.list;
+            entries.n = write_entries<kRounds / 2>(s, s.list, first, rounds, [&](int place) {
+                const unsigned *at = s.bins + bin_of_place(place);
                 unsigned sum = 0;
-                if (place < kBins) {
-                    const unsigned *at = s.bins + bin_of_place(place);
-#pragma unroll 1
-                    for (int k = 0; k < C; ++k) sum += load_peer(peer_address(at, k));
-                }
-                s.merged[i * kThreads + tid] = sum;
-            }
-            __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kMostCtas; ++k)
+                    if (k < C) sum += load_peer(peer_address(at, k));
+                return sum;
+            });
         }
-        Sums much, slice_total, slice_heavy;
-        add_up(s, slice, first, per, least, own, much);
-        before = scan(s, own, slice_total);
-        scan(s, much, slice_heavy);
+        add_up(s, entries, least, total);
         if (tid == 0) {
-            s.told.hi = (u64)(slice_total.mass >> 64);
-            s.told.lo = (u64)slice_total.mass;
-            s.told.n = slice_total.n;
-            s.told.least_hi = (u64)(slice_heavy.mass >> 64);
-            s.told.least_lo = (u64)slice_heavy.mass;
-            s.told.least_n = slice_heavy.n;
+            s.told.hi = (u64)(total.mass >> 64);
+            s.told.lo = (u64)total.mass;
+            s.told.n = total.n;
         }
         hear(s, C);
         total = heavy = {0, 0};
         for (int k = 0; k < C; ++k) {
             const Told &o = s.all[k];
             if (k == c) {
-                before.mass += total.mass;
-                before.n += total.n;
+                entries.before.mass += total.mass;
+                entries.before.n += total.n;
             }
+            if (o.least_n) heavy = {total.mass + join(o.least_hi, o.least_lo), total.n + o.least_n};
             total.mass += join(o.hi, o.lo);
             total.n += o.n;
-            heavy.mass += join(o.least_hi, o.least_lo);
-            heavy.n += o.least_n;
         }
     }
-    // the column of the order where sums pass a bound, in s.found of every CTA
-    const auto find = [&](u128 mass, int n) {
-        if (!one) {
-            find_by_windows(s, row, p.V, mass, n);
-            return;
-        }
-        Found f;
-        if (look(s, slice, first, per, before, own, mass, n, f)) {
-            if (C == 1) s.found = f;
-            else
-                for (int k = 0; k < C; ++k) {
-                    const uint32_t to = peer_address(&s.found, k);
-#pragma unroll
-                    for (int i = 0; i < (int)(sizeof(Found) / 4); ++i) store_peer(to + i * 4, ((const unsigned *)&f)[i]);
-                }
-        }
-        cluster_sync(C);
-    };
-    // what is kept: n columns that weigh `mass`
+    // What is kept is n columns that weigh `mass`: by top-k, by top-p, by min-p.  The fourth step is the draw.
     int n = total.n;
     u128 mass = total.mass;
     if (greedy) {
         n = 1;
         mass = (u128)1 << 62;
-    } else {
-        if (top_k > 0 && top_k < n) {
-            find(~(u128)0, top_k);
-            n = top_k;
-            mass = join(s.found.hi, s.found.lo);
-            cluster_sync(one ? C : 1);
-        }
-        if (top_p < 1.f) {
-            // the sum has to reach top_p * mass, so it has to exceed the next integer below
-            bool exact;
-            const u128 down = times(mass, top_p, exact);
-            find(exact && down ? down - 1 : down, n);
-            n = s.found.n;
-            mass = join(s.found.hi, s.found.lo);
-            cluster_sync(one ? C : 1);
-        }
-        if (least && heavy.n < n) {
-            n = heavy.n;
-            mass = heavy.mass;
-        }
     }
-    bool exact;
-    find(times(mass, u < 1.f ? u : u >= 1.f ? 0x1.fffffep-1f : 0.f, exact), n);
+    const float draw = u < 1.f ? u : u >= 1.f ? 0x1.fffffep-1f : 0.f;
+#pragma unroll 1
+    for (int step = greedy ? 2 : 0; step < 3; ++step) {
+        u128 bound = ~(u128)0;  // the column at which sums exceed it
+        int most = n;           // ... or which is this one
+        if (step == 0) {
+            if (top_k < 1 || top_k >= n) continue;
+            most = top_k;
+        } else {
+            if (step == 1 && !(top_p < 1.f)) continue;
+            if (step == 2 && !greedy && least && heavy.n < n) {
+                most = heavy.n;
+                mass = heavy.mass;
+            }
+            bool exact;
+            bound = times(mass, step == 1 ? top_p : draw, exact);
+            // a share of the weight has to be reached: the next integer below exceeded
+            if (step == 1 && exact && bound) --bound;
+        }
+        if (!one) window_of(s, row, p.V, bound, most, entries);
+        Found f;
+        if (look(s, entries, bound, most, f)) {
+            if (C == 1 || !one) s.found[step] = f;
+            else
+                for (int k = 0; k < C; ++k) {
+                    const uint32_t to = peer_address(&s.found[step], k);
+#pragma unroll
+                    for (int i = 0; i < (int)(sizeof(Found) / 4); ++i) store_peer(to + i * 4, ((const unsigned *)&f)[i]);
+                }
+        }
+        cluster_sync(one ? C : 1);
+        n = s.found[step].n;
+        mass = join(s.found[step].hi, s.found[step].lo);
+    }
 
     // which column that is: number `rank` of those with the found key.  A warp's columns follow each other.
-    const unsigned key = s.found.key;
-    const int rank = s.found.rank;
+    const unsigned key = s.found[2].key;
+    const int rank = s.found[2].rank;
     const int from = one ? begin : 0, to = one ? end : p.V;
     const int chunk = ((to - from + kWarps - 1) / kWarps + 255) & ~255;
     const int w0 = min(to, from + warp * chunk), w1 = min(to, w0 + chunk);
     const unsigned bits = key == 0x8000u ? 0u : __float_as_uint(value_of(key)) >> 16, both = bits | bits << 16;
     const unsigned odd_keys = key == 0x8000u || key == kKeyMax;  // those that several bits stand for
-    int mine = 0;
-    each_vector(
-        row, w0, w1, lane, 32,
-        [&](int, const uint4 &v) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t hit = odd_keys;
+    // how many of 8 columns have it
+    const auto matches = [&](const uint4 &v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hit = odd_keys;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t x = w[k] ^ both;
-                hit |= (x - 0x00010001u) & ~x & 0x80008000u;  // not 0 where a half of x is
-            }
-            if (!hit) return;
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x = w[k] ^ both;
+            hit |= (x - 0x00010001u) & ~x & 0x80008000u;  // not 0 where a half of x is
+        }
+        int n = 0;
+        if (hit)
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k) mine += key_of(w[k >> 1] >> (k & 1) * 16 & 0xffffu) == key;
-        },
-        [&](int, unsigned b) { mine += key_of(b) == key; });
+            for (int k = 0; k < 8; ++k) n += key_of(w[k >> 1] >> (k & 1) * 16 & 0xffffu) == key;
+        return n;
+    };
+    int mine = 0;
+    each_vector(row, w0, w1, lane, 32, [&](int, const uint4 &v) { mine += matches(v); }, [&](int, unsigned b) { mine += key_of(b) == key; });
     mine = (int)__reduce_add_sync(kAll, (unsigned)mine);
     __syncthreads();
     if (lane == 0) s.warp_n[warp] = mine;
@@ -696,31 +753,55 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     }
     for (int w = 0; w < warp; ++w) ahead += s.warp_n[w];
     if (ahead > rank || rank >= ahead + mine) return;
-    for (int i = w0; i < w1; i += 32) {
-        const int at = i + lane;
-        const unsigned hit = __ballot_sync(kAll, at < w1 && key_of(row[at]) == key);
-        if (rank < ahead + __popc(hit)) {
-            if ((hit >> lane & 1) && ahead + __popc(hit & ((1u << lane) - 1)) == rank) {
-                p.tokens[t] = at;
-                if (p.logprobs) {
-                    float hi, lo;
-                    distance(s.scale, value_of(key), hi, lo);
-                    // ln of the sum: 2^62 is one
-                    const int lead = total.mass >> 64 ? 64 - __clzll((u64)(total.mass >> 64)) : 0;
-                    const float m = (float)(u64)(total.mass >> lead);
-                    p.logprobs[t] = -(hi * 0.69314718056f + (logf(m * 0x1p-62f) + (float)lead * 0.69314718056f));
-                }
-            }
-            break;
+    // the warp's columns again, 256 at a time, from L1 or L2
+    int found_at = -1;
+#pragma unroll 1
+    for (int i = w0; i < w1; i += 256) {
+        const int at = i + lane * 8, few = min(8, w1 - at);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        int here = 0;
+        if (few == 8) {
+            v = __ldg((const uint4 *)(row + at));
+            here = matches(v);
+        } else {
+            for (int k = 0; k < few; ++k) here += key_of(row[at + k]) == key;
         }
-        ahead += __popc(hit);
+        const int all = (int)__reduce_add_sync(kAll, (unsigned)here);
+        if (rank >= ahead + all) {
+            ahead += all;
+            continue;
+        }
+        int upto = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int k = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += k;
+        }
+        ahead += upto - here;  // ahead of this lane's columns
+        if (ahead <= rank && rank < ahead + here)
+            for (int k = 0; k < few; ++k)
+                if (key_of(row[at + k]) == key && ahead++ == rank) found_at = at + k;
+        break;
+    }
+    if (found_at < 0) return;
+    p.tokens[t] = found_at;
+    if (p.logprobs) {
+        float hi, lo;
+        distance(s.scale, value_of(key), hi, lo);
+        // ln of the sum: 2^62 is one
+        const int lead = total.mass >> 64 ? 64 - __clzll((u64)(total.mass >> 64)) : 0;
+        const float m = (float)(u64)(total.mass >> lead);
+        p.logprobs[t] = -(hi * 0.69314718056f + (logf(m * 0x1p-62f) + (float)lead * 0.69314718056f));
     }
 }
 
-// CTAs that share a row: as many as all find room at once, two to an SM, of 4096 columns at least.
+// CTAs that share a row: as many as all find room at once, two to an SM, of 12000 columns at least; a short
+// row is not shared, as the cluster's barriers and what goes around take 5 us (one row of 4000
+// columns 15.7 us by one CTA, 21.1 by two; of 32007 21.6, 23.1 and by eight 21.7; of 128256 38.5, 31.4 and 22.9).
 int ctas_of_a_row(int T, int V, int sms) {
     int C = 1;
-    while (C < kMostCtas && (long long)T * C * 2 <= 2LL * sms && V >= C * 2 * 4096) C *= 2;
+    if (V < 40000) return C;
+    while (C < kMostCtas && (long long)T * C * 2 <= 2LL * sms && V >= C * 2 * 12000) C *= 2;
     return C;
 }
 
