@@ -243,9 +243,8 @@ __device__ __forceinline__ Sums scan(Shared &s, Sums mine, Sums &total) {
 
 // A row's columns from `begin` on, 8 at a time: f(column, its 8 bits' words), and g(column, bits) for
 // those of a last vector that is not whole.
-template <typename F, typename G>
+template <int kAhead, typename F, typename G>
 __device__ __forceinline__ void each_vector(const uint16_t *row, int begin, int end, int at, int step, F f, G g) {
-    constexpr int kAhead = 2;
     const int whole = begin + ((end - begin) & ~7);
     for (int i = begin + at * 8; i < whole; i += kAhead * step * 8) {
         uint4 v[kAhead];
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     const int part = ((p.V + C - 1) / C + 7) & ~7, begin = min(p.V, c * part), end = min(p.V, begin + part);
     Counter counter;
     counter.bins = s.bins;
-    each_vector(row, begin, end, tid, kThreads, [&](int, const uint4 &v) { counter.eight(v); }, [&](int, unsigned b) { counter.one(b); });
+    each_vector<2>(row, begin, end, tid, kThreads, [&](int, const uint4 &v) { counter.eight(v); }, [&](int, unsigned b) { counter.one(b); });
     const unsigned low = __reduce_max_sync(kAll, counter.low);
     if (lane == 0 && low) atomicMax(&s.told.low, low);
     if (__any_sync(kAll, counter.odd) && lane == 0) s.told.odd = 1;
@@ -718,24 +717,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     const int chunk = ((to - from + kWarps - 1) / kWarps + 255) & ~255;
     const int w0 = min(to, from + warp * chunk), w1 = min(to, w0 + chunk);
     const unsigned bits = key == 0x8000u ? 0u : __float_as_uint(value_of(key)) >> 16, both = bits | bits << 16;
-    const unsigned odd_keys = key == 0x8000u || key == kKeyMax;  // those that several bits stand for
+    const unsigned signs = key == 0x8000u ? 0x7fff7fffu : 0xffffffffu;  // -0 is 0
+    const bool largest = key == kKeyMax;                                // +inf counts as that, too
     // how many of 8 columns have it
     const auto matches = [&](const uint4 &v) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t hit = odd_keys;
+        int n = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t x = w[k] ^ both;
-            hit |= (x - 0x00010001u) & ~x & 0x80008000u;  // not 0 where a half of x is
+            const uint32_t x = (w[k] ^ both) & signs;
+            n += __popc(~(((x & 0x7fff7fffu) + 0x7fff7fffu) | x) & 0x80008000u);  // halves of 0
         }
-        int n = 0;
-        if (hit)
+        if (largest) {
+            n = 0;
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) n += key_of(w[k >> 1] >> (k & 1) * 16 & 0xffffu) == key;
+        }
         return n;
     };
     int mine = 0;
-    each_vector(row, w0, w1, lane, 32, [&](int, const uint4 &v) { mine += matches(v); }, [&](int, unsigned b) { mine += key_of(b) == key; });
+    each_vector<4>(row, w0, w1, lane, 32, [&](int, const uint4 &v) { mine += matches(v); }, [&](int, unsigned b) { mine += key_of(b) == key; });
     mine = (int)__reduce_add_sync(kAll, (unsigned)mine);
     __syncthreads();
     if (lane == 0) s.warp_n[warp] = mine;
