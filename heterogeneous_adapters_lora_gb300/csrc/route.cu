@@ -1,36 +1,40 @@
 // The router's choice: the top_k experts of every token by score (softmax or
 // logistic function of the logits) plus a bias, and their weights.
 //
-// A warp takes a token and keeps its logits in registers, expert j * 32 + lane
-// in element j.  Choosing needs no scores where they grow with the logits (no
-// bias): the order is that of the logits, exact in fp32.  The choice is top_k
-// rounds of a maximum over order-preserving integers (redux.sync) and the lowest
-// id among those that have it.  A round costs the same for every token, so a
-// call is bound by its launch for few tokens, and by these rounds for many.
+// A warp takes a token and keeps its logits in registers, experts lane * N to lane * N + N - 1
+// in a lane: the lowest lane that has the largest key then has the lowest id of equal ones.  Choosing needs no
+// scores where they grow with the logits (no bias): the order is that of the logits, exact in fp32.
+// The choice is top_k rounds: the lanes' own maxima as order-preserving integers, the largest of them
+// (redux.sync), and a new maximum in the lane that had it.  A round takes some 45 instructions,
+// the scores as many as two rounds, and many tokens are bound by issuing them; few by the launch
+// and one read.  Warps walk over tokens and read the next one's logits ahead.
 //
 // With a bias the fp32 scores may be off by a few 2^-24, which could order two
-// experts wrongly.  So one more expert than asked for is looked at, and where two
-// neighbours of the order are nearer than twice the error bound the
-// token is done again with scores in 64 bits.
+// experts wrongly.  So rounds go on until the next expert is further behind than twice the error bound, and
+// where neighbours of the order are nearer than that the ones that were found, one in a lane, are
+// ordered again by scores in 64 bits (a logistic function each; a softmax's sum takes all of the token's).
 #include <float.h>
 #include <string.h>
+
+#include <atomic>
 
 #include "lora_internal.cuh"
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kCtasPerSm = 8;
 constexpr unsigned kAll = 0xffffffffu;
-// Bounds on the relative error of an fp32 score with the rounding of its biased
-// sum.  Logistic function: exp 2 ulp, three more roundings.  Softmax: a logit minus the
-// largest is rounded once, 2^-24 of up to 104 past which the score is 0; exp 2 ulp; the sum
-// of up to 1024 terms in 32 lanes and 5 steps 37 roundings; the product and the bias two more.
+// Bounds on the absolute error of an fp32 score with the rounding of its biased sum, for sums
+// of magnitude 1 or less (larger ones in proportion).  Scores that decide take the fast exp and division: e =
+// exp(x) is off by 2^-22 and by 2^-24 * 1.45 |x| of itself, the quotient by 2 ulp.  Logistic
+// function: s (1 - s) <= 1/4 and s (1 - s) |x| < 0.23, so 2e-7 with the quotient's.  Softmax: s |x - top| < 0.37, the sum of up
+// to 1024 terms in 32 lanes and 5 steps takes 37 roundings, 3e-6.  The sum with the bias 6e-8.
 constexpr float kEpsSigmoid = 1.0e-6f, kEpsSoftmax = 1.0e-5f;
 
 struct RouteArgs {
     const void *logits;
     long long ld;
-    int T, E, k, sigmoid, renormalize, wide;
+    int T, E, k, sigmoid, renormalize, wide, vec;
     float scale;
     const float *bias;
     int32_t *ids;
@@ -72,129 +76,226 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
     return ((unsigned long long)hi << 32) | lo;
 }
 
-// One round: the expert of the largest key, taken out; -1 if none is left.
+// One round: the expert of the largest key, taken out; -1 if none is left.  `mine`: this lane's largest.
 template <int N, typename K>
-__device__ __forceinline__ int take_best(K (&key)[N], K &best, int lane) {
-    K mine = key[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) mine = key[j] > mine ? key[j] : mine;
+__device__ __forceinline__ int take_best(K (&key)[N], K &mine, K &best, int lane) {
     best = warp_max(mine);
     if (best == 0) return -1;
-    int at = 0x7fffffff;
+    const int who = __ffs(__ballot_sync(kAll, mine == best)) - 1;
+    int at = 0;
+    if (lane == who) {
+        K next = 0;
+        bool taken = false;
 #pragma unroll
-    for (int j = N - 1; j >= 0; --j) at = key[j] == best ? j * 32 + lane : at;
-    at = (int)__reduce_min_sync(kAll, (unsigned)at);
+        for (int j = 0; j < N; ++j) {
+            if (!taken && key[j] == best) {
+                key[j] = 0;
+                at = j;
+                taken = true;
+            }
+            next = key[j] > next ? key[j] : next;
+        }
+        mine = next;
+    }
+    return who * N + __shfl_sync(kAll, at, who);
+}
+template <int N, typename K>
+__device__ __forceinline__ K largest(const K (&key)[N]) {
+    K m = key[0];
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j * 32 + lane == at) key[j] = 0;
-    return at;
+    for (int j = 1; j < N; ++j) m = key[j] > m ? key[j] : m;
+    return m;
 }
 
 __device__ __forceinline__ float load_logit(const RouteArgs &p, long long t, int e) {
     if (p.wide) return ((const float *)p.logits)[t * p.ld + e];
     return __uint_as_float((uint32_t)((const uint16_t *)p.logits)[t * p.ld + e] << 16);
 }
+// What a logit counts as: NaN and -inf take no part, +inf is the largest number.
+__device__ __forceinline__ float counted(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
 
-// The choice by scores in 64 bits, for a token whose fp32 scores are too near to each other.
+// This lane's logits of token t.  `vec`: rows are whole and aligned.
 template <int N>
-__device__ __noinline__ int choose_exactly(const RouteArgs &p, const float (&x)[N], float top, int lane, int k_lane) {
-    double s[N], total = 0.0;
+__device__ __forceinline__ void load_logits(const RouteArgs &p, long long t, int lane, float (&x)[N]) {
+    if (p.vec) {
+        if (p.wide) {
+            const float *row = (const float *)p.logits + t * p.ld + lane * N;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        s[j] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)top);
-        total += s[j];
-    }
-    total = p.sigmoid ? 1.0 : warp_sum(total);
-    unsigned long long key[N], best;
+            for (int j = 0; j < N; j += 2) {
+                const float2 v = __ldg((const float2 *)(row + j));
+                x[j] = v.x;
+                x[j + 1] = v.y;
+            }
+        } else {
+            const uint16_t *row = (const uint16_t *)p.logits + t * p.ld + lane * N;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int e = j * 32 + lane;
-        key[j] = e < p.E && x[j] > -INFINITY ? order_key(s[j] / total + (double)p.bias[e]) : 0ull;
-    }
-    int chosen = -1;
-    for (int r = 0; r < p.k; ++r) {
-        const int e = take_best<N>(key, best, lane);
-        if (r == k_lane) chosen = e;
-    }
-    return chosen;
-}
-
-// N: elements per lane (experts up to 32 N).
-template <int N>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
-    const int lane = threadIdx.x & 31;
-    const long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (t >= p.T) return;
-    float x[N];
-    unsigned key[N], best;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const int e = j * 32 + lane;
-        const float v = e < p.E ? load_logit(p, t, e) : -INFINITY;
-        x[j] = v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY;  // NaN takes no part either
-    }
-    float mine = x[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) mine = fmaxf(mine, x[j]);
-    const unsigned top_key = __reduce_max_sync(kAll, order_key(mine));
-    const float top = top_key ? key_value(top_key) : 0.f;
-    // the scores' common factor: 1 / sum of exp(x - top), or 1
-    float inv = 1.f;
-    float part = 0.f;
-    if (!p.sigmoid) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) part += expf(x[j] - top);
-        inv = 1.f / warp_sum(part);
-    }
-    // score of a logit
-    const auto score = [&](float v) { return p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) * inv; };
-    int chosen = -1;  // of round `lane`
-    if (!p.bias) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
-        for (int r = 0; r < p.k; ++r) {
-            const int e = take_best<N>(key, best, lane);
-            if (r == lane) chosen = e;
+            for (int j = 0; j < N; j += 2) {
+                const uint32_t v = __ldg((const uint32_t *)(row + j));
+                x[j] = bf16lo(v);
+                x[j + 1] = bf16hi(v);
+            }
         }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int e = j * 32 + lane;
-            key[j] = e < p.E && x[j] > -INFINITY ? order_key(score(x[j]) + p.bias[e]) : 0u;
+            const int e = lane * N + j;
+            x[j] = e < p.E ? load_logit(p, t, e) : -INFINITY;
         }
-        float before = 0.f, widest = 1.f;
-        bool near = false;
-        const float eps = p.sigmoid ? kEpsSigmoid : kEpsSoftmax;
-        for (int r = 0; r <= p.k; ++r) {
-            const int e = take_best<N>(key, best, lane);
-            if (e < 0) break;
-            const float v = key_value(best);
-            widest = fmaxf(widest, fabsf(v));
-            if (r > 0 && !(before - v > 2.f * eps * widest)) near = true;
-            before = v;
-            if (r == lane && r < p.k) chosen = e;
-        }
-        if (near) chosen = choose_exactly<N>(p, x, top, lane, lane);
-    }
-    float s = 0.f;
-    if (chosen >= 0) {
-        float v = load_logit(p, t, chosen);
-        s = score(fminf(v, FLT_MAX));
-    }
-    if (p.renormalize) {
-        const float sum = warp_sum(s);
-        s = sum > 0.f ? s / sum : 0.f;
-    }
-    if (lane < p.k) {
-        p.ids[t * p.k + lane] = chosen;
-        p.w[t * p.k + lane] = chosen >= 0 ? s * p.scale : 0.f;
     }
 }
 
+// The first k of `found` candidates (lane r has the one of round r) by scores in 64 bits; lane r gets number r.
 template <int N>
-cudaError_t route_launch(const RouteArgs &p, cudaStream_t s) {
+__device__ __noinline__ int order_exactly(const RouteArgs &p, long long t, float top, int lane, int candidate, int found) {
+    double total = 1.0;
+    if (!p.sigmoid) {
+        double part = 0.0;
+#pragma unroll 1
+        for (int j = 0; j < N; ++j) {
+            const int e = lane * N + j;
+            if (e < p.E) part += exp((double)counted(load_logit(p, t, e)) - (double)top);
+        }
+        total = warp_sum(part);
+    }
+    unsigned long long key = 0;
+    if (lane < found) {
+        const double v = (double)counted(load_logit(p, t, candidate));
+        const double s = p.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - (double)top) / total;
+        key = order_key(s + (double)p.bias[candidate]);
+    }
+    int place = 0;  // of equal keys the lower id comes first
+    for (int r = 0; r < found; ++r) {
+        const unsigned long long other = __shfl_sync(kAll, key, r);
+        const int id = __shfl_sync(kAll, candidate, r);
+        place += other > key || (other == key && id < candidate);
+    }
+    int chosen = -1;
+    for (int r = 0; r < found; ++r) {
+        const int at = __shfl_sync(kAll, place, r), id = __shfl_sync(kAll, candidate, r);
+        if (at == lane) chosen = id;
+    }
+    return lane < p.k ? chosen : -1;
+}
+
+// The same for a token with more than 32 of them: all experts by scores in 64 bits.
+template <int N>
+__device__ __noinline__ int choose_exactly(const RouteArgs &p, long long t, float top, int lane) {
+    double total = 1.0;
+    unsigned long long key[N], best;
+    for (int pass = p.sigmoid; pass < 2; ++pass) {  // the sum, then the keys
+        double part = 0.0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int e = lane * N + j;
+            const float v = counted(e < p.E ? load_logit(p, t, e) : -INFINITY);
+            const double s = v == -INFINITY ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)top) / total;
+            part += s;
+            key[j] = v == -INFINITY ? 0ull : order_key(s + (double)p.bias[e]);
+        }
+        if (pass == 0) total = warp_sum(part);
+    }
+    unsigned long long mine = largest<N>(key);
+    int chosen = -1;
+    for (int r = 0; r < p.k; ++r) {
+        const int e = take_best<N>(key, mine, best, lane);
+        if (r == lane) chosen = e;
+    }
+    return chosen;
+}
+
+// N: experts of a lane (32 N in all).
+template <int N, bool BIAS>
+__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
+    const int lane = threadIdx.x & 31, step = (int)gridDim.x * (kThreads / 32);
+    long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float bias[BIAS ? N : 1], ahead[N];
+    if (BIAS)
+#pragma unroll
+        for (int j = 0; j < N; ++j) bias[j] = lane * N + j < p.E ? p.bias[lane * N + j] : 0.f;
+    if (t < p.T) load_logits<N>(p, t, lane, ahead);
+    for (; t < p.T; t += step) {
+        float x[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = counted(ahead[j]);
+        if (t + step < p.T) load_logits<N>(p, t + step, lane, ahead);
+        const unsigned top_key = warp_max(order_key(largest<N>(x)));
+        const float top = top_key ? key_value(top_key) : 0.f;
+        unsigned key[N], best, mine;
+        int chosen = -1;  // of round `lane`
+        float total = 1.f;  // of exp(x - top)
+        if (!p.sigmoid) {
+            float part = 0.f;
+#pragma unroll
+            for (int j = 0; j < N; ++j) part += BIAS ? __expf(x[j] - top) : expf(x[j] - top);
+            total = warp_sum(part);
+        }
+        if (!BIAS) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
+            mine = largest<N>(key);
+            for (int r = 0; r < p.k; ++r) {
+                const int e = take_best<N>(key, mine, best, lane);
+                if (r == lane) chosen = e;
+            }
+        } else {
+            const float inv = 1.f / total;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float s = p.sigmoid ? __fdividef(1.f, 1.f + fminf(__expf(-x[j]), 1e30f)) : __expf(x[j] - top) * inv;
+                key[j] = x[j] > -INFINITY ? order_key(s + bias[j]) : 0u;
+            }
+            mine = largest<N>(key);
+            float before = 0.f, widest = 1.f;
+            bool near = false;
+            const float eps = p.sigmoid ? kEpsSigmoid : kEpsSoftmax;
+            int found = 0;
+            bool many = false;
+            for (int r = 0;; ++r) {
+                const int e = take_best<N>(key, mine, best, lane);
+                if (e < 0) break;
+                const float v = key_value(best);
+                widest = fmaxf(widest, fabsf(v));
+                const bool close = r > 0 && !(before - v > 2.f * eps * widest);
+                if (r >= p.k && !close) break;  // and all that follow are further behind
+                near |= close;
+                many = r >= 32;
+                if (many) break;
+                before = v;
+                if (r == lane) chosen = e;
+                found = r + 1;
+            }
+            if (many) chosen = choose_exactly<N>(p, t, top, lane);
+            else if (near) chosen = order_exactly<N>(p, t, top, lane, chosen, found);
+            if (!p.sigmoid) {  // the weights' sum, of exp itself
+                float part = 0.f;
+#pragma unroll
+                for (int j = 0; j < N; ++j) part += expf(x[j] - top);
+                total = warp_sum(part);
+            }
+        }
+        float s = 0.f;
+        if (chosen >= 0) {
+            const float v = counted(load_logit(p, t, chosen));
+            s = p.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / total;
+        }
+        if (p.renormalize) {
+            const float sum = warp_sum(s);
+            s = sum > 0.f ? s / sum : 0.f;
+        }
+        if (lane < p.k) {
+            p.ids[t * p.k + lane] = chosen;
+            p.w[t * p.k + lane] = chosen >= 0 ? s * p.scale : 0.f;
+        }
+    }
+}
+
+template <int N, bool BIAS>
+cudaError_t route_launch(RouteArgs p, int sms, cudaStream_t s) {
+    // rows as pairs of whole experts for every lane
+    const int size = p.wide ? 4 : 2;
+    p.vec = p.E == 32 * N && p.ld % 2 == 0 && ((uintptr_t)p.logits & (2 * size - 1)) == 0;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cudaLaunchAttribute at[1];
@@ -202,11 +303,14 @@ cudaError_t route_launch(const RouteArgs &p, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)lora_ceil_div(p.T, kThreads / 32), 1, 1);
+    const int need = lora_ceil_div(p.T, kThreads / 32), most = sms * kCtasPerSm;
+    cfg.gridDim = dim3((unsigned)(need < most ? need : most), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, route_kernel<N>, p);
+    return cudaLaunchKernelEx(&cfg, route_kernel<N, BIAS>, p);
 }
+
+std::atomic<int> g_route_sms[64];  // SM count per device, looked up once
 
 }  // namespace
 
@@ -236,9 +340,22 @@ extern "C" lora_status_t lora_moe_route(const lora_route_desc_t *desc, const voi
     p.ids = topk_ids;
     p.w = topk_w;
     cudaStream_t s = (cudaStream_t)stream;
-    LORA_CUDA_TRY(d.n_experts <= 64    ? route_launch<2>(p, s)
-                  : d.n_experts <= 256 ? route_launch<8>(p, s)
-                                       : route_launch<32>(p, s));
+    int dev = 0;
+    LORA_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return LORA_ERR_INVALID_ARG;
+    int sms = g_route_sms[dev].load(std::memory_order_relaxed);
+    if (!sms) {
+        LORA_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        g_route_sms[dev].store(sms, std::memory_order_relaxed);
+    }
+    if (bias)
+        LORA_CUDA_TRY(d.n_experts <= 64    ? (route_launch<2, true>(p, sms, s))
+                      : d.n_experts <= 256 ? (route_launch<8, true>(p, sms, s))
+                                           : (route_launch<32, true>(p, sms, s)));
+    else
+        LORA_CUDA_TRY(d.n_experts <= 64    ? (route_launch<2, false>(p, sms, s))
+                      : d.n_experts <= 256 ? (route_launch<8, false>(p, sms, s))
+                                           : (route_launch<32, false>(p, sms, s)));
     lora_note_launch();
     return LORA_OK;
 }
