@@ -52,7 +52,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxE = LORA_ROUTE_MAX_EXPERTS, kMaxP = LORA_MOE_LAYER_MAX_PAIRS;
-constexpr int kGroup = 64;                    // pairs of a group
+constexpr int kGroup = 64;                    // most pairs of a group
 constexpr int kRows = 256, kTile = 128;       // weight rows of a unit, of an MMA
 constexpr int kBK = 64;                       // columns of a block: one 128-byte swizzle row
 constexpr uint32_t kABytes = kRows * kBK * 2;
@@ -85,6 +85,8 @@ struct LayerArgs {
     float *part;                  // [CTA][2][kGroup][kTile] sums of shared units
     int *flags;                   // [2][CTA] part is there (up, down)
     int grid, spin_limit;
+    int group;                    // pairs of a group (8, 16, 32 or 64)
+    int single;                   // shrink13: a pair to a CTA
 };
 
 __device__ __forceinline__ int expert_of(const LayerArgs &p, int pair, bool note) {
@@ -136,7 +138,16 @@ __global__ void __launch_bounds__(kThreads, 3) shrink13_kernel(const LayerArgs p
     asm volatile("griddepcontrol.launch_dependents;");
     const int count = p.shared ? p.T : p.P, sets = gridDim.x, me = blockIdx.x;
     uint32_t *key = found + count;
-    for (int i0 = tid; i0 < count; i0 += kAhead * kThreads) {
+    // few pairs: a CTA takes one, whoever else has its adapter
+    const bool single = !p.shared && gridDim.z == 1 && sets == p.P && p.single;
+    int e_me = me;
+    if (single) {
+        const int e = p.ids[me], a = p.idx[me / p.K];
+        if (e < 0 || e >= p.E || a < 0 || a >= p.L) return;
+        e_me = e;
+        if (tid == 0) key[0] = (uint32_t)a << 12 | (uint32_t)me, s_n = 1;
+    }
+    for (int i0 = single ? count : tid; i0 < count; i0 += kAhead * kThreads) {
         int e[kAhead], a[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
@@ -152,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 3) shrink13_kernel(const LayerArgs p
     __syncthreads();
     const int n = s_n;
     // in order, whatever order they were found in; those of slots without an adapter go unused
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n && !single; i += kThreads) {
         const uint32_t mine = found[i];
         int before = 0;
         for (int j = 0; j < n; ++j) before += found[j] < mine;
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 3) shrink13_kernel(const LayerArgs p
         if (b % (int)gridDim.z != (int)blockIdx.z) continue;
         const int rank = p.rank[slot];
         const float scale = p.scale[slot];
-        const uint16_t *A = p.A[m] + (long long)slot * p.a_ss[m] + (p.shared ? 0 : (long long)me * p.a_es[m]);
+        const uint16_t *A = p.A[m] + (long long)slot * p.a_ss[m] + (p.shared ? 0 : (long long)e_me * p.a_es[m]);
         const int i = (int)(key[first + min(g, few - 1)] & 0xfffu);
         const uint16_t *x = p.x + (long long)(p.shared ? i : i / p.K) * p.ldx + c0;
         const uint16_t *row0 = A + (long long)min(r0 + g, p.R - 1) * p.D + c0, *row1 = A + (long long)min(r0 + g + 8, p.R - 1) * p.D + c0;
@@ -379,7 +390,7 @@ __device__ int find_groups(const LayerArgs &p, Shared &s) {
         const int lane = threadIdx.x;
         int groups = 0, pairs = 0;
         for (int e0 = 0; e0 <= p.E; e0 += 32) {
-            const int c = e0 + lane < p.E ? s.u.g.count[e0 + lane] : 0, n = (c + kGroup - 1) / kGroup;
+            const int c = e0 + lane < p.E ? s.u.g.count[e0 + lane] : 0, n = (c + p.group - 1) / p.group;
             int cs = c, ns = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -422,8 +433,8 @@ __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
             at += __popc(m);
         }
         __syncwarp();
-        for (int g = first; sizeof(s.u.g.slots) > 2 && g < first + n; g += kGroup) {
-            const int few = min(kGroup, first + n - g);
+        for (int g = first; sizeof(s.u.g.slots) > 2 && g < first + n; g += p.group) {
+            const int few = min(p.group, first + n - g);
             // keys that are all different: the slot, then the place
             uint16_t pair[2];
             unsigned key[2];
@@ -451,7 +462,8 @@ __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
 // What a CTA does: blocks [b0, b1) of all the units' blocks in a row.
 struct Range {
     int b0, b1, total, n;  // n CTAs share them
-    __device__ __forceinline__ int start(int c) const { return (int)((long long)total * c / n); }
+    // total * c / n, whose parts stay below 2^31
+    __device__ __forceinline__ int start(int c) const { return total / n * c + (int)((unsigned)(total % n * c) / (unsigned)n); }
 };
 
 // The CTA's part of unit u, and what the unit is.
@@ -468,8 +480,8 @@ __device__ __forceinline__ Part part_of(const StreamArgs &q, const Shared &s, co
     const int g = u / q.MT;
     x.m = u - g * q.MT;
     x.e = expert_of_group(q.a, s, g);
-    const int first = s.pairs[x.e] + (g - s.groups[x.e]) * kGroup;
-    x.n = min(kGroup, s.pairs[x.e + 1] - first);
+    const int first = s.pairs[x.e] + (g - s.groups[x.e]) * q.a.group;
+    x.n = min(q.a.group, s.pairs[x.e + 1] - first);
     x.pos = first;
     x.at = first - s.pairs[e_first];
     return x;
@@ -920,8 +932,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                     // sums that other CTAs have left of this unit
                     if (last && x.k0 > 0) {
                         // the CTA that has the unit's first block: start(f) <= u KB < start(f + 1)
-                        from = (int)((long long)u * q.KB * r.n / r.total);
-                        while (r.start(from) > u * q.KB) --from;
+                        from = max(0, c - (int)((unsigned)x.k0 * (unsigned)r.n / (unsigned)r.total) - 1);
                         while (r.start(from + 1) <= u * q.KB) ++from;
                         if (tid < c - from) {
                             int polls = 0;
@@ -962,6 +973,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                             __stcg(my_part + (size_t)(kGroup + col + j) * kTile + row, v[j]);
                         }
                     } else {
+#pragma unroll 2
                         for (int f = from; f < c; ++f) {
                             const float *o = p.part + (size_t)f * 2 * kGroup * kTile;
 #pragma unroll
@@ -1203,6 +1215,13 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     p.y = (float *)(ws + c.y);
     p.grid = sms;
     p.spin_limit = lora_spin_limit();
+    // Few units: smaller groups, which read weights more often (from L2) but share out the work behind the products.
+    // 37 tokens over 6 experts of 1040 x 272 with adapters 61 us with groups of 64, 33 with groups of 8.
+    const int experts = p.P < d.n_experts ? p.P : d.n_experts, each = lora_ceil_div(p.P, experts), mt = lora_ceil_div(d.d_mlp, kTile);
+    p.group = kGroup;
+    while (p.group > kBatchCols && (int64_t)experts * lora_ceil_div(each, p.group) * mt * 2 <= sms) p.group /= 2;
+    // A pair to a CTA of shrink13: no search for pairs, but rows of A that pairs share are read for each.
+    p.single = p.P <= 256;
     if (pool) {
         const lora_pool_desc_t &q = pool->desc;
         p.L = q.max_loras;
@@ -1240,8 +1259,8 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     up.a = down.a = p;
     if (pool) {
         // experts, or as many sets of slots as there can be; CTAs that share the batches of one
-        const int sets = !p.shared ? p.E : p.L < T ? p.L : T, chunks = lora_ceil_div(p.R, kRanks);
-        const int slots = 3 * sms / (sets * p.n13 * chunks), share = slots < 1 ? 1 : slots > 8 ? 8 : slots;
+        const int chunks = lora_ceil_div(p.R, kRanks), sets = !p.shared ? p.single ? p.P : p.E : p.L < T ? p.L : T;
+        const int slots = 3 * sms / (sets * p.n13 * chunks), share = p.single || slots < 1 ? 1 : slots > 8 ? 8 : slots;
         const dim3 grid((unsigned)sets, (unsigned)(p.n13 * chunks), (unsigned)(share < T ? share : T));
         LORA_CUDA_TRY(launch(shrink13_kernel, grid, kThreads, (size_t)p.P * 8, s, p, chunks));
     }
