@@ -265,7 +265,8 @@ struct SharedOf {
     alignas(16) union {
         struct {
             int count[kMaxE];
-            uint16_t ids[kMaxP], slots[ADAPT ? kMaxP : 1];
+            uint16_t ids[kMaxP], at[kMaxP], slots[ADAPT ? kMaxP : 1];  // of a pair: expert, place among the expert's as counted
+            uint32_t key[kMaxP];                                       // slot << 12 | pair, by expert
         } g;  // while groups are found
         struct {
             float delta[kBatchCols][kDPitch];  // the adapters' part of eight columns
@@ -378,12 +379,25 @@ template <class Shared>
 __device__ int find_groups(const LayerArgs &p, Shared &s) {
     for (int i = threadIdx.x; i < p.E; i += kStreamThreads) s.u.g.count[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.P; i += kStreamThreads) {
-        const int e = p.ids[i];
-        const bool ok = e >= 0 && e < p.E;
-        s.u.g.ids[i] = ok ? (uint16_t)e : 0xffffu;
-        if (sizeof(s.u.g.slots) > 2) s.u.g.slots[i] = (uint16_t)min((unsigned)p.idx[i / p.K], 0xffffu);
-        if (ok) atomicAdd(&s.u.g.count[e], 1);
+    constexpr int kIds = 4;
+    constexpr bool kSlots = sizeof(s.u.g.slots) > 2;
+    for (int i0 = threadIdx.x; i0 < p.P; i0 += kIds * kStreamThreads) {
+        int e[kIds], a[kIds];
+#pragma unroll
+        for (int j = 0; j < kIds; ++j) {
+            const int i = i0 + j * kStreamThreads;
+            e[j] = i < p.P ? p.ids[i] : -1;
+            a[j] = kSlots && i < p.P ? p.idx[i / p.K] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kIds; ++j) {
+            const int i = i0 + j * kStreamThreads;
+            if (i >= p.P) break;
+            const bool ok = e[j] >= 0 && e[j] < p.E;
+            s.u.g.ids[i] = ok ? (uint16_t)e[j] : 0xffffu;
+            if (kSlots) s.u.g.slots[i] = (uint16_t)min((unsigned)a[j], 0xffffu);
+            if (ok) s.u.g.at[i] = (uint16_t)atomicAdd(&s.u.g.count[e[j]], 1);
+        }
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -418,44 +432,26 @@ __device__ __forceinline__ int expert_of_group(const LayerArgs &p, const Shared 
     }
     return lo;
 }
-// The pairs of experts e0..e1, each expert's by a warp: in their order, with adapters those of a group by slot.
+// The pairs of experts e0..e1, an expert's by slot (with adapters) and in their order: the same in every CTA, whatever
+// the order in which they were counted.
 template <class Shared>
 __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = e0 + warp; e <= e1; e += kStreamThreads / 32) {
-        const int first = s.pairs[e] - s.pairs[e0], n = s.pairs[e + 1] - s.pairs[e];
-        if (n == 0) continue;
-        int at = first;
-        for (int i = 0; i < p.P; i += 32) {
-            const bool mine = i + lane < p.P && s.u.g.ids[i + lane] == e;
-            const unsigned m = __ballot_sync(kAll, mine);
-            if (mine) s.list[at + __popc(m & ((1u << lane) - 1))] = (uint16_t)(i + lane);
-            at += __popc(m);
-        }
-        __syncwarp();
-        for (int g = first; sizeof(s.u.g.slots) > 2 && g < first + n; g += p.group) {
-            const int few = min(p.group, first + n - g);
-            // keys that are all different: the slot, then the place
-            uint16_t pair[2];
-            unsigned key[2];
-            int before[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int i = j * 32 + lane;
-                pair[j] = i < few ? s.list[g + i] : 0;
-                key[j] = (i < few ? (unsigned)s.u.g.slots[pair[j]] : 0xffffu) << 6 | (unsigned)i;
-            }
-            for (int j = 0; j < few; ++j) {
-                const unsigned other = __shfl_sync(kAll, j < 32 ? key[0] : key[1], j & 31);
-                before[0] += other < key[0];
-                before[1] += other < key[1];
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j * 32 + lane < few) s.list[g + before[j]] = pair[j];
-            __syncwarp();
-        }
+    const int base = s.pairs[e0];
+    for (int i = threadIdx.x; i < p.P; i += kStreamThreads) {
+        const int e = s.u.g.ids[i];
+        if (e < e0 || e > e1) continue;
+        const uint32_t slot = sizeof(s.u.g.slots) > 2 ? s.u.g.slots[i] : 0u;
+        s.u.g.key[s.pairs[e] - base + s.u.g.at[i]] = slot << 12 | (uint32_t)i;
+    }
+    __syncthreads();
+    const int n = s.pairs[e1 + 1] - base;
+    for (int i = threadIdx.x; i < n; i += kStreamThreads) {
+        const uint32_t mine = s.u.g.key[i];
+        const int e = s.u.g.ids[mine & 0xfffu], first = s.pairs[e] - base, end = s.pairs[e + 1] - base;
+        int place = first;
+#pragma unroll 4
+        for (int j = first; j < end; ++j) place += s.u.g.key[j] < mine;
+        s.list[place] = (uint16_t)(mine & 0xfffu);
     }
 }
 
@@ -1125,7 +1121,8 @@ cudaError_t device_sms(int &dev, int &sms) {
     if (sms) return cudaSuccess;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if ((e = set_smem<false, false>()) != cudaSuccess || (e = set_smem<false, true>()) != cudaSuccess ||
-        (e = set_smem<true, false>()) != cudaSuccess || (e = set_smem<true, true>()) != cudaSuccess)
+        (e = set_smem<true, false>()) != cudaSuccess || (e = set_smem<true, true>()) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(shrink13_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxP * 8)) != cudaSuccess)
         return e;
     g_devices[dev].sms.store(sms, std::memory_order_release);
     return cudaSuccess;

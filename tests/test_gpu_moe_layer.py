@@ -41,7 +41,7 @@ def test_one_expert_takes_every_token(T):
     run(T, 1, 1, 128, 64, adapters=2, rank=8, seed=T)
 
 
-@pytest.mark.parametrize("T,E,K", [(100, 2, 2), (40, 3, 3), (300, 5, 2), (128, 1, 32)])
+@pytest.mark.parametrize("T,E,K", [(100, 2, 2), (40, 3, 3), (300, 5, 2), (128, 1, 32), (128, 40, 32), (600, 7, 2)])
 def test_many_pairs_of_an_expert(T, E, K):
     run(T, E, K, 64, 72, adapters=3, rank=8, seed=T)
 
