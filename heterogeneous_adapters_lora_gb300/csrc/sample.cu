@@ -43,7 +43,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMagLo = 72 * 128, kMags = 64 * 128;  // magnitudes [2^-55, 2^9) as bf16 bits
 constexpr int kBins = 2 * kMags + 1;                // by magnitude, the sign above it, 0 last
 constexpr int kPlaces = 2 * kMags;                  // of the order; +2^-55 has none
-constexpr int kRounds = kPlaces / kThreads;         // of a place per thread
+constexpr int kRounds = kPlaces / kThreads / 4;     // of four places per thread
 constexpr int kMostCtas = 8;
 constexpr int kWinBins = 4096;
 constexpr int kWindows = 65536 / kWinBins;
@@ -72,10 +72,8 @@ __device__ __forceinline__ float value_of(unsigned key) {
     return __uint_as_float(b << 16);
 }
 
-// Places of the one window, in descending order of values: positive magnitudes, 0, negative ones.
-__device__ __forceinline__ int bin_of_place(int place) {
-    return place < kMags - 1 ? kMags - 1 - place : place == kMags - 1 ? 2 * kMags : place;
-}
+// Places of the one window, in descending order of values: positive magnitudes, 0, negative ones (bins
+// kMags - 1 to 1, the one of 0, kMags to 2 kMags - 1).
 __device__ __forceinline__ unsigned key_of_place(int place, int window) {
     if (window >= 0) return (unsigned)(window * kWinBins + kWinBins - 1 - place);
     if (place == kMags - 1) return 0x8000u;
@@ -187,7 +185,7 @@ struct Told {
 };
 
 struct Shared {
-    unsigned bins[kBins + 7];                         // by bits; or a window's in descending order
+    alignas(16) unsigned bins[kBins + 7];             // by bits; or a window's in descending order
     unsigned list[kPlaces / 2];                       // a slice's entries, where two CTAs or more share the row
     u64 pw[192];
     u64 warp_lo[kWarps], warp_hi[kWarps];  // 128-bit partial sums
@@ -224,18 +222,23 @@ __device__ __forceinline__ Sums scan(Shared &s, Sums mine, Sums &total) {
         s.warp_n[warp] = inc.n;
     }
     __syncthreads();
-    Sums before = {0, 0};
-    total = {0, 0};
-#pragma unroll 1
-    for (int w = 0; w < kWarps; ++w) {
-        const u128 m = join(s.warp_hi[w], s.warp_lo[w]);
-        if (w < warp) {
-            before.mass += m;
-            before.n += s.warp_n[w];
+    static_assert(kWarps == 16, "a warp's sums to a lane of half a warp");
+    Sums all = {join(s.warp_hi[lane & 15], s.warp_lo[lane & 15]), s.warp_n[lane & 15]};
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const u64 hi = __shfl_up_sync(kAll, (u64)(all.mass >> 64), o, 16), lo = __shfl_up_sync(kAll, (u64)all.mass, o, 16);
+        const int n = __shfl_up_sync(kAll, all.n, o, 16);
+        if ((lane & 15) >= o) {
+            all.mass += join(hi, lo);
+            all.n += n;
         }
-        total.mass += m;
-        total.n += s.warp_n[w];
     }
+    total.mass = join(__shfl_sync(kAll, (u64)(all.mass >> 64), 15), __shfl_sync(kAll, (u64)all.mass, 15));
+    total.n = __shfl_sync(kAll, all.n, 15);
+    const int ahead = warp ? warp - 1 : 0;
+    Sums before = {join(__shfl_sync(kAll, (u64)(all.mass >> 64), ahead), __shfl_sync(kAll, (u64)all.mass, ahead)),
+                   __shfl_sync(kAll, all.n, ahead)};
+    if (!warp) before = {0, 0};
     before.mass += inc.mass - mine.mass;
     before.n += inc.n - mine.n;
     return before;
@@ -278,35 +281,55 @@ struct Entries {
 constexpr unsigned kColumns = (1u << 18) - 1;
 static_assert(LORA_MAX_VOCAB <= kColumns && kPlaces <= 1 << 14 && kWinBins <= 1 << 14, "an entry's parts");
 
-// Writes the entries of places first + j * kThreads * .. : a warp has rounds * 32 places in a row, count(place)
-// columns each; `list` may be where the counts are.
+// Writes the entries of a slice of 4 * kThreads * rounds places from `first` on.  four(place): the columns of four
+// places in a row, in their order; a warp has rounds * 128 of them.  `list` may be where the counts are.
 template <int MAX, typename F>
-__device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int first, int rounds, F count) {
+__device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int first, int rounds, F four) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    first += warp * rounds * 32 + lane;
-    unsigned c[MAX];
+    first += (warp * rounds * 32 + lane) * 4;
+    uint4 c[MAX];
+    unsigned some = 0;  // rounds in which the warp has any
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < MAX; ++j) {
-        c[j] = j < rounds ? count(first + j * 32) : 0u;
-        mine += c[j] != 0u;
+        c[j] = j < rounds ? four(first + j * 128) : make_uint4(0, 0, 0, 0);
+        const int here = (c[j].x != 0) + (c[j].y != 0) + (c[j].z != 0) + (c[j].w != 0);
+        mine += here;
+        if (__any_sync(kAll, here)) some |= 1u << j;
     }
     mine = (int)__reduce_add_sync(kAll, (unsigned)mine);
     if (lane == 0) s.warp_n[warp] = mine;
     __syncthreads();  // (all counts have been read)
-    int at = 0, n = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        at += w < warp ? s.warp_n[w] : 0;
-        n += s.warp_n[w];
-    }
+    const int all = s.warp_n[lane & 15], n = (int)__reduce_add_sync(kAll, lane < 16 ? (unsigned)all : 0u);
+    int at = (int)__reduce_add_sync(kAll, lane < warp ? (unsigned)all : 0u);
 #pragma unroll
     for (int j = 0; j < MAX; ++j) {
-        const unsigned some = __ballot_sync(kAll, c[j] != 0u);
-        if (c[j]) list[at + __popc(some & ((1u << lane) - 1))] = (unsigned)(first + j * 32) << 18 | c[j];
-        at += __popc(some);
+        if (!(some >> j & 1)) continue;
+        const unsigned q[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+        const int here = (q[0] != 0) + (q[1] != 0) + (q[2] != 0) + (q[3] != 0);
+        int upto = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int k = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += k;
+        }
+        int to = at + upto - here;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (q[k]) list[to++] = (unsigned)(first + j * 128 + k) << 18 | q[k];
+        at += __shfl_sync(kAll, upto, 31);
     }
     __syncthreads();
     return n;
+}
+
+// The columns of four places of the one window, added up over C CTAs' bins; places of 0 and up to it come in
+// descending order of the bins.
+template <typename L>
+__device__ __forceinline__ uint4 four_places(int place, L load) {
+    if (place >= kMags) return load(place);
+    const uint4 v = load(kMags - 4 - place);
+    return make_uint4(v.w, v.z, v.y, v.x);
 }
 
 // Sums of the entries in `total`; of their beginning that weighs at least `least` a column in s.told.
@@ -404,10 +427,10 @@ __device__ __noinline__ void count_window(Shared &s, const uint16_t *row, int V,
 
 __device__ __noinline__ void window_entries(Shared &s, const uint16_t *row, int V, int window, u64 least, Entries &q, Sums &all) {
     count_window(s, row, V, window);
-    constexpr int kPer = kWinBins / kThreads;
+    constexpr int kPer = kWinBins / kThreads / 4;
     q.list = s.bins;
     q.window = window;
-    q.n = write_entries<kPer>(s, s.bins, 0, kPer, [&](int place) { return s.bins[place]; });
+    q.n = write_entries<kPer>(s, s.bins, 0, kPer, [&](int place) { return *(const uint4 *)&s.bins[place]; });
     add_up(s, q, least, all);
 }
 
@@ -473,6 +496,11 @@ __device__ __forceinline__ uint32_t peer_address(const void *local, int peer) {
 __device__ __forceinline__ unsigned load_peer(uint32_t a) {
     unsigned v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 load_peer4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
 __device__ __forceinline__ void store_peer(uint32_t a, unsigned v) {
@@ -580,15 +608,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     if (lane == 0 && low) atomicMax(&s.told.low, low);
     if (__any_sync(kAll, counter.odd) && lane == 0) s.told.odd = 1;
     __syncthreads();
-    if (tid == 0 && s.bins[0]) s.told.odd = 1;  // +2^-55
+    if (tid == 0) {
+        if (s.bins[0]) s.told.odd = 1;  // +2^-55, whose place is that of 0
+        s.bins[0] = s.bins[2 * kMags];
+    }
+    __syncthreads();
     int top = kPlaces;
-    for (int i = tid; i < kPlaces; i += kThreads)
-        if (s.bins[bin_of_place(i)]) {
-            top = i;
-            break;
-        }
-    top = (int)__reduce_min_sync(kAll, (unsigned)top);
-    if (lane == 0) atomicMin(&s.told.top, top);
+    for (int i = tid * 4; i < kPlaces && top == kPlaces && i < *(volatile int *)&s.told.top; i += kThreads * 4) {
+        const uint4 v = four_places(i, [&](int bin) { return *(const uint4 *)&s.bins[bin]; });
+        if (v.x | v.y | v.z | v.w) top = i + (v.x ? 0 : v.y ? 1 : v.z ? 2 : 3);
+        if (top < kPlaces) atomicMin(&s.told.top, top);
+    }
     const float temperature = p.temperature ? p.temperature[t] : 1.f;
     const bool greedy = !(temperature > 0.f);
     const float min_p = p.min_p ? p.min_p[t] : 0.f, top_p = p.top_p ? p.top_p[t] : 1.f, u = p.uniform ? p.uniform[t] : 0.f;
@@ -633,20 +663,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         window_sums(s, row, p.V, least, total, heavy);
     } else {
         entries.window = -1;
-        const int rounds = kRounds / C, first = c * rounds * kThreads;
+        const int rounds = kRounds / C, first = c * rounds * 4 * kThreads;
         if (C == 1) {
             entries.list = s.bins;
-            entries.n = write_entries<kRounds>(s, s.bins, 0, kRounds, [&](int place) { return s.bins[bin_of_place(place)]; });
+            entries.n = write_entries<kRounds>(s, s.bins, 0, kRounds, [&](int place) {
+                return four_places(place, [&](int bin) { return *(const uint4 *)&s.bins[bin]; });
+            });
         } else {
             // a slice's counts in the parts of all
             entries.list = s.list;
             entries.n = write_entries<kRounds / 2>(s, s.list, first, rounds, [&](int place) {
-                const unsigned *at = s.bins + bin_of_place(place);
-                unsigned sum = 0;
+                return four_places(place, [&](int bin) {
+                    uint4 sum = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int k = 0; k < kMostCtas; ++k)
-                    if (k < C) sum += load_peer(peer_address(at, k));
-                return sum;
+                    for (int k = 0; k < kMostCtas; ++k)
+                        if (k < C) {
+                            const uint4 v = load_peer4(peer_address(&s.bins[bin], k));
+                            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                        }
+                    return sum;
+                });
             });
         }
         add_up(s, entries, least, total);
