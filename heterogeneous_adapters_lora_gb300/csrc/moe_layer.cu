@@ -923,31 +923,43 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                         epi.next_task(task, x, of);
                     }
                 }
-                if (b0 == 0) {
-                    ok = wait(&s.accf[buf], (uint32_t)((i >> 1) & 1), p, s);
-                    // sums that other CTAs have left of this unit
-                    if (last && x.k0 > 0) {
-                        // the CTA that has the unit's first block: start(f) <= u KB < start(f + 1)
-                        from = max(0, c - (int)((unsigned)x.k0 * (unsigned)r.n / (unsigned)r.total) - 1);
-                        while (r.start(from + 1) <= u * q.KB) ++from;
-                        if (tid < c - from) {
-                            int polls = 0;
-                            while (ok && ld_acquire_gpu(flags + from + tid) == 0) {
-                                if (*(volatile int *)&s.abort) ok = false;
-                                else if (++polls > p.spin_limit) {
-                                    note_timeout(p, s);
-                                    ok = false;
-                                } else
-                                    __nanosleep(64);
-                            }
+                const int col = b0 + half * 4;
+                if (b0 == 0 && last && x.k0 > 0) {
+                    // Sums that other CTAs have left of this unit, while its products are still to come.
+                    // The CTA that has the unit's first block: start(f) <= u KB < start(f + 1)
+                    from = max(0, c - (int)((unsigned)x.k0 * (unsigned)r.n / (unsigned)r.total) - 1);
+                    while (r.start(from + 1) <= u * q.KB) ++from;
+                    if (tid < c - from) {
+                        int polls = 0;
+                        while (ok && ld_acquire_gpu(flags + from + tid) == 0) {
+                            if (*(volatile int *)&s.abort) ok = false;
+                            else if (++polls > p.spin_limit) {
+                                note_timeout(p, s);
+                                ok = false;
+                            } else
+                                __nanosleep(64);
                         }
                     }
+                    ok = bar_and(1, kEpiThreads, ok);
+                }
+                float pg[4] = {0.f, 0.f, 0.f, 0.f}, pv[4] = {0.f, 0.f, 0.f, 0.f};
+                if (col < x.n && ok)
+#pragma unroll 2
+                    for (int f = from; f < c; ++f) {
+                        const float *o = p.part + (size_t)f * 2 * kGroup * kTile;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            pg[j] += __ldcg(o + (size_t)(col + j) * kTile + row);
+                            pv[j] += __ldcg(o + (size_t)(kGroup + col + j) * kTile + row);
+                        }
+                    }
+                if (b0 == 0) {
+                    ok = ok && wait(&s.accf[buf], (uint32_t)((i >> 1) & 1), p, s);
                     // one wait that gave up ends the work of all
                     ok = bar_and(1, kEpiThreads, ok);
                     if (!ok) break;
                     tc::tc_fence_after();
                 }
-                const int col = b0 + half * 4;
                 if (col < x.n) {
                     float g[4], v[4];  // gate and up; or the two tiles' rows
                     tmem_ld4(acc + col, g);
@@ -969,15 +981,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                             __stcg(my_part + (size_t)(kGroup + col + j) * kTile + row, v[j]);
                         }
                     } else {
-#pragma unroll 2
-                        for (int f = from; f < c; ++f) {
-                            const float *o = p.part + (size_t)f * 2 * kGroup * kTile;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                g[j] += __ldcg(o + (size_t)(col + j) * kTile + row);
-                                v[j] += __ldcg(o + (size_t)(kGroup + col + j) * kTile + row);
-                            }
-                        }
+                        for (int j = 0; j < 4; ++j) g[j] += pg[j], v[j] += pv[j];
                         const int at = x.m * (DOWN ? kRows : kTile) + row;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -1044,17 +1049,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
 // The pairs' results of a token in their order; the flags are left as they were found.
 __global__ void __launch_bounds__(kThreads) combine_kernel(const LayerArgs p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (i < 2 * p.grid) p.flags[i] = 0;
     const int per = p.D / 8;
-    if (i >= (long long)p.T * per) return;
+    const bool mine = i < (long long)p.T * per;
     const int t = (int)(i / per), d = (int)(i % per) * 8;
-    if (d == 0) slot_of(p, t, true);
+    unsigned there = 0;  // pairs that have an expert (ids are older than the kernel before this one)
+    if (mine)
+        for (int k = 0; k < p.K; ++k) there |= (unsigned)(expert_of(p, t * p.K + k, d == 0) >= 0) << k;
+    if (mine && d == 0) slot_of(p, t, true);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (i < 2 * p.grid) p.flags[i] = 0;
+    if (!mine) return;
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int k = 0; k < p.K; ++k) {
         const int pair = t * p.K + k;
-        if (expert_of(p, pair, d == 0) < 0) continue;
+        if (!(there >> k & 1)) continue;
         const float *y = p.y + (long long)pair * p.D + d;
         const float4 a = __ldcg((const float4 *)y), b = __ldcg((const float4 *)(y + 4));
         sum[0] += a.x, sum[1] += a.y, sum[2] += a.z, sum[3] += a.w;
