@@ -53,6 +53,11 @@ def test_one_rank_slice_of_every_size():
         run(3, 2, 1, D, 80, adapters=2, rank=8, seed=D)
 
 
+@pytest.mark.parametrize("T,E,K,adapters", [(1, 1024, 32, 2), (9, 300, 4, 3), (130, 200, 1, 0)])
+def test_many_experts(T, E, K, adapters):
+    run(T, E, K, 64, 40, adapters=adapters, rank=8, seed=E)
+
+
 def test_padded_rows():
     run(11, 4, 2, 200, 104, adapters=2, rank=16, pads=(8, 16, 24, 40), seed=3)
 
