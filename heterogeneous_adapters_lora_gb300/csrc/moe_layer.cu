@@ -105,15 +105,16 @@ __device__ __forceinline__ int slot_of(const LayerArgs &p, int t, bool note) {
     return p.enabled[a] && p.rank[a] > 0 ? a : -1;
 }
 
-// A number as the sum of two bf16.
+// A number as the sum of two bf16; an infinite one is the first of them.
+__device__ __forceinline__ float rest(float v, float hi) { return fabsf(hi) < INFINITY ? v - hi : 0.f; }
 __device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
-    const __nv_bfloat16 a = __float2bfloat16_rn(v), b = __float2bfloat16_rn(v - __bfloat162float(a));
+    const __nv_bfloat16 a = __float2bfloat16_rn(v), b = __float2bfloat16_rn(rest(v, __bfloat162float(a)));
     hi = *(const uint16_t *)&a;
     lo = *(const uint16_t *)&b;
 }
 __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = bgmv::pack_bf16x2(a, b);
-    lo = bgmv::pack_bf16x2(a - bf16lo(hi), b - bf16hi(hi));
+    lo = bgmv::pack_bf16x2(rest(a, bf16lo(hi)), rest(b, bf16hi(hi)));
 }
 
 // v = scale A13 x.  A CTA takes an expert (shared outer: the slots of one

@@ -151,6 +151,20 @@ def test_not_a_number_stays_with_its_token():
     assert not torch.any(torch.isfinite(layer.out[6, :72]))
 
 
+@pytest.mark.parametrize("adapters", [0, 2])
+def test_infinite_h_is_infinite_in_the_result(adapters):
+    """act(g) u beyond fp32 for one token, weights above 0: infinity, as the formula in fp32 has it, not NaN."""
+    layer = Layer(5, 2, 2, 72, 64, adapters=adapters, rank=8, seed=7)
+    x, tiny = layer.x.clone(), 2.0 ** -20
+    x[3] = 1e25
+    values = dict(x=x, w13=layer.w13.abs() + tiny, w2=layer.w2.abs() + tiny)
+    if adapters:
+        values["idx"] = torch.tensor([0, 1, 0, -1, 1], dtype=torch.int32)
+    layer.batch(**values).call()
+    assert torch.all(layer.out[3, :72] == float("inf"))
+    assert torch.all(torch.isfinite(layer.out[[0, 1, 2, 4], :72]))
+
+
 def test_captured_with_another_workspace_and_replayed():
     layer = Layer(10, 4, 2, 128, 72, adapters=2, rank=8, seed=10)
     side = torch.cuda.Stream()
