@@ -31,7 +31,8 @@
  *    on the device set the pool's status word (LORA_ERR_DEVICE_INDEX) and the
  *    row is treated as idx -1; a cross-CTA wait that runs out of iterations
  *    sets LORA_ERR_TIMEOUT.  Read and clear it with lora_get_device_status (an
- *    attention plan has a word of its own: lora_attn_get_status).
+ *    attention plan has a word of its own: lora_attn_get_status; lora_moe_layer
+ *    takes a word from the caller).
  *  - A row is *active* when 0 <= idx < max_loras, the slot is enabled and its
  *    rank is > 0 (and, for MoE, its expert id is in range).  Inactive rows of
  *    y / ic1 / ic3 are left bit-identical.
@@ -384,15 +385,15 @@ LORA_API lora_status_t lora_get_device_status(const lora_pool_t *pool, void *str
 
 /* Bound on the polls of every cross-CTA wait of lora_apply_slices and
  * lora_moe_apply (default 1 << 20, each poll sleeps up to ~64 ns), and of the
- * waits for copies of lora_qk_norm_rope and those of the attention calls (each
- * poll up to ~1.5 us).  When a wait gives up, the device status (of
- * lora_qk_norm_rope: its status word; of the attention calls: the plan's)
- * becomes LORA_ERR_TIMEOUT and that work item is skipped (of lora_qk_norm_rope:
- * the tokens that the CTA has left, of which nothing is written; of the
- * attention calls: the output is not to be used, the next call is whole).  A
- * negative value makes every wait that is not already satisfied give up at once
- * (to exercise the error path; of the attention calls, one that is not within a
- * poll or two).  Process-wide. */
+ * waits for copies of lora_qk_norm_rope and those of the attention calls and of
+ * lora_moe_layer (each poll up to ~1.5 us).  When a wait gives up, the device
+ * status (of lora_qk_norm_rope and lora_moe_layer: the call's status word; of the
+ * attention calls: the plan's) becomes LORA_ERR_TIMEOUT and that work item is
+ * skipped (of lora_qk_norm_rope: the tokens that the CTA has left, of which
+ * nothing is written; of the attention calls and lora_moe_layer: the output is
+ * not to be used, the next call is whole).  A negative value makes every wait
+ * that is not already satisfied give up at once (to exercise the error path; of
+ * the attention calls, one that is not within a poll or two).  Process-wide. */
 LORA_API void lora_set_spin_limit(int32_t max_polls);
 
 /* The full LoRA linear layer of a dense pool (vLLM LoRA layer pages,
@@ -667,15 +668,17 @@ LORA_API size_t lora_moe_layer_workspace_bytes(const lora_moe_layer_desc_t *desc
  * slices of width F, or one of 2F), either layout; NULL = no adapters.  d_idx:
  * [T] int32 slots, -1 = none; NULL exactly when pool is NULL.  No metadata are
  * needed.  Rank and scale are read on the stream.
- * Every chosen expert's weights are read once for up to 64 of its pairs; the
- * call is meant for batches whose time is that of reading weights.
+ * A chosen expert's weights are read once for up to 64 of its pairs (8 to 32, the rest
+ * from L2, where that leaves too few pieces of work for the SMs); the call is meant for
+ * batches whose time is that of reading weights.
  * Sums are fp32; h, which the second product takes in 16 bits, goes as the sum
  * of two bf16; out is rounded once.  The result does not change from run to run.
  * An id of -1 is no expert, and a token without experts gets zeros.  Other ids outside
  * [0, n_experts) count as -1, slots outside [-1, max_loras) as no adapter, and both
  * set *status (an int32 device word, may be NULL) to LORA_ERR_DEVICE_INDEX.  A wait that
  * gives up (lora_set_spin_limit) sets it to LORA_ERR_TIMEOUT; out is not to be
- * used then, the next call is whole.  out must overlap nothing else.
+ * used then, the next call is whole.  The word is never cleared by a call.  out must
+ * overlap nothing else.
  * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, a field or a leading
  * dimension out of range, a pool of another device than the current one),
  * LORA_ERR_SHAPE (the pool's sizes), LORA_ERR_UNSUPPORTED (a dense pool, one that is
@@ -704,7 +707,7 @@ LORA_API lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const l
  * logprob -inf.  Weights and their sums are integers of 2^-62 of the largest
  * weight, accurate to about 10^-14, so that sums do not depend on their order and the
  * token is that of the exact formula but for numbers that close to a border.
- * Rows whose logits that matter are 0 or of magnitudes in [2^-23, 2^9) are read twice;
+ * Rows whose logits that matter are 0 or of magnitudes between 2^-55 and 2^9 are read twice;
  * others up to 22 times.
  * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, T < 0, ld < vocab_size or
  * not a multiple of 8), LORA_ERR_SHAPE (vocab_size < 1 or > LORA_MAX_VOCAB). */
