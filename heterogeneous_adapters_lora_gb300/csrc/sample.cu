@@ -106,30 +106,32 @@ struct Scale {
     float up;      // a power of two that logits are multiplied by, so that fp32 holds what follows
     float hi, lo;  // log2(e) / temperature / up as a sum
     float top;     // the largest logit, times up
+    int e;         // exponent of the temperature
 };
 
-// With temperature = m 2^e, m in [0.5, 1): logits times 2^-e, and log2(e) / m, a quotient and
-// its remainder's.  Where the power would make the largest logit exceed 2^100, a smaller one does: distinct logits
+// With temperature = m 2^e, m in [0.5, 1): log2(e) / m, a quotient and its remainder's; and logits times
+// 2^-e.  Where the power would make the largest logit exceed 2^100, a smaller one does: distinct logits
 // are then at least 2^91 apart, and every weight but the largest is 0 whatever the factor.
-__device__ __forceinline__ Scale make_scale(float temperature, float top) {
+__device__ __forceinline__ Scale begin_scale(float temperature) {
     constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kLog2e);
     Scale r;
-    int s = -2;
     r.hi = r.lo = 0.f;
+    r.e = 2;
     if (temperature < INFINITY) {
-        int e;
-        const float m = frexpf(temperature, &e);
-        s = max(-126, min(126, -e));
-        if (top != 0.f) s = min(s, 100 - ilogbf(top));
+        const float m = frexpf(temperature, &r.e);
         r.hi = kLog2e / m;
         r.lo = (fmaf(-r.hi, m, kLog2e) + kRest) / m;
-        const float rest = exp2f((float)min(-e - s, 30));
-        r.hi *= rest;
-        r.lo *= rest;
     }
+    return r;
+}
+__device__ __forceinline__ void end_scale(Scale &r, float top) {
+    int s = max(-126, min(126, -r.e));
+    if (top != 0.f) s = min(s, 100 - ilogbf(top));
+    const float rest = exp2f((float)min(-r.e - s, 30));
+    r.hi *= rest;
+    r.lo *= rest;
     r.up = __int_as_float((s + 127) << 23);
     r.top = top * r.up;
-    return r;
 }
 
 // (top - v) * log2(e) / temperature as hi + lo, to about 2^-46 of it.
@@ -163,15 +165,15 @@ __device__ __forceinline__ u64 weight62(const Scale &c, float v, const u64 *pw) 
     return w >> (1 + (high >> 18));
 }
 
+struct Sums {
+    u128 mass;
+    int n;
+};
+
 struct Found {
     unsigned key;
     int rank, n;  // which of the key's columns; columns up to and with it
     u64 lo, hi;   // ... and their weight
-};
-
-struct Sums {
-    u128 mass;
-    int n;
 };
 
 // What a CTA tells the others of its row.
@@ -181,6 +183,7 @@ struct Told {
     int odd;       // a key in the gaps of the one window, or above it
     u64 lo, hi, least_lo, least_hi;  // weight of its slice, and of the beginning of at least min_p a column
     int n, least_n;
+    int entries;   // places of its slice that are not empty
     int matches;   // columns of its part with the chosen key
 };
 
@@ -190,9 +193,11 @@ struct Shared {
     u64 pw[192];
     u64 warp_lo[kWarps], warp_hi[kWarps];  // 128-bit partial sums
     int warp_n[kWarps], last;
+    u64 pre_lo[kThreads], pre_hi[kThreads];  // sums ahead of a thread's entries
+    int pre_n[kThreads];
     Told told;
     Told all[kMostCtas];  // of every CTA
-    Found found[3];  // of each step
+    Found found;
     Scale scale;
     // many windows
     int coarse[kWindows];
@@ -259,6 +264,7 @@ __device__ __forceinline__ void each_vector(const uint16_t *row, int begin, int 
             if (i + j * step * 8 < whole) f(i + j * step * 8, v[j]);
     }
     if (at == 0)
+#pragma unroll 1
         for (int i = whole; i < end; ++i) g(i, (unsigned)row[i]);
 }
 // (where time matters less than the size of the code)
@@ -269,15 +275,16 @@ __device__ __forceinline__ void each_column(const uint16_t *row, int end, G g) {
 }
 
 // What a CTA has of the order: the places that are not empty, as place << 18 | columns (a row has
-// fewer than 2^18), `each` of them to a thread in a row.
+// fewer than 2^18), an equal number of them to a thread, in a row.
 struct Entries {
-    const unsigned *list;
-    int n, each, window;  // window: -1, the one
-    Sums before, own;     // sums ahead of this thread's entries, and theirs
-    __device__ __forceinline__ u64 weight(const Shared &s, unsigned entry) const {
-        return weight62(s.scale, value_of(key_of_place((int)(entry >> 18), window)), s.pw);
-    }
+    unsigned *list;
+    int n, window;  // window: -1, the one
+    Sums before;    // sums ahead of them
 };
+__device__ __forceinline__ u64 weight_of(const Shared &s, unsigned entry, int window) {
+    return weight62(s.scale, value_of(key_of_place((int)(entry >> 18), window)), s.pw);
+}
+__device__ __forceinline__ int each_of(int n) { return (n + kThreads - 1) / kThreads; }
 constexpr unsigned kColumns = (1u << 18) - 1;
 static_assert(LORA_MAX_VOCAB <= kColumns && kPlaces <= 1 << 14 && kWinBins <= 1 << 14, "an entry's parts");
 
@@ -306,18 +313,16 @@ __device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int firs
     for (int j = 0; j < MAX; ++j) {
         if (!(some >> j & 1)) continue;
         const unsigned q[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
-        const int here = (q[0] != 0) + (q[1] != 0) + (q[2] != 0) + (q[3] != 0);
-        int upto = here;
+        int to = at;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int k = __shfl_up_sync(kAll, upto, o);
-            if (lane >= o) upto += k;
+        for (int k = 0; k < 4; ++k) {
+            const unsigned some_k = __ballot_sync(kAll, q[k] != 0);
+            to += __popc(some_k & ((1u << lane) - 1));
+            at += __popc(some_k);
         }
-        int to = at + upto - here;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (q[k]) list[to++] = (unsigned)(first + j * 128 + k) << 18 | q[k];
-        at += __shfl_sync(kAll, upto, 31);
     }
     __syncthreads();
     return n;
@@ -332,22 +337,25 @@ __device__ __forceinline__ uint4 four_places(int place, L load) {
     return make_uint4(v.w, v.z, v.y, v.x);
 }
 
-// Sums of the entries in `total`; of their beginning that weighs at least `least` a column in s.told.
-__device__ __forceinline__ void add_up(Shared &s, Entries &q, u64 least, Sums &total) {
-    Sums much = {0, 0};
-    q.own = {0, 0};
-    q.each = (q.n + kThreads - 1) / kThreads;
-    const int begin = min(q.n, (int)threadIdx.x * q.each), end = min(q.n, begin + q.each);
+// Sums of the entries in `total`, those ahead of each thread's in s.pre; of their beginning that weighs at
+// least `least` a column in s.told.
+__device__ __forceinline__ void add_up(Shared &s, const Entries &q, u64 least, Sums &total) {
+    Sums much = {0, 0}, own = {0, 0};
+    const int each = each_of(q.n), begin = min(q.n, (int)threadIdx.x * each), end = min(q.n, begin + each);
 #pragma unroll 1
     for (int i = begin; i < end; ++i) {
         const unsigned entry = q.list[i];
         const int c = (int)(entry & kColumns);
-        const u64 w = q.weight(s, entry);
-        q.own.mass += (u128)w * (unsigned)c;
-        q.own.n += c;
-        if (w >= least) much = q.own;
+        const u64 w = weight_of(s, entry, q.window);
+        own.mass += (u128)w * (unsigned)c;
+        own.n += c;
+        if (w >= least) much = own;
     }
-    q.before = scan(s, q.own, total);
+    const Sums before = scan(s, own, total);
+    s.pre_hi[threadIdx.x] = (u64)(before.mass >> 64);
+    s.pre_lo[threadIdx.x] = (u64)before.mass;
+    s.pre_n[threadIdx.x] = before.n;
+    if (!least) return;
     // the last thread that has some ends that beginning
     if (threadIdx.x == 0) s.last = -1, s.told.least_n = 0, s.told.least_hi = 0, s.told.least_lo = 0;
     __syncthreads();
@@ -355,28 +363,79 @@ __device__ __forceinline__ void add_up(Shared &s, Entries &q, u64 least, Sums &t
     if (some && (threadIdx.x & 31) == 0) atomicMax(&s.last, (int)threadIdx.x + 31 - __clz(some));
     __syncthreads();
     if ((int)threadIdx.x == s.last) {
-        much.mass += q.before.mass;
-        much.n += q.before.n;
+        much.mass += before.mass;
+        much.n += before.n;
         s.told.least_hi = (u64)(much.mass >> 64);
         s.told.least_lo = (u64)much.mass;
         s.told.least_n = much.n;
     }
 }
 
+// ------------------------------------------------------------ clusters
+
+__device__ __forceinline__ void cluster_sync(int C) {
+    if (C == 1) {
+        __syncthreads();
+        return;
+    }
+    bgmv::cluster_arrive();
+    bgmv::cluster_wait();
+}
+__device__ __forceinline__ uint32_t peer_address(const void *local, int peer) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32_of(local)), "r"(peer));
+    return a;
+}
+__device__ __forceinline__ unsigned load_peer(uint32_t a) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ u64 load_peer8(uint32_t a) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 load_peer4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+// What every CTA of the row tells, in s.all.
+__device__ __forceinline__ void hear(Shared &s, int C) {
+    cluster_sync(C);  // all have told
+    constexpr int kWords = sizeof(Told) / 4;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < C * kWords; i += kThreads)
+        ((unsigned *)s.all)[i] = load_peer(peer_address((unsigned *)&s.told + i % kWords, i / kWords));
+    __syncthreads();
+}
+
 // The first column of the order at which the sum of weights exceeds `mass`, or that is number `n`,
-// whichever comes first, if it lies within the entries.  The warp whose thread has it looks through that
-// thread's entries, one a lane; the lane that has the column returns true.
-__device__ __forceinline__ bool look(const Shared &s, const Entries &q, u128 mass, int n, Found &out) {
-    const int lane = threadIdx.x & 31;
-    const bool here = q.before.mass <= mass && q.before.n < n && (q.before.mass + q.own.mass > mass || q.before.n + q.own.n >= n);
-    const unsigned who = __ballot_sync(kAll, here);
-    if (!who) return false;
-    const int owner = __ffs(who) - 1, i = ((int)threadIdx.x - lane + owner) * q.each + lane;
-    const u64 hi = __shfl_sync(kAll, (u64)(q.before.mass >> 64), owner), lo = __shfl_sync(kAll, (u64)q.before.mass, owner);
-    const int n0 = __shfl_sync(kAll, q.before.n, owner);
-    const unsigned entry = lane < q.each && i < q.n ? q.list[i] : 0u;
+// whichever comes first, if it is among the entries of CTA `peer` (q.n of them at q.list, behind q.before).
+// A warp's work: the thread that has it by two ballots over s.pre, then that thread's entries, one a lane.
+__device__ __forceinline__ Found look(const Shared &s, const Entries &q, int peer, u128 mass, int n) {
+    const int lane = threadIdx.x & 31, each = each_of(q.n);
+    int who = lane < kWarps ? lane * 32 : 0, n0 = 0;
+    u128 before = 0;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+        before = q.before.mass + join(load_peer8(peer_address(&s.pre_hi[who], peer)), load_peer8(peer_address(&s.pre_lo[who], peer)));
+        n0 = q.before.n + (int)load_peer(peer_address(&s.pre_n[who], peer));
+        const unsigned upto = __ballot_sync(kAll, before <= mass && n0 < n && (level || lane < kWarps));
+        const int at = upto ? 31 - __clz(upto) : 0;  // (that of lane 0 always is)
+        if (level) {
+            before = join(__shfl_sync(kAll, (u64)(before >> 64), at), __shfl_sync(kAll, (u64)before, at));
+            n0 = __shfl_sync(kAll, n0, at);
+            who = who - lane + at;
+        } else {
+            who = at * 32 + lane;
+        }
+    }
+    const int i = who * each + lane;
+    const unsigned entry = lane < each && i < q.n ? load_peer(peer_address(&q.list[i], peer)) : 0u;
     const int c = (int)(entry & kColumns);
-    const u64 w = c ? q.weight(s, entry) : 0ull;
+    const u64 w = c ? weight_of(s, entry, q.window) : 0ull;
     Sums sum = {(u128)w * (unsigned)c, c};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -387,29 +446,37 @@ __device__ __forceinline__ bool look(const Shared &s, const Entries &q, u128 mas
             sum.n += k;
         }
     }
-    sum.mass += join(hi, lo);
+    sum.mass += before;
     sum.n += n0;
     const unsigned past = __ballot_sync(kAll, c && (sum.mass > mass || sum.n >= n));
-    if (lane != __ffs(past) - 1) return false;
-    const u128 m0 = sum.mass - (u128)w * (unsigned)c;
-    const int k0 = sum.n - c, last = min(c, n - k0) - 1;
-    // smallest r with m0 + (r + 1) w > mass, at most the number asked for: a quotient below 2^18, from fp32 to within one
-    int r = last;
-    if (sum.mass > mass) {
-        const u128 gap = mass - m0;
-        const int down = gap >> 64 ? 64 - __clzll((u64)(gap >> 64)) : 0;
-        const float quotient = (float)(u64)(gap >> down) / (float)w * exp2f((float)down);
-        r = quotient < (float)last ? (int)quotient : last;
-        while (r > 0 && m0 + (u128)w * (unsigned)r > mass) --r;
-        while (r < last && m0 + (u128)w * (unsigned)(r + 1) <= mass) ++r;
+    const int winner = past ? __ffs(past) - 1 : 0;
+    Found f = {0, 0, 0, 0, 0};
+    if (lane == winner) {
+        const u128 m0 = sum.mass - (u128)w * (unsigned)c;
+        const int k0 = sum.n - c, last = min(c, n - k0) - 1;
+        // smallest r with m0 + (r + 1) w > mass, at most the number asked for: a quotient below 2^18, from fp32 to within one
+        int r = last;
+        if (sum.mass > mass) {
+            const u128 gap = mass - m0;
+            const int down = gap >> 64 ? 64 - __clzll((u64)(gap >> 64)) : 0;
+            const float quotient = (float)(u64)(gap >> down) / (float)w * exp2f((float)down);
+            r = quotient < (float)last ? (int)quotient : last;
+            while (r > 0 && m0 + (u128)w * (unsigned)r > mass) --r;
+            while (r < last && m0 + (u128)w * (unsigned)(r + 1) <= mass) ++r;
+        }
+        const u128 m = m0 + (u128)w * (unsigned)(r + 1);
+        f.key = key_of_place((int)(entry >> 18), q.window);
+        f.rank = r;
+        f.n = k0 + r + 1;
+        f.hi = (u64)(m >> 64);
+        f.lo = (u64)m;
     }
-    const u128 m = m0 + (u128)w * (unsigned)(r + 1);
-    out.key = key_of_place((int)(entry >> 18), q.window);
-    out.rank = r;
-    out.n = k0 + r + 1;
-    out.hi = (u64)(m >> 64);
-    out.lo = (u64)m;
-    return true;
+    f.key = __shfl_sync(kAll, f.key, winner);
+    f.rank = __shfl_sync(kAll, f.rank, winner);
+    f.n = __shfl_sync(kAll, f.n, winner);
+    f.hi = __shfl_sync(kAll, f.hi, winner);
+    f.lo = __shfl_sync(kAll, f.lo, winner);
+    return f;
 }
 
 // ------------------------------------------------------------ many windows (one CTA)
@@ -449,7 +516,7 @@ __device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, 
             Entries q;
             window_entries(s, row, V, w, least, q, all);
             __syncthreads();
-            if (s.told.least_n) heavy = {total.mass + join(s.told.least_hi, s.told.least_lo), total.n + s.told.least_n};
+            if (least && s.told.least_n) heavy = {total.mass + join(s.told.least_hi, s.told.least_lo), total.n + s.told.least_n};
             __syncthreads();
         }
         if (threadIdx.x == 0) {
@@ -474,45 +541,7 @@ __device__ __noinline__ void window_of(Shared &s, const uint16_t *row, int V, u1
         at.n += s.win_n[w];
     }
     window_entries(s, row, V, w, 0, q, all);
-    q.before.mass += at.mass;
-    q.before.n += at.n;
-}
-
-// ------------------------------------------------------------ clusters
-
-__device__ __forceinline__ void cluster_sync(int C) {
-    if (C == 1) {
-        __syncthreads();
-        return;
-    }
-    bgmv::cluster_arrive();
-    bgmv::cluster_wait();
-}
-__device__ __forceinline__ uint32_t peer_address(const void *local, int peer) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32_of(local)), "r"(peer));
-    return a;
-}
-__device__ __forceinline__ unsigned load_peer(uint32_t a) {
-    unsigned v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 load_peer4(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void store_peer(uint32_t a, unsigned v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-// What every CTA of the row tells, in s.all.
-__device__ __forceinline__ void hear(Shared &s, int C) {
-    cluster_sync(C);  // all have told
-    constexpr int kWords = sizeof(Told) / 4;
-    for (int i = threadIdx.x; i < C * kWords; i += kThreads)
-        ((unsigned *)s.all)[i] = C == 1 ? ((unsigned *)&s.told)[i] : load_peer(peer_address((unsigned *)&s.told + i % kWords, i / kWords));
-    __syncthreads();
+    q.before = at;
 }
 
 // floor(m * f) for 0 <= f < 1, and whether that is m * f itself.
@@ -526,6 +555,15 @@ __device__ __forceinline__ u128 times(u128 m, float f, bool &exact) {
     const u128 down = shift > 127 ? 0 : product >> shift;
     exact = shift <= 127 && down << shift == product;
     return down;
+}
+
+// A share of the largest weight, in units of 2^-62, from below.
+__device__ __forceinline__ u64 share62(float f) {
+    if (!(f > 0.f)) return 0ull;
+    if (f >= 1.f) return 1ull << 62;
+    const unsigned b = __float_as_uint(f), m = (b & 0x7fffffu) | 0x800000u;
+    const int up = (int)(b >> 23) - 88;  // f = m 2^(exponent - 150)
+    return up >= 0 ? (u64)m << up : up > -24 && b >> 23 ? (u64)(m >> -up) : 0ull;
 }
 
 // Adds the columns of a vector to the bins, which lie at `bins` in shared memory.
@@ -585,6 +623,15 @@ struct Counter {
     }
 };
 
+// How many of 8 columns count as the largest finite number: it or +inf (rare, and kept out of the way).
+__device__ __noinline__ int eight_largest(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n += (key_of(w[k] & 0xffffu) == kKeyMax) + (key_of(w[k] >> 16) == kKeyMax);
+    return n;
+}
+
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
     extern __shared__ __align__(16) char smem[];
     Shared &s = *(Shared *)smem;
@@ -594,10 +641,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     const uint16_t *row = p.logits + (long long)t * p.ld;
     asm volatile("griddepcontrol.launch_dependents;");
     fill_powers(s.pw);
-    if (tid == 0) s.told.low = 0, s.told.odd = 0, s.told.top = kPlaces;
+    if (tid == 0) s.told.low = 0, s.told.odd = 0;
     for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const float temperature = p.temperature ? p.temperature[t] : 1.f;
+    const bool greedy = !(temperature > 0.f);
+    const float min_p = p.min_p ? p.min_p[t] : 0.f, top_p = p.top_p ? p.top_p[t] : 1.f, u = p.uniform ? p.uniform[t] : 0.f;
+    const int top_k = p.top_k ? p.top_k[t] : 0;
 
     // counts of this CTA's part of the row
     const int part = ((p.V + C - 1) / C + 7) & ~7, begin = min(p.V, c * part), end = min(p.V, begin + part);
@@ -613,21 +665,42 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         s.bins[0] = s.bins[2 * kMags];
     }
     __syncthreads();
-    int top = kPlaces;
-    for (int i = tid * 4; i < kPlaces && top == kPlaces && i < *(volatile int *)&s.told.top; i += kThreads * 4) {
-        const uint4 v = four_places(i, [&](int bin) { return *(const uint4 *)&s.bins[bin]; });
-        if (v.x | v.y | v.z | v.w) top = i + (v.x ? 0 : v.y ? 1 : v.z ? 2 : 3);
-        if (top < kPlaces) atomicMin(&s.told.top, top);
+    const u64 least = greedy ? 0ull : share62(min_p);
+    Entries entries;
+    entries.window = -1;
+    entries.before = {0, 0};
+    if (C == 1) {
+        entries.list = s.bins;
+        entries.n = write_entries<kRounds>(s, s.bins, 0, kRounds, [&](int place) {
+            return four_places(place, [&](int bin) { return *(const uint4 *)&s.bins[bin]; });
+        });
+    } else {
+        // a slice's counts in the parts of all
+        cluster_sync(C);
+        const int rounds = kRounds / C;
+        entries.list = s.list;
+        entries.n = write_entries<kRounds / 2>(s, s.list, c * rounds * 4 * kThreads, rounds, [&](int place) {
+            return four_places(place, [&](int bin) {
+                uint4 sum = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kMostCtas; ++k)
+                    if (k < C) {
+                        const uint4 v = load_peer4(peer_address(&s.bins[bin], k));
+                        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                    }
+                return sum;
+            });
+        });
     }
-    const float temperature = p.temperature ? p.temperature[t] : 1.f;
-    const bool greedy = !(temperature > 0.f);
-    const float min_p = p.min_p ? p.min_p[t] : 0.f, top_p = p.top_p ? p.top_p[t] : 1.f, u = p.uniform ? p.uniform[t] : 0.f;
-    const int top_k = p.top_k ? p.top_k[t] : 0;
-    const u64 least = !(min_p > 0.f) ? 0ull : min_p >= 1.f ? 1ull << 62 : (u64)((double)min_p * 0x1p62);
+    if (tid == 0) {
+        s.told.entries = entries.n;
+        s.told.top = entries.n ? (int)(entries.list[0] >> 18) : kPlaces;
+        s.scale = begin_scale(greedy ? 1.f : temperature);
+    }
     hear(s, C);
     unsigned lowest = 0;
-    int odd = 0;
-    top = kPlaces;
+    int odd = 0, top = kPlaces;
+#pragma unroll 1
     for (int k = 0; k < C; ++k) {
         top = min(top, s.all[k].top);
         lowest = max(lowest, s.all[k].low);
@@ -636,12 +709,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     // The one window is enough if nothing lies outside of it but numbers too low to weigh anything.
     bool one = !odd && top < kPlaces;
     if (one) {
-        if (tid == 0) s.scale = make_scale(greedy ? 1.f : temperature, value_of(key_of_place(top, -1)));
+        if (tid == 0) end_scale(s.scale, value_of(key_of_place(top, -1)));
         __syncthreads();
         one = lowest == 0 || weight62(s.scale, value_of(lowest), s.pw) == 0;
     }
-    Sums total, heavy;
-    Entries entries;
+    Sums total, heavy = {0, 0};
     if (!one) {
         // the first CTA does the row alone
         cluster_sync(C);  // (and is no longer read by the others)
@@ -651,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         key = __reduce_max_sync(kAll, key);
         if (lane == 0) s.warp_n[warp] = (int)key;
         __syncthreads();
+#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) key = max(key, (unsigned)s.warp_n[w]);
         if (key == 0) {  // nothing to choose from
             if (tid == 0) {
@@ -659,32 +732,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             }
             return;
         }
-        if (tid == 0) s.scale = make_scale(greedy ? 1.f : temperature, value_of(key));
+        if (tid == 0) {
+            s.scale = begin_scale(greedy ? 1.f : temperature);
+            end_scale(s.scale, value_of(key));
+        }
         window_sums(s, row, p.V, least, total, heavy);
     } else {
-        entries.window = -1;
-        const int rounds = kRounds / C, first = c * rounds * 4 * kThreads;
-        if (C == 1) {
-            entries.list = s.bins;
-            entries.n = write_entries<kRounds>(s, s.bins, 0, kRounds, [&](int place) {
-                return four_places(place, [&](int bin) { return *(const uint4 *)&s.bins[bin]; });
-            });
-        } else {
-            // a slice's counts in the parts of all
-            entries.list = s.list;
-            entries.n = write_entries<kRounds / 2>(s, s.list, first, rounds, [&](int place) {
-                return four_places(place, [&](int bin) {
-                    uint4 sum = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int k = 0; k < kMostCtas; ++k)
-                        if (k < C) {
-                            const uint4 v = load_peer4(peer_address(&s.bins[bin], k));
-                            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-                        }
-                    return sum;
-                });
-            });
-        }
         add_up(s, entries, least, total);
         if (tid == 0) {
             s.told.hi = (u64)(total.mass >> 64);
@@ -692,63 +745,72 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             s.told.n = total.n;
         }
         hear(s, C);
-        total = heavy = {0, 0};
+        total = {0, 0};
+#pragma unroll 1
         for (int k = 0; k < C; ++k) {
             const Told &o = s.all[k];
-            if (k == c) {
-                entries.before.mass += total.mass;
-                entries.before.n += total.n;
-            }
-            if (o.least_n) heavy = {total.mass + join(o.least_hi, o.least_lo), total.n + o.least_n};
+            if (least && o.least_n) heavy = {total.mass + join(o.least_hi, o.least_lo), total.n + o.least_n};
             total.mass += join(o.hi, o.lo);
             total.n += o.n;
         }
     }
-    // What is kept is n columns that weigh `mass`: by top-k, by top-p, by min-p.  The fourth step is the draw.
-    int n = total.n;
-    u128 mass = total.mass;
-    if (greedy) {
-        n = 1;
-        mass = (u128)1 << 62;
-    }
-    const float draw = u < 1.f ? u : u >= 1.f ? 0x1.fffffep-1f : 0.f;
-#pragma unroll 1
-    for (int step = greedy ? 2 : 0; step < 3; ++step) {
-        u128 bound = ~(u128)0;  // the column at which sums exceed it
-        int most = n;           // ... or which is this one
-        if (step == 0) {
-            if (top_k < 1 || top_k >= n) continue;
-            most = top_k;
-        } else {
-            if (step == 1 && !(top_p < 1.f)) continue;
-            if (step == 2 && !greedy && least && heavy.n < n) {
-                most = heavy.n;
-                mass = heavy.mass;
-            }
-            bool exact;
-            bound = times(mass, step == 1 ? top_p : draw, exact);
-            // a share of the weight has to be reached: the next integer below exceeded
-            if (step == 1 && exact && bound) --bound;
+    // What is kept is n columns that weigh `mass`: by top-k, by top-p, by min-p.  The last step is the draw.
+    // With the one window the first warp of every CTA takes these steps for itself.
+    if (!one || warp == 0) {
+        int n = total.n;
+        u128 mass = total.mass;
+        if (greedy) {
+            n = 1;
+            mass = (u128)1 << 62;
         }
-        if (!one) window_of(s, row, p.V, bound, most, entries);
+        const float draw = u < 1.f ? u : u >= 1.f ? 0x1.fffffep-1f : 0.f;
         Found f;
-        if (look(s, entries, bound, most, f)) {
-            if (C == 1 || !one) s.found[step] = f;
-            else
-                for (int k = 0; k < C; ++k) {
-                    const uint32_t to = peer_address(&s.found[step], k);
-#pragma unroll
-                    for (int i = 0; i < (int)(sizeof(Found) / 4); ++i) store_peer(to + i * 4, ((const unsigned *)&f)[i]);
+#pragma unroll 1
+        for (int step = greedy ? 2 : 0; step < 3; ++step) {
+            u128 bound = ~(u128)0;  // the column at which sums exceed it
+            int most = n;           // ... or which is this one
+            if (step == 0) {
+                if (top_k < 1 || top_k >= n) continue;
+                most = top_k;
+            } else {
+                if (step == 1 && !(top_p < 1.f)) continue;
+                if (step == 2 && least && heavy.n < n) {
+                    most = heavy.n;
+                    mass = heavy.mass;
                 }
+                bool exact;
+                bound = times(mass, step == 1 ? top_p : draw, exact);
+                // a share of the weight has to be reached: the next integer below exceeded
+                if (step == 1 && exact && bound) --bound;
+            }
+            int peer = c;
+            if (!one) {
+                window_of(s, row, p.V, bound, most, entries);
+                __syncthreads();
+            } else {
+                Sums upto = {0, 0};
+#pragma unroll 1
+                for (int k = 0; k < C; ++k) {
+                    peer = k;
+                    entries.before = upto;
+                    entries.n = s.all[k].entries;
+                    upto.mass += join(s.all[k].hi, s.all[k].lo);
+                    upto.n += s.all[k].n;
+                    if (upto.mass > bound || upto.n >= most) break;
+                }
+            }
+            f = look(s, entries, peer, bound, most);
+            n = f.n;
+            mass = join(f.hi, f.lo);
+            if (!one) __syncthreads();
         }
-        cluster_sync(one ? C : 1);
-        n = s.found[step].n;
-        mass = join(s.found[step].hi, s.found[step].lo);
+        if (tid == 0) s.found = f;
     }
+    __syncthreads();
 
     // which column that is: number `rank` of those with the found key.  A warp's columns follow each other.
-    const unsigned key = s.found[2].key;
-    const int rank = s.found[2].rank;
+    const unsigned key = s.found.key;
+    const int rank = s.found.rank;
     const int from = one ? begin : 0, to = one ? end : p.V;
     const int chunk = ((to - from + kWarps - 1) / kWarps + 255) & ~255;
     const int w0 = min(to, from + warp * chunk), w1 = min(to, w0 + chunk);
@@ -764,11 +826,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             const uint32_t x = (w[k] ^ both) & signs;
             n += __popc(~(((x & 0x7fff7fffu) + 0x7fff7fffu) | x) & 0x80008000u);  // halves of 0
         }
-        if (largest) {
-            n = 0;
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) n += key_of(w[k >> 1] >> (k & 1) * 16 & 0xffffu) == key;
-        }
+        if (largest) n = eight_largest(v);
         return n;
     };
     int mine = 0;
@@ -781,14 +839,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     if (one && C > 1) {
         if (tid == 0) {
             int sum = 0;
+#pragma unroll 1
             for (int w = 0; w < kWarps; ++w) sum += s.warp_n[w];
             s.told.matches = sum;
         }
         hear(s, C);
+#pragma unroll 1
         for (int k = 0; k < c; ++k) ahead += s.all[k].matches;
         cluster_sync(C);  // nobody is read any more
     }
-    for (int w = 0; w < warp; ++w) ahead += s.warp_n[w];
+    ahead += (int)__reduce_add_sync(kAll, lane < warp ? (unsigned)s.warp_n[lane] : 0u);
     if (ahead > rank || rank >= ahead + mine) return;
     // the warp's columns again, 256 at a time, from L1 or L2
     int found_at = -1;
@@ -801,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             v = __ldg((const uint4 *)(row + at));
             here = matches(v);
         } else {
+#pragma unroll 1
             for (int k = 0; k < few; ++k) here += key_of(row[at + k]) == key;
         }
         const int all = (int)__reduce_add_sync(kAll, (unsigned)here);
@@ -816,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         }
         ahead += upto - here;  // ahead of this lane's columns
         if (ahead <= rank && rank < ahead + here)
+#pragma unroll 1
             for (int k = 0; k < few; ++k)
                 if (key_of(row[at + k]) == key && ahead++ == rank) found_at = at + k;
         break;
