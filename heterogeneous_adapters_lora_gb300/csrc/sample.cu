@@ -15,8 +15,10 @@
 //
 // Counting takes 13 instructions for two columns, all of them on both at once but the
 // addresses; columns outside of the counted range (masked ones, zeros) leave that path by eights.
-// A cluster of up to 8 CTAs shares a row: each counts its part, the counts are added up by slices
-// over distributed shared memory, and sums before a slice go around with a cluster barrier.
+// Where rows are few a cluster of up to 8 CTAs shares one: each counts its part, tells which groups of 128
+// values it has any of, and adds up all parts' counts of its share of those over distributed shared memory.
+// The rest, some 6 us, is a chain of dependent steps: weights and their running sums, then up to three
+// bounds, which the first warp of every CTA finds for itself (256 rows of 128256 columns 59 us, of which counting is 25).
 //
 // Keys are bf16 bits mapped to integers that grow with the value.  A window is a
 // range of keys that is counted at once:
@@ -28,6 +30,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "lora_internal.cuh"
 #include "mma_common.cuh"
@@ -43,7 +46,8 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMagLo = 72 * 128, kMags = 64 * 128;  // magnitudes [2^-55, 2^9) as bf16 bits
 constexpr int kBins = 2 * kMags + 1;                // by magnitude, the sign above it, 0 last
 constexpr int kPlaces = 2 * kMags;                  // of the order; +2^-55 has none
-constexpr int kRounds = kPlaces / kThreads / 4;     // of four places per thread
+constexpr int kGroups = kPlaces / 128;              // of places: four to a lane of a warp
+constexpr int kRounds = kGroups / kWarps;           // most of them to a warp
 constexpr int kMostCtas = 8;
 constexpr int kWinBins = 4096;
 constexpr int kWindows = 65536 / kWinBins;
@@ -178,7 +182,8 @@ struct Found {
 
 // What a CTA tells the others of its row.
 struct Told {
-    int top;       // first place that is not empty
+    int top;       // first place of its part that is not empty
+    uint8_t some[kWarps];  // groups of its part that are not empty, a bit each
     unsigned low;  // largest key below the one window
     int odd;       // a key in the gaps of the one window, or above it
     u64 lo, hi, least_lo, least_hi;  // weight of its slice, and of the beginning of at least min_p a column
@@ -191,10 +196,12 @@ struct Shared {
     alignas(16) unsigned bins[kBins + 7];             // by bits; or a window's in descending order
     unsigned list[kPlaces / 2];                       // a slice's entries, where two CTAs or more share the row
     u64 pw[192];
+    unsigned groups[kGroups / 32];         // that are not empty in any part, as bits
+    uint8_t group_at[kGroups];             // ... and in their order
     u64 warp_lo[kWarps], warp_hi[kWarps];  // 128-bit partial sums
     int warp_n[kWarps], last;
     u64 pre_lo[kThreads], pre_hi[kThreads];  // sums ahead of a thread's entries
-    int pre_n[kThreads];
+    unsigned pre_n[kThreads];
     Told told;
     Told all[kMostCtas];  // of every CTA
     Found found;
@@ -267,6 +274,16 @@ __device__ __forceinline__ void each_vector(const uint16_t *row, int begin, int 
 #pragma unroll 1
         for (int i = whole; i < end; ++i) g(i, (unsigned)row[i]);
 }
+// The vectors of columns that are kept in shared memory, and a last one that is not whole from the row itself.
+template <typename F, typename G>
+__device__ __forceinline__ void each_kept(const uint16_t *row, const uint4 *kept, int begin, int end, int at, int step, F f, G g) {
+    const int n = (end - begin) >> 3;
+#pragma unroll 2
+    for (int i = at; i < n; i += step) f(begin + i * 8, kept[i]);
+    if (at == 0)
+#pragma unroll 1
+        for (int i = begin + n * 8; i < end; ++i) g(i, (unsigned)row[i]);
+}
 // (where time matters less than the size of the code)
 template <typename G>
 __device__ __forceinline__ void each_column(const uint16_t *row, int end, G g) {
@@ -288,18 +305,17 @@ __device__ __forceinline__ int each_of(int n) { return (n + kThreads - 1) / kThr
 constexpr unsigned kColumns = (1u << 18) - 1;
 static_assert(LORA_MAX_VOCAB <= kColumns && kPlaces <= 1 << 14 && kWinBins <= 1 << 14, "an entry's parts");
 
-// Writes the entries of a slice of 4 * kThreads * rounds places from `first` on.  four(place): the columns of four
-// places in a row, in their order; a warp has rounds * 128 of them.  `list` may be where the counts are.
-template <int MAX, typename F>
-__device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int first, int rounds, F four) {
+// Writes the entries of the warps' groups, one warp's after the other's.  group(j): a warp's group number j, of
+// `rounds`; four(j): the columns of this lane's four places of it.  `list` may be where the counts are.
+template <int MAX, typename G, typename F>
+__device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int rounds, G group, F four) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    first += (warp * rounds * 32 + lane) * 4;
     uint4 c[MAX];
     unsigned some = 0;  // rounds in which the warp has any
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < MAX; ++j) {
-        c[j] = j < rounds ? four(first + j * 128) : make_uint4(0, 0, 0, 0);
+        c[j] = j < rounds ? four(j) : make_uint4(0, 0, 0, 0);
         const int here = (c[j].x != 0) + (c[j].y != 0) + (c[j].z != 0) + (c[j].w != 0);
         mine += here;
         if (__any_sync(kAll, here)) some |= 1u << j;
@@ -313,6 +329,7 @@ __device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int firs
     for (int j = 0; j < MAX; ++j) {
         if (!(some >> j & 1)) continue;
         const unsigned q[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+        const unsigned first = (unsigned)(group(j) * 128 + lane * 4);
         int to = at;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -322,20 +339,15 @@ __device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int firs
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (q[k]) list[to++] = (unsigned)(first + j * 128 + k) << 18 | q[k];
+            if (q[k]) list[to++] = (first + k) << 18 | q[k];
     }
     __syncthreads();
     return n;
 }
 
-// The columns of four places of the one window, added up over C CTAs' bins; places of 0 and up to it come in
-// descending order of the bins.
-template <typename L>
-__device__ __forceinline__ uint4 four_places(int place, L load) {
-    if (place >= kMags) return load(place);
-    const uint4 v = load(kMags - 4 - place);
-    return make_uint4(v.w, v.z, v.y, v.x);
-}
+// The columns of four places of the one window: of 0 and ahead of it they come in descending order of the bins.
+__device__ __forceinline__ int bin_of_places(int place) { return place < kMags ? kMags - 4 - place : place; }
+__device__ __forceinline__ uint4 in_order(int place, uint4 v) { return place < kMags ? make_uint4(v.w, v.z, v.y, v.x) : v; }
 
 // Sums of the entries in `total`, those ahead of each thread's in s.pre; of their beginning that weighs at
 // least `least` a column in s.told.
@@ -354,7 +366,7 @@ __device__ __forceinline__ void add_up(Shared &s, const Entries &q, u64 least, S
     const Sums before = scan(s, own, total);
     s.pre_hi[threadIdx.x] = (u64)(before.mass >> 64);
     s.pre_lo[threadIdx.x] = (u64)before.mass;
-    s.pre_n[threadIdx.x] = before.n;
+    s.pre_n[threadIdx.x] = (unsigned)before.n;
     if (!least) return;
     // the last thread that has some ends that beginning
     if (threadIdx.x == 0) s.last = -1, s.told.least_n = 0, s.told.least_hi = 0, s.told.least_lo = 0;
@@ -373,8 +385,9 @@ __device__ __forceinline__ void add_up(Shared &s, const Entries &q, u64 least, S
 
 // ------------------------------------------------------------ clusters
 
-__device__ __forceinline__ void cluster_sync(int C) {
-    if (C == 1) {
+template <bool SHARE>
+__device__ __forceinline__ void cluster_sync() {
+    if (!SHARE) {
         __syncthreads();
         return;
     }
@@ -401,27 +414,38 @@ __device__ __forceinline__ uint4 load_peer4(uint32_t a) {
     asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+// A number of a CTA of the row.
+template <bool SHARE>
+__device__ __forceinline__ unsigned peers(const unsigned *local, int peer) {
+    return SHARE ? load_peer(peer_address(local, peer)) : *(const volatile unsigned *)local;
+}
+template <bool SHARE>
+__device__ __forceinline__ u64 peers(const u64 *local, int peer) {
+    return SHARE ? load_peer8(peer_address(local, peer)) : *(const volatile u64 *)local;
+}
 // What every CTA of the row tells, in s.all.
+template <bool SHARE>
 __device__ __forceinline__ void hear(Shared &s, int C) {
-    cluster_sync(C);  // all have told
+    cluster_sync<SHARE>();  // all have told
     constexpr int kWords = sizeof(Told) / 4;
 #pragma unroll 1
     for (int i = threadIdx.x; i < C * kWords; i += kThreads)
-        ((unsigned *)s.all)[i] = load_peer(peer_address((unsigned *)&s.told + i % kWords, i / kWords));
+        ((unsigned *)s.all)[i] = peers<SHARE>((unsigned *)&s.told + i % kWords, i / kWords);
     __syncthreads();
 }
 
 // The first column of the order at which the sum of weights exceeds `mass`, or that is number `n`,
 // whichever comes first, if it is among the entries of CTA `peer` (q.n of them at q.list, behind q.before).
 // A warp's work: the thread that has it by two ballots over s.pre, then that thread's entries, one a lane.
+template <bool SHARE>
 __device__ __forceinline__ Found look(const Shared &s, const Entries &q, int peer, u128 mass, int n) {
     const int lane = threadIdx.x & 31, each = each_of(q.n);
     int who = lane < kWarps ? lane * 32 : 0, n0 = 0;
     u128 before = 0;
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {
-        before = q.before.mass + join(load_peer8(peer_address(&s.pre_hi[who], peer)), load_peer8(peer_address(&s.pre_lo[who], peer)));
-        n0 = q.before.n + (int)load_peer(peer_address(&s.pre_n[who], peer));
+        before = q.before.mass + join(peers<SHARE>(&s.pre_hi[who], peer), peers<SHARE>(&s.pre_lo[who], peer));
+        n0 = q.before.n + (int)peers<SHARE>(&s.pre_n[who], peer);
         const unsigned upto = __ballot_sync(kAll, before <= mass && n0 < n && (level || lane < kWarps));
         const int at = upto ? 31 - __clz(upto) : 0;  // (that of lane 0 always is)
         if (level) {
@@ -433,7 +457,7 @@ __device__ __forceinline__ Found look(const Shared &s, const Entries &q, int pee
         }
     }
     const int i = who * each + lane;
-    const unsigned entry = lane < each && i < q.n ? load_peer(peer_address(&q.list[i], peer)) : 0u;
+    const unsigned entry = lane < each && i < q.n ? peers<SHARE>(&q.list[i], peer) : 0u;
     const int c = (int)(entry & kColumns);
     const u64 w = c ? weight_of(s, entry, q.window) : 0ull;
     Sums sum = {(u128)w * (unsigned)c, c};
@@ -497,7 +521,9 @@ __device__ __noinline__ void window_entries(Shared &s, const uint16_t *row, int 
     constexpr int kPer = kWinBins / kThreads / 4;
     q.list = s.bins;
     q.window = window;
-    q.n = write_entries<kPer>(s, s.bins, 0, kPer, [&](int place) { return *(const uint4 *)&s.bins[place]; });
+    const int own = (int)(threadIdx.x >> 5) * kPer;
+    q.n = write_entries<kPer>(s, s.bins, kPer, [&](int j) { return own + j; },
+                              [&](int j) { return *(const uint4 *)&s.bins[(own + j) * 128 + (int)(threadIdx.x & 31) * 4]; });
     add_up(s, q, least, all);
 }
 
@@ -623,6 +649,12 @@ struct Counter {
     }
 };
 
+constexpr int kKept = (int)((sizeof(Shared) + 15) & ~(size_t)15);  // where a row's part is kept, behind the rest
+constexpr int kMostKept = 227 * 1024 - kKept;                      // bytes of it
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32_of(to)), "l"(from) : "memory");
+}
+
 // How many of 8 columns count as the largest finite number: it or +inf (rare, and kept out of the way).
 __device__ __noinline__ int eight_largest(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -632,16 +664,18 @@ __device__ __noinline__ int eight_largest(uint4 v) {
     return n;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
+// SHARE: CTAs share a row (p.C of them; otherwise one has it).  KEEP: a CTA keeps its part of the row in shared memory.
+template <bool SHARE, bool KEEP>
+__global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const SampleArgs p) {
     extern __shared__ __align__(16) char smem[];
     Shared &s = *(Shared *)smem;
-    const int C = p.C, c = C > 1 ? (int)bgmv::cluster_rank() : 0;
+    const int C = SHARE ? p.C : 1, c = SHARE ? (int)bgmv::cluster_rank() : 0;
     const int t = (int)blockIdx.x / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint16_t *row = p.logits + (long long)t * p.ld;
     asm volatile("griddepcontrol.launch_dependents;");
     fill_powers(s.pw);
-    if (tid == 0) s.told.low = 0, s.told.odd = 0;
+    if (tid == 0) s.told.low = 0, s.told.odd = 0, s.told.top = kPlaces;
     for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -655,7 +689,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     const int part = ((p.V + C - 1) / C + 7) & ~7, begin = min(p.V, c * part), end = min(p.V, begin + part);
     Counter counter;
     counter.bins = s.bins;
-    each_vector<2>(row, begin, end, tid, kThreads, [&](int, const uint4 &v) { counter.eight(v); }, [&](int, unsigned b) { counter.one(b); });
+    uint4 *const kept = (uint4 *)(smem + kKept);
+    if (KEEP) {
+        // a thread copies and counts the same vectors, in two halves
+        const int n = (end - begin) >> 3, half = n >> 1;
+#pragma unroll 1
+        for (int i = tid; i < half; i += kThreads) copy16(&kept[i], row + begin + i * 8);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll 1
+        for (int i = half + tid; i < n; i += kThreads) copy16(&kept[i], row + begin + i * 8);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            if (h) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else asm volatile("cp.async.wait_group 1;" ::: "memory");
+            const int to = h ? n : half;
+#pragma unroll 2
+            for (int i = (h ? half : 0) + tid; i < to; i += kThreads) counter.eight(kept[i]);
+        }
+        if (tid == 0)
+#pragma unroll 1
+            for (int i = begin + n * 8; i < end; ++i) counter.one((unsigned)row[i]);
+    } else {
+        each_vector<2>(row, begin, end, tid, kThreads, [&](int, const uint4 &v) { counter.eight(v); }, [&](int, unsigned b) { counter.one(b); });
+    }
     const unsigned low = __reduce_max_sync(kAll, counter.low);
     if (lane == 0 && low) atomicMax(&s.told.low, low);
     if (__any_sync(kAll, counter.odd) && lane == 0) s.told.odd = 1;
@@ -666,21 +723,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     }
     __syncthreads();
     const u64 least = greedy ? 0ull : share62(min_p);
+    if (tid == 0) s.scale = begin_scale(greedy ? 1.f : temperature);
+    unsigned lowest = s.told.low;
+    int odd = s.told.odd, top = kPlaces;
+    int n_groups = kGroups;
+    if (SHARE) {
+        // Most groups of places are empty: those that are not are found, and shared out.
+        unsigned some = 0;
+#pragma unroll 4
+        for (int j = 0; j < kRounds; ++j) {
+            const int place = (warp * kRounds + j) * 128 + lane * 4;
+            const uint4 v = in_order(place, *(const uint4 *)&s.bins[bin_of_places(place)]);
+            const unsigned lanes = __ballot_sync(kAll, (v.x | v.y | v.z | v.w) != 0);
+            if (lanes && !some && lane == __ffs(lanes) - 1) atomicMin(&s.told.top, place + (v.x ? 0 : v.y ? 1 : v.z ? 2 : 3));
+            some |= (lanes ? 1u : 0u) << j;
+        }
+        if (lane == 0) s.told.some[warp] = (uint8_t)some;
+        hear<SHARE>(s, C);
+        bool mine = false;  // group `tid` has any
+#pragma unroll 1
+        for (int k = 0; k < C; ++k) {
+            const Told &o = s.all[k];
+            top = min(top, o.top);
+            lowest = max(lowest, o.low);
+            odd |= o.odd;
+            if (tid < kGroups) mine |= o.some[tid / kRounds] >> tid % kRounds & 1;
+        }
+        if (warp < kGroups / 32) {
+            const unsigned bits = __ballot_sync(kAll, mine);
+            if (lane == 0) s.groups[warp] = bits;
+        }
+        __syncthreads();
+        n_groups = 0;
+        int ahead = 0;
+#pragma unroll
+        for (int k = 0; k < kGroups / 32; ++k) {
+            if (k < warp) ahead += __popc(s.groups[k]);
+            if (k == warp) ahead += __popc(s.groups[k] & ((1u << lane) - 1));
+            n_groups += __popc(s.groups[k]);
+        }
+        if (mine) s.group_at[ahead] = (uint8_t)tid;
+        __syncthreads();
+    }
     Entries entries;
-    entries.window = -1;
-    entries.before = {0, 0};
-    if (C == 1) {
-        entries.list = s.bins;
-        entries.n = write_entries<kRounds>(s, s.bins, 0, kRounds, [&](int place) {
-            return four_places(place, [&](int bin) { return *(const uint4 *)&s.bins[bin]; });
-        });
-    } else {
-        // a slice's counts in the parts of all
-        cluster_sync(C);
-        const int rounds = kRounds / C;
-        entries.list = s.list;
-        entries.n = write_entries<kRounds / 2>(s, s.list, c * rounds * 4 * kThreads, rounds, [&](int place) {
-            return four_places(place, [&](int bin) {
+    {
+        const int g0 = c * n_groups / C, few = (c + 1) * n_groups / C - g0;
+        const int w0 = few * warp / kWarps, rounds = few * (warp + 1) / kWarps - w0;
+        unsigned *const list = SHARE ? s.list : s.bins;
+        const auto group = [&](int j) { return SHARE ? (int)s.group_at[g0 + w0 + j] : w0 + j; };
+        if (SHARE) {
+            // the counts of all parts
+#pragma unroll 1
+            for (int j = 0; j < rounds; ++j) {
+                const int place = group(j) * 128 + lane * 4, bin = bin_of_places(place);
                 uint4 sum = make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int k = 0; k < kMostCtas; ++k)
@@ -688,35 +783,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                         const uint4 v = load_peer4(peer_address(&s.bins[bin], k));
                         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
                     }
-                return sum;
-            });
+                *(uint4 *)&list[(w0 + j) * 128 + lane * 4] = in_order(place, sum);
+            }
+        }
+        entries.list = list;
+        entries.window = -1;
+        entries.before = {0, 0};
+        entries.n = write_entries<kRounds>(s, list, rounds, group, [&](int j) {
+            const int place = group(j) * 128 + lane * 4;
+            return SHARE ? *(const uint4 *)&list[(w0 + j) * 128 + lane * 4] : in_order(place, *(const uint4 *)&list[bin_of_places(place)]);
         });
+        if (!SHARE && entries.n) top = (int)(list[0] >> 18);
     }
-    if (tid == 0) {
-        s.told.entries = entries.n;
-        s.told.top = entries.n ? (int)(entries.list[0] >> 18) : kPlaces;
-        s.scale = begin_scale(greedy ? 1.f : temperature);
-    }
-    hear(s, C);
-    unsigned lowest = 0;
-    int odd = 0, top = kPlaces;
-#pragma unroll 1
-    for (int k = 0; k < C; ++k) {
-        top = min(top, s.all[k].top);
-        lowest = max(lowest, s.all[k].low);
-        odd |= s.all[k].odd;
-    }
+    if (tid == 0 && top < kPlaces) end_scale(s.scale, value_of(key_of_place(top, -1)));
+    __syncthreads();
     // The one window is enough if nothing lies outside of it but numbers too low to weigh anything.
     bool one = !odd && top < kPlaces;
-    if (one) {
-        if (tid == 0) end_scale(s.scale, value_of(key_of_place(top, -1)));
-        __syncthreads();
-        one = lowest == 0 || weight62(s.scale, value_of(lowest), s.pw) == 0;
-    }
+    if (one) one = lowest == 0 || weight62(s.scale, value_of(lowest), s.pw) == 0;
     Sums total, heavy = {0, 0};
     if (!one) {
         // the first CTA does the row alone
-        cluster_sync(C);  // (and is no longer read by the others)
+        cluster_sync<SHARE>();  // (and is no longer read by the others)
         if (c) return;
         unsigned key = 0;
         each_column(row, p.V, [&](unsigned b) { key = max(key, key_of(b)); });
@@ -743,8 +830,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             s.told.hi = (u64)(total.mass >> 64);
             s.told.lo = (u64)total.mass;
             s.told.n = total.n;
+            s.told.entries = entries.n;
         }
-        hear(s, C);
+        hear<SHARE>(s, C);
         total = {0, 0};
 #pragma unroll 1
         for (int k = 0; k < C; ++k) {
@@ -799,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
                     if (upto.mass > bound || upto.n >= most) break;
                 }
             }
-            f = look(s, entries, peer, bound, most);
+            f = look<SHARE>(s, entries, peer, bound, most);
             n = f.n;
             mass = join(f.hi, f.lo);
             if (!one) __syncthreads();
@@ -829,54 +917,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         if (largest) n = eight_largest(v);
         return n;
     };
-    int mine = 0;
-    each_vector<4>(row, w0, w1, lane, 32, [&](int, const uint4 &v) { mine += matches(v); }, [&](int, unsigned b) { mine += key_of(b) == key; });
-    mine = (int)__reduce_add_sync(kAll, (unsigned)mine);
+    int found = 0;
+    const bool here = KEEP && one;
+    if (here)
+        each_kept(row, kept + ((w0 - begin) >> 3), w0, w1, lane, 32, [&](int, const uint4 &v) { found += matches(v); },
+                  [&](int, unsigned b) { found += key_of(b) == key; });
+    else
+        each_vector<4>(row, w0, w1, lane, 32, [&](int, const uint4 &v) { found += matches(v); }, [&](int, unsigned b) { found += key_of(b) == key; });
+    found = (int)__reduce_add_sync(kAll, (unsigned)found);
     __syncthreads();
-    if (lane == 0) s.warp_n[warp] = mine;
+    if (lane == 0) s.warp_n[warp] = found;
     __syncthreads();
     int ahead = 0;
-    if (one && C > 1) {
+    if (SHARE && one) {
         if (tid == 0) {
             int sum = 0;
 #pragma unroll 1
             for (int w = 0; w < kWarps; ++w) sum += s.warp_n[w];
             s.told.matches = sum;
         }
-        hear(s, C);
+        hear<SHARE>(s, C);
 #pragma unroll 1
         for (int k = 0; k < c; ++k) ahead += s.all[k].matches;
-        cluster_sync(C);  // nobody is read any more
+        cluster_sync<SHARE>();  // nobody is read any more
     }
     ahead += (int)__reduce_add_sync(kAll, lane < warp ? (unsigned)s.warp_n[lane] : 0u);
-    if (ahead > rank || rank >= ahead + mine) return;
+    if (ahead > rank || rank >= ahead + found) return;
     // the warp's columns again, 256 at a time, from L1 or L2
     int found_at = -1;
 #pragma unroll 1
     for (int i = w0; i < w1; i += 256) {
         const int at = i + lane * 8, few = min(8, w1 - at);
         uint4 v = make_uint4(0, 0, 0, 0);
-        int here = 0;
+        int n = 0;
         if (few == 8) {
-            v = __ldg((const uint4 *)(row + at));
-            here = matches(v);
+            v = here ? kept[(at - begin) >> 3] : __ldg((const uint4 *)(row + at));
+            n = matches(v);
         } else {
 #pragma unroll 1
-            for (int k = 0; k < few; ++k) here += key_of(row[at + k]) == key;
+            for (int k = 0; k < few; ++k) n += key_of(row[at + k]) == key;
         }
-        const int all = (int)__reduce_add_sync(kAll, (unsigned)here);
+        const int all = (int)__reduce_add_sync(kAll, (unsigned)n);
         if (rank >= ahead + all) {
             ahead += all;
             continue;
         }
-        int upto = here;
+        int upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int k = __shfl_up_sync(kAll, upto, o);
             if (lane >= o) upto += k;
         }
-        ahead += upto - here;  // ahead of this lane's columns
-        if (ahead <= rank && rank < ahead + here)
+        ahead += upto - n;  // ahead of this lane's columns
+        if (ahead <= rank && rank < ahead + n)
 #pragma unroll 1
             for (int k = 0; k < few; ++k)
                 if (key_of(row[at + k]) == key && ahead++ == rank) found_at = at + k;
@@ -895,8 +988,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 }
 
 // CTAs that share a row: as many as all find room at once, two to an SM, of 12000 columns at least; a short
-// row is not shared, as the cluster's barriers and what goes around take 5 us (one row of 4000
-// columns 15.7 us by one CTA, 21.1 by two; of 32007 21.6, 23.1 and by eight 21.7; of 128256 38.5, 31.4 and 22.9).
+// row is not shared, as the cluster's barriers and what goes around take 3 us (one row, by 1, 2, 4 and 8 CTAs:
+// of 4000 columns 10.0, 13.2, 13.4 and 13.9 us, of 32007 15.3, 16.4, 15.8 and 15.7, of 128256 27.9, 23.3, 17.6 and 15.9).
 int ctas_of_a_row(int T, int V, int sms) {
     int C = 1;
     if (V < 40000) return C;
@@ -904,18 +997,67 @@ int ctas_of_a_row(int T, int V, int sms) {
     return C;
 }
 
-std::atomic<int> g_sample_sms[64];  // SM count per device, looked up once (the kernel's attribute is set on the way)
-cudaError_t device_sms(int &sms) {
+// A row's part in shared memory: one CTA to an SM, so only where all rows find room at once.  It is read
+// once, and more of it at a time (64 rows of 32007 columns 19.2 -> 16.3 us, one 18.0 -> 16.8, with all filters).
+// Half as many CTAs to a row that have that room are faster than all without it (18 rows of 128256 columns by four
+// 18.5 us, by eight 22.4; 64 of 100000 by two 21.6, by four 25.9).
+struct Device {
+    std::atomic<int> sms;  // 0: not looked up yet
+    int rooms[4];          // clusters of 1, 2, 4 and 8 such CTAs that run at once
+};
+Device g_devices[64];
+
+size_t part_of(int V, int C) { return (size_t)((lora_ceil_div(V, C) + 7) & ~7); }
+bool kept(const Device &d, int T, int V, int C) {
+    return part_of(V, C) * 2 <= (size_t)kMostKept && T <= d.rooms[C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3];
+}
+
+void configure(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int T, int C, size_t smem, cudaStream_t stream) {
+    memset(&cfg, 0, sizeof(cfg));
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)C;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    cfg.gridDim = dim3((unsigned)T * (unsigned)C, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+}
+
+template <bool SHARE, bool KEEP>
+cudaError_t set_smem() {
+    return cudaFuncSetAttribute(sample_kernel<SHARE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? kKept + kMostKept : (int)sizeof(Shared));
+}
+
+// What the current device has; looked up once (the kernels' attributes are set on the way).
+cudaError_t device_of(Device *&d) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    sms = g_sample_sms[dev].load(std::memory_order_acquire);
-    if (sms) return cudaSuccess;
+    d = &g_devices[dev];
+    if (d->sms.load(std::memory_order_acquire)) return cudaSuccess;
+    int sms = 0, rooms[4];
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-    if (e == cudaSuccess) g_sample_sms[dev].store(sms, std::memory_order_release);
-    return e;
+    if ((e = set_smem<false, false>()) != cudaSuccess || (e = set_smem<false, true>()) != cudaSuccess ||
+        (e = set_smem<true, false>()) != cudaSuccess || (e = set_smem<true, true>()) != cudaSuccess)
+        return e;
+    rooms[0] = sms;
+    for (int i = 1; i < 4; ++i) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute at[2];
+        configure(cfg, at, 1, 1 << i, kKept + kMostKept, nullptr);
+        if ((e = cudaOccupancyMaxActiveClusters(&rooms[i], sample_kernel<true, true>, &cfg)) != cudaSuccess) return e;
+    }
+    static std::mutex lock;
+    std::lock_guard<std::mutex> hold(lock);
+    if (d->sms.load(std::memory_order_relaxed)) return cudaSuccess;
+    for (int i = 0; i < 4; ++i) d->rooms[i] = rooms[i];
+    d->sms.store(sms, std::memory_order_release);
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -933,14 +1075,14 @@ extern "C" lora_status_t lora_sample(const void *logits, int64_t ld, int32_t T, 
         (((uintptr_t)temperature | (uintptr_t)top_k | (uintptr_t)top_p | (uintptr_t)min_p | (uintptr_t)uniform |
           (uintptr_t)tokens | (uintptr_t)logprobs) & 3))
         return LORA_ERR_INVALID_ARG;
-    int sms = 0;
-    LORA_CUDA_TRY(device_sms(sms));
+    Device *dev = nullptr;
+    LORA_CUDA_TRY(device_of(dev));
     SampleArgs p;
     p.logits = (const uint16_t *)logits;
     p.ld = ld;
     p.T = T;
     p.V = vocab_size;
-    p.C = ctas_of_a_row(T, vocab_size, sms);
+    p.C = ctas_of_a_row(T, vocab_size, dev->sms);
     p.temperature = temperature;
     p.top_k = top_k;
     p.top_p = top_p;
@@ -948,21 +1090,15 @@ extern "C" lora_status_t lora_sample(const void *logits, int64_t ld, int32_t T, 
     p.uniform = uniform;
     p.tokens = tokens;
     p.logprobs = logprobs;
+    if (!kept(*dev, T, vocab_size, p.C) && p.C > 1 && kept(*dev, T, vocab_size, p.C / 2)) p.C /= 2;
+    const bool keep = kept(*dev, T, vocab_size, p.C);
     cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)p.C;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = p.C > 1 ? 2 : 1;
-    cfg.gridDim = dim3((unsigned)T * (unsigned)p.C, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(Shared);
-    cfg.stream = (cudaStream_t)stream;
-    LORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, sample_kernel, p));
+    configure(cfg, at, T, p.C, keep ? (size_t)kKept + part_of(vocab_size, p.C) * 2 : sizeof(Shared), (cudaStream_t)stream);
+    if (p.C > 1)
+        LORA_CUDA_TRY(keep ? cudaLaunchKernelEx(&cfg, sample_kernel<true, true>, p) : cudaLaunchKernelEx(&cfg, sample_kernel<true, false>, p));
+    else
+        LORA_CUDA_TRY(keep ? cudaLaunchKernelEx(&cfg, sample_kernel<false, true>, p) : cudaLaunchKernelEx(&cfg, sample_kernel<false, false>, p));
     lora_note_launch();
     return LORA_OK;
 }

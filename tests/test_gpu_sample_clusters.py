@@ -64,3 +64,12 @@ def test_equals_end_where_a_part_ends(V):
     check(x, top_k=k, uniform=[1 - 2.0 ** -24] * 16)
     check(x, top_k=k, uniform=[0.5] * 16)
     check(x, top_p=[1.0, 0.5, 0.25, 0.125] * 4, uniform=[1 - 2.0 ** -24] * 16)
+
+
+@pytest.mark.parametrize("T,V", [(1, 39999), (152, 39990), (153, 39990), (15, 128256), (16, 128256), (17, 128256), (20, 257024), (38, 128000), (39, 120000),
+                                 (76, 100003), (76, 116001), (77, 90000)])
+def test_rows_in_shared_memory_or_not(T, V):
+    """Sizes at and beside the ones from which a CTA no longer keeps its part of the row."""
+    x = rows(T, V, T)
+    x[:, 5::7] = -math.inf
+    check(x, [1.0] * T, [0, 20] * (T // 2) + [3] * (T % 2), None, None, uniform(T, V))
