@@ -247,7 +247,9 @@ struct Shape {
 
 constexpr int kBatchCols = 8;                // columns that the epilogue takes at a time
 constexpr int kDPitch = kRows + 4;           // of the adapters' part of a column: no two of a product's lanes on one bank
-constexpr int kVFloats = 8192;
+constexpr int kLotCols = 32;                 // ... whose adapters' part is there at once
+constexpr int kVFloats = 4096;
+static_assert(kVFloats / (2 * LORA_MAX_RANK) >= kBatchCols, "v of eight pairs");
 constexpr int kHPitch = kTile + 32;          // of a column of h: no two of 8 lanes' 16 bytes on one bank
 
 template <bool DOWN, bool ADAPT>
@@ -270,13 +272,13 @@ struct SharedOf {
             uint32_t key[kMaxP];                                       // slot << 12 | pair, by expert
         } g;  // while groups are found
         struct {
-            float delta[kBatchCols][kDPitch];  // the adapters' part of eight columns
+            float delta[ADAPT ? kLotCols : 1][kDPitch];  // the adapters' part of a lot of columns
             float v[ADAPT ? kVFloats : 1];     // scale A x or scale A2 h of some pairs
             alignas(16) uint16_t h[ADAPT && !DOWN ? 2 : 1][ADAPT && !DOWN ? kGroup : 1][kHPitch];  // hi and lo of the unit's columns of h
         } e;  // epilogue
     } u;
 };
-static_assert(sizeof(float[kBatchCols][kDPitch]) % 16 == 0 && kHPitch % 8 == 0, "read 16 bytes at a time");
+static_assert(sizeof(float[kDPitch]) % 16 == 0 && kHPitch % 8 == 0, "read 16 bytes at a time");
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -635,7 +637,7 @@ struct Epilogue {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s.u.e.delta[t4 * 2 + (k & 1)][warp * 32 + j * 16 + g + (k >> 1) * 8] = d[j][k];
+            for (int k = 0; k < 4; ++k) s.u.e.delta[b0 % kLotCols + t4 * 2 + (k & 1)][warp * 32 + j * 16 + g + (k >> 1) * 8] = d[j][k];
     }
 
     // 16 ranks of an adapter's A2, this unit's columns of them: what a warp multiplies with h at a time (up).
@@ -886,31 +888,38 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             const typename Shared::Pairs &of = s.of[now];
             bool any_delta = false, ok = true;
             int from = c;
+            unsigned with = 0;  // batches of the lot that have an adapter's part
 #pragma unroll 1
             for (int b0 = 0; b0 < x.n; b0 += kBatchCols) {
-                const bool end = b0 + kBatchCols >= x.n;
-                bool delta = false;
-                if (ADAPT) {
+                if (ADAPT && b0 % kLotCols == 0) {
+                    // the adapters' part of a lot of columns, before their products are there
                     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
                     waited = true;
-                    delta = last && epi.runs(of, b0);
-                    any_delta |= delta;
-                    if (delta) {
-                        const int lot = (u / q.MT) * kGroup + b0 / epi.lot;
-                        if (lot != filled) {
-                            epi.fill(x, of, b0 / epi.lot * epi.lot);
-                            bar_sync(1, kEpiThreads);
+                    const int to = min(x.n, b0 + kLotCols);
+                    with = 0;
+                    if (last)
+#pragma unroll 1
+                        for (int b = b0; b < to; b += kBatchCols) {
+                            if (!epi.runs(of, b)) continue;
+                            with |= 1u << (b - b0) / kBatchCols;
+                            const int lot = (u / q.MT) * kGroup + b / epi.lot;
+                            if (lot != filled) {
+                                if (b > 0) bar_sync(1, kEpiThreads);  // v is no longer read
+                                epi.fill(x, of, b / epi.lot * epi.lot);
+                                bar_sync(1, kEpiThreads);
+                            }
+                            filled = lot;
+                            epi.rows(rows, asked, x, of, b);
+                            asked = false;
                         }
-                        filled = lot;
-                        epi.rows(rows, asked, x, of, b0);
-                        asked = false;
-                    }
+                    any_delta |= with != 0;
                     bar_sync(1, kEpiThreads);
                     if (b0 == 0 && more) epi.prefetch(y, s.of[next]);
                     // rows of B of the columns after these, and rows of A2, are on their way while these are worked on
+                    const bool end = to == x.n;
                     const Part &z = end ? y : x;
                     const typename Shared::Pairs &oz = end ? s.of[next] : of;
-                    const int bz = end ? 0 : b0 + kBatchCols;
+                    const int bz = end ? 0 : to;
                     if (end ? more : last) {
                         rows.left = epi.runs(oz, bz);
                         rows.r = 0;
@@ -924,6 +933,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                         epi.next_task(task, x, of);
                     }
                 }
+                const bool delta = with >> b0 % kLotCols / kBatchCols & 1;
                 const int col = b0 + half * 4;
                 if (b0 == 0 && last && x.k0 > 0) {
                     // Sums that other CTAs have left of this unit, while its products are still to come.
@@ -989,8 +999,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                         for (int j = 0; j < 4; ++j) {
                             if (col + j >= x.n) break;
                             if (delta) {
-                                g[j] += s.u.e.delta[half * 4 + j][row];
-                                v[j] += s.u.e.delta[half * 4 + j][kTile + row];
+                                g[j] += s.u.e.delta[col % kLotCols + j][row];
+                                v[j] += s.u.e.delta[col % kLotCols + j][kTile + row];
                             }
                             if (DOWN) {
                                 float *y = p.y + (long long)s.list[x.at + col + j] * p.D + at;
@@ -1012,7 +1022,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                         }
                     }
                 }
-                if (ADAPT && last) bar_sync(1, kEpiThreads);  // delta is no longer read; at the end, all of h is there
+                // the lot's delta is no longer read; at the end, all of h is there
+                if (ADAPT && last && ((b0 + kBatchCols) % kLotCols == 0 || b0 + kBatchCols >= x.n)) bar_sync(1, kEpiThreads);
             }
             if (!ok) {
                 if (!last) asm volatile("bar.arrive 3, %0;" ::"r"(kEpiThreads + 32) : "memory");
