@@ -97,6 +97,7 @@ __device__ __forceinline__ u64 mul63(u64 a, u64 b) { return __umul64hi(a, b) << 
 
 // The factors 2^(-i / 64), 2^(-i / 4096) and 2^(-i / 2^18), i < 64, of weight62.
 __device__ __forceinline__ void fill_powers(u64 *pw) {
+#pragma unroll 1
     for (int i = threadIdx.x; i < 192; i += kThreads) {
         u64 v = kOne63;
 #pragma unroll
@@ -194,14 +195,11 @@ struct Told {
 
 struct Shared {
     alignas(16) unsigned bins[kBins + 7];             // by bits; or a window's in descending order
-    unsigned list[kPlaces / 2];                       // a slice's entries, where two CTAs or more share the row
     u64 pw[192];
     unsigned groups[kGroups / 32];         // that are not empty in any part, as bits
     uint8_t group_at[kGroups];             // ... and in their order
     u64 warp_lo[kWarps], warp_hi[kWarps];  // 128-bit partial sums
     int warp_n[kWarps], last;
-    u64 pre_lo[kThreads], pre_hi[kThreads];  // sums ahead of a thread's entries
-    unsigned pre_n[kThreads];
     Told told;
     Told all[kMostCtas];  // of every CTA
     Found found;
@@ -211,6 +209,19 @@ struct Shared {
     u64 win_lo[kWindows], win_hi[kWindows];
     int win_n[kWindows];
 };
+
+// Sums ahead of a thread's entries.
+struct Pre {
+    u64 lo[kThreads], hi[kThreads];
+    unsigned n[kThreads];
+};
+
+// Behind the rest of shared memory: the entries of a CTA's share, where several have the row (one has them where the
+// counts were), and Pre.  Of two CTAs Pre lies where the counts were, so that half of a long row can be kept.
+constexpr size_t kExtra = (sizeof(Shared) + 15) & ~(size_t)15;
+__host__ __device__ constexpr size_t list_bytes(int C) { return C == 1 ? 0 : (size_t)kPlaces / C * 4; }
+__host__ __device__ constexpr size_t extra_bytes(int C) { return list_bytes(C) + (C == 2 ? 0 : sizeof(Pre)); }
+static_assert(sizeof(Pre) <= sizeof(unsigned[kPlaces / 2]) && kWinBins <= kPlaces / 2, "Pre in the second half of the counts");
 
 __device__ __forceinline__ u128 join(u64 hi, u64 lo) { return ((u128)hi << 64) | lo; }
 
@@ -261,6 +272,7 @@ __device__ __forceinline__ Sums scan(Shared &s, Sums mine, Sums &total) {
 template <int kAhead, typename F, typename G>
 __device__ __forceinline__ void each_vector(const uint16_t *row, int begin, int end, int at, int step, F f, G g) {
     const int whole = begin + ((end - begin) & ~7);
+#pragma unroll 1
     for (int i = begin + at * 8; i < whole; i += kAhead * step * 8) {
         uint4 v[kAhead];
 #pragma unroll
@@ -349,9 +361,15 @@ __device__ __forceinline__ int write_entries(Shared &s, unsigned *list, int roun
 __device__ __forceinline__ int bin_of_places(int place) { return place < kMags ? kMags - 4 - place : place; }
 __device__ __forceinline__ uint4 in_order(int place, uint4 v) { return place < kMags ? make_uint4(v.w, v.z, v.y, v.x) : v; }
 
-// Sums of the entries in `total`, those ahead of each thread's in s.pre; of their beginning that weighs at
+__device__ __forceinline__ void put(Pre &pre, const Sums &before) {
+    pre.hi[threadIdx.x] = (u64)(before.mass >> 64);
+    pre.lo[threadIdx.x] = (u64)before.mass;
+    pre.n[threadIdx.x] = (unsigned)before.n;
+}
+
+// Sums of the entries in `total`; returns those ahead of this thread's.  Of their beginning that weighs at
 // least `least` a column in s.told.
-__device__ __forceinline__ void add_up(Shared &s, const Entries &q, u64 least, Sums &total) {
+__device__ __forceinline__ Sums add_up(Shared &s, const Entries &q, u64 least, Sums &total) {
     Sums much = {0, 0}, own = {0, 0};
     const int each = each_of(q.n), begin = min(q.n, (int)threadIdx.x * each), end = min(q.n, begin + each);
 #pragma unroll 1
@@ -364,10 +382,7 @@ __device__ __forceinline__ void add_up(Shared &s, const Entries &q, u64 least, S
         if (w >= least) much = own;
     }
     const Sums before = scan(s, own, total);
-    s.pre_hi[threadIdx.x] = (u64)(before.mass >> 64);
-    s.pre_lo[threadIdx.x] = (u64)before.mass;
-    s.pre_n[threadIdx.x] = (unsigned)before.n;
-    if (!least) return;
+    if (!least) return before;
     // the last thread that has some ends that beginning
     if (threadIdx.x == 0) s.last = -1, s.told.least_n = 0, s.told.least_hi = 0, s.told.least_lo = 0;
     __syncthreads();
@@ -381,6 +396,7 @@ __device__ __forceinline__ void add_up(Shared &s, const Entries &q, u64 least, S
         s.told.least_lo = (u64)much.mass;
         s.told.least_n = much.n;
     }
+    return before;
 }
 
 // ------------------------------------------------------------ clusters
@@ -436,16 +452,16 @@ __device__ __forceinline__ void hear(Shared &s, int C) {
 
 // The first column of the order at which the sum of weights exceeds `mass`, or that is number `n`,
 // whichever comes first, if it is among the entries of CTA `peer` (q.n of them at q.list, behind q.before).
-// A warp's work: the thread that has it by two ballots over s.pre, then that thread's entries, one a lane.
+// A warp's work: the thread that has it by two ballots over `pre`, then that thread's entries, one a lane.
 template <bool SHARE>
-__device__ __forceinline__ Found look(const Shared &s, const Entries &q, int peer, u128 mass, int n) {
+__device__ __forceinline__ Found look(const Shared &s, const Pre &pre, const Entries &q, int peer, u128 mass, int n) {
     const int lane = threadIdx.x & 31, each = each_of(q.n);
     int who = lane < kWarps ? lane * 32 : 0, n0 = 0;
     u128 before = 0;
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {
-        before = q.before.mass + join(peers<SHARE>(&s.pre_hi[who], peer), peers<SHARE>(&s.pre_lo[who], peer));
-        n0 = q.before.n + (int)peers<SHARE>(&s.pre_n[who], peer);
+        before = q.before.mass + join(peers<SHARE>(&pre.hi[who], peer), peers<SHARE>(&pre.lo[who], peer));
+        n0 = q.before.n + (int)peers<SHARE>(&pre.n[who], peer);
         const unsigned upto = __ballot_sync(kAll, before <= mass && n0 < n && (level || lane < kWarps));
         const int at = upto ? 31 - __clz(upto) : 0;  // (that of lane 0 always is)
         if (level) {
@@ -507,6 +523,7 @@ __device__ __forceinline__ Found look(const Shared &s, const Entries &q, int pee
 
 __device__ __noinline__ void count_window(Shared &s, const uint16_t *row, int V, int window) {
     __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < kWinBins; i += kThreads) s.bins[i] = 0;
     __syncthreads();
     each_column(row, V, [&](unsigned b) {
@@ -516,7 +533,7 @@ __device__ __noinline__ void count_window(Shared &s, const uint16_t *row, int V,
     __syncthreads();
 }
 
-__device__ __noinline__ void window_entries(Shared &s, const uint16_t *row, int V, int window, u64 least, Entries &q, Sums &all) {
+__device__ __noinline__ void window_entries(Shared &s, Pre &pre, const uint16_t *row, int V, int window, u64 least, Entries &q, Sums &all) {
     count_window(s, row, V, window);
     constexpr int kPer = kWinBins / kThreads / 4;
     q.list = s.bins;
@@ -524,10 +541,10 @@ __device__ __noinline__ void window_entries(Shared &s, const uint16_t *row, int 
     const int own = (int)(threadIdx.x >> 5) * kPer;
     q.n = write_entries<kPer>(s, s.bins, kPer, [&](int j) { return own + j; },
                               [&](int j) { return *(const uint4 *)&s.bins[(own + j) * 128 + (int)(threadIdx.x & 31) * 4]; });
-    add_up(s, q, least, all);
+    put(pre, add_up(s, q, least, all));
 }
 
-__device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, u64 least, Sums &total, Sums &heavy) {
+__device__ __noinline__ void window_sums(Shared &s, Pre &pre, const uint16_t *row, int V, u64 least, Sums &total, Sums &heavy) {
     if (threadIdx.x < kWindows) s.coarse[threadIdx.x] = 0;
     __syncthreads();
     each_column(row, V, [&](unsigned b) {
@@ -536,11 +553,12 @@ __device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, 
     });
     __syncthreads();
     total = heavy = {0, 0};
+#pragma unroll 1
     for (int w = kWindows - 1; w >= 0; --w) {
         Sums all = {0, 0};
         if (s.coarse[w]) {
             Entries q;
-            window_entries(s, row, V, w, least, q, all);
+            window_entries(s, pre, row, V, w, least, q, all);
             __syncthreads();
             if (least && s.told.least_n) heavy = {total.mass + join(s.told.least_hi, s.told.least_lo), total.n + s.told.least_n};
             __syncthreads();
@@ -557,16 +575,17 @@ __device__ __noinline__ void window_sums(Shared &s, const uint16_t *row, int V, 
 }
 
 // The window where a sum passes a bound, and its entries.
-__device__ __noinline__ void window_of(Shared &s, const uint16_t *row, int V, u128 mass, int n, Entries &q) {
+__device__ __noinline__ void window_of(Shared &s, Pre &pre, const uint16_t *row, int V, u128 mass, int n, Entries &q) {
     Sums at = {0, 0}, all;
     int w = kWindows - 1;
+#pragma unroll 1
     for (; w > 0; --w) {
         const u128 m = at.mass + join(s.win_hi[w], s.win_lo[w]);
         if (m > mass || at.n + s.win_n[w] >= n) break;
         at.mass = m;
         at.n += s.win_n[w];
     }
-    window_entries(s, row, V, w, 0, q, all);
+    window_entries(s, pre, row, V, w, 0, q, all);
     q.before = at;
 }
 
@@ -649,8 +668,6 @@ struct Counter {
     }
 };
 
-constexpr int kKept = (int)((sizeof(Shared) + 15) & ~(size_t)15);  // where a row's part is kept, behind the rest
-constexpr int kMostKept = 227 * 1024 - kKept;                      // bytes of it
 __device__ __forceinline__ void copy16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32_of(to)), "l"(from) : "memory");
 }
@@ -670,12 +687,15 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
     extern __shared__ __align__(16) char smem[];
     Shared &s = *(Shared *)smem;
     const int C = SHARE ? p.C : 1, c = SHARE ? (int)bgmv::cluster_rank() : 0;
+    unsigned *const extra = (unsigned *)(smem + kExtra);
+    Pre &pre = *(Pre *)(C == 2 ? s.bins + kPlaces / 2 : SHARE ? extra + kPlaces / C : extra);
     const int t = (int)blockIdx.x / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint16_t *row = p.logits + (long long)t * p.ld;
     asm volatile("griddepcontrol.launch_dependents;");
     fill_powers(s.pw);
     if (tid == 0) s.told.low = 0, s.told.odd = 0, s.told.top = kPlaces;
+#pragma unroll 1
     for (int i = tid; i < kBins; i += kThreads) s.bins[i] = 0;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -689,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
     const int part = ((p.V + C - 1) / C + 7) & ~7, begin = min(p.V, c * part), end = min(p.V, begin + part);
     Counter counter;
     counter.bins = s.bins;
-    uint4 *const kept = (uint4 *)(smem + kKept);
+    uint4 *const kept = (uint4 *)(smem + kExtra + extra_bytes(C));
     if (KEEP) {
         // a thread copies and counts the same vectors, in two halves
         const int n = (end - begin) >> 3, half = n >> 1;
@@ -769,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
     {
         const int g0 = c * n_groups / C, few = (c + 1) * n_groups / C - g0;
         const int w0 = few * warp / kWarps, rounds = few * (warp + 1) / kWarps - w0;
-        unsigned *const list = SHARE ? s.list : s.bins;
+        unsigned *const list = SHARE ? extra : s.bins;
         const auto group = [&](int j) { return SHARE ? (int)s.group_at[g0 + w0 + j] : w0 + j; };
         if (SHARE) {
             // the counts of all parts
@@ -823,9 +843,10 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
             s.scale = begin_scale(greedy ? 1.f : temperature);
             end_scale(s.scale, value_of(key));
         }
-        window_sums(s, row, p.V, least, total, heavy);
+        window_sums(s, pre, row, p.V, least, total, heavy);
     } else {
-        add_up(s, entries, least, total);
+        const Sums before = add_up(s, entries, least, total);
+        if (C != 2) put(pre, before);
         if (tid == 0) {
             s.told.hi = (u64)(total.mass >> 64);
             s.told.lo = (u64)total.mass;
@@ -833,6 +854,11 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
             s.told.entries = entries.n;
         }
         hear<SHARE>(s, C);
+        if (C == 2) {
+            // (nobody reads the counts any more)
+            put(pre, before);
+            cluster_sync<SHARE>();
+        }
         total = {0, 0};
 #pragma unroll 1
         for (int k = 0; k < C; ++k) {
@@ -873,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
             }
             int peer = c;
             if (!one) {
-                window_of(s, row, p.V, bound, most, entries);
+                window_of(s, pre, row, p.V, bound, most, entries);
                 __syncthreads();
             } else {
                 Sums upto = {0, 0};
@@ -887,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
                     if (upto.mass > bound || upto.n >= most) break;
                 }
             }
-            f = look<SHARE>(s, entries, peer, bound, most);
+            f = look<SHARE>(s, pre, entries, peer, bound, most);
             n = f.n;
             mass = join(f.hi, f.lo);
             if (!one) __syncthreads();
@@ -997,6 +1023,7 @@ int ctas_of_a_row(int T, int V, int sms) {
     return C;
 }
 
+constexpr int kMostSmem = 227 * 1024;  // of a CTA
 // A row's part in shared memory: one CTA to an SM, so only where all rows find room at once.  It is read
 // once, and more of it at a time (64 rows of 32007 columns 19.2 -> 16.3 us, one 18.0 -> 16.8, with all filters).
 // Half as many CTAs to a row that have that room are faster than all without it (18 rows of 128256 columns by four
@@ -1009,7 +1036,7 @@ Device g_devices[64];
 
 size_t part_of(int V, int C) { return (size_t)((lora_ceil_div(V, C) + 7) & ~7); }
 bool kept(const Device &d, int T, int V, int C) {
-    return part_of(V, C) * 2 <= (size_t)kMostKept && T <= d.rooms[C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3];
+    return kExtra + extra_bytes(C) + part_of(V, C) * 2 <= (size_t)kMostSmem && T <= d.rooms[C == 1 ? 0 : C == 2 ? 1 : C == 4 ? 2 : 3];
 }
 
 void configure(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int T, int C, size_t smem, cudaStream_t stream) {
@@ -1029,7 +1056,7 @@ void configure(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *at, int T, int C, s
 
 template <bool SHARE, bool KEEP>
 cudaError_t set_smem() {
-    return cudaFuncSetAttribute(sample_kernel<SHARE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? kKept + kMostKept : (int)sizeof(Shared));
+    return cudaFuncSetAttribute(sample_kernel<SHARE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? kMostSmem : (int)(kExtra + extra_bytes(2)));
 }
 
 // What the current device has; looked up once (the kernels' attributes are set on the way).
@@ -1049,7 +1076,7 @@ cudaError_t device_of(Device *&d) {
     for (int i = 1; i < 4; ++i) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute at[2];
-        configure(cfg, at, 1, 1 << i, kKept + kMostKept, nullptr);
+        configure(cfg, at, 1, 1 << i, kMostSmem, nullptr);
         if ((e = cudaOccupancyMaxActiveClusters(&rooms[i], sample_kernel<true, true>, &cfg)) != cudaSuccess) return e;
     }
     static std::mutex lock;
@@ -1094,7 +1121,7 @@ extern "C" lora_status_t lora_sample(const void *logits, int64_t ld, int32_t T, 
     const bool keep = kept(*dev, T, vocab_size, p.C);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at[2];
-    configure(cfg, at, T, p.C, keep ? (size_t)kKept + part_of(vocab_size, p.C) * 2 : sizeof(Shared), (cudaStream_t)stream);
+    configure(cfg, at, T, p.C, kExtra + extra_bytes(p.C) + (keep ? part_of(vocab_size, p.C) * 2 : 0), (cudaStream_t)stream);
     if (p.C > 1)
         LORA_CUDA_TRY(keep ? cudaLaunchKernelEx(&cfg, sample_kernel<true, true>, p) : cudaLaunchKernelEx(&cfg, sample_kernel<true, false>, p));
     else

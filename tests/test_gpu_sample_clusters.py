@@ -67,7 +67,8 @@ def test_equals_end_where_a_part_ends(V):
 
 
 @pytest.mark.parametrize("T,V", [(1, 39999), (152, 39990), (153, 39990), (15, 128256), (16, 128256), (17, 128256), (20, 257024), (38, 128000), (39, 120000),
-                                 (76, 100003), (76, 116001), (77, 90000)])
+                                 (76, 100003), (76, 116001), (77, 90000),
+                                 (17, 257024), (64, 128256), (76, 131000), (76, 131040), (1, 36000)])
 def test_rows_in_shared_memory_or_not(T, V):
     """Sizes at and beside the ones from which a CTA no longer keeps its part of the row."""
     x = rows(T, V, T)
