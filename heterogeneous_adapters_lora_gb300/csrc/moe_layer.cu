@@ -1117,6 +1117,29 @@ Carve carve(const lora_moe_layer_desc_t &d, const lora_pool_t *pool, int64_t T, 
     return c;
 }
 
+// Pairs of a group.  Groups of an expert read its weights once each: the batch's pairs make up to P / group of them
+// more, at some 0.5 us for a block and an SM.  A group's epilogue, of which the last one of a kernel is seen, takes some 1 us
+// for eight pairs, 2 with adapters, and a token's favourite experts may get many (91 pairs over 51 experts of 672 x 568, most for
+// one of them: groups of 64 73.7 us, of 8 31.1; 904 pairs over 18 of 432 x 760 85 us, of 16 67; 2048 pairs over 64 of
+// 2048 x 1408 284 us, of 32 359).  And where units are few, smaller groups share out the work behind the products
+// (111 pairs over 6 of 1040 x 272 with adapters: groups of 64 54 us, of 8 31).
+int group_of(const lora_moe_layer_desc_t &d, int P, bool adapters, int sms) {
+    const int experts = P < d.n_experts ? P : d.n_experts, each = lora_ceil_div(P, experts);
+    const int mt = lora_ceil_div(d.d_mlp, kTile);
+    const int64_t blocks = (int64_t)mt * lora_ceil_div(d.d_model, kBK) + (int64_t)lora_ceil_div(d.d_model, kRows) * lora_ceil_div(d.d_mlp, kBK);
+    int best = kGroup;
+    double least = 1e30;
+    for (int g = kGroup; g >= kBatchCols; g /= 2) {
+        const double cost = 0.5 * (double)P / g * (double)blocks / sms + (adapters ? 4.0 : 2.0) * g / kBatchCols;
+        if (cost < least) {
+            least = cost;
+            best = g;
+        }
+    }
+    while (best > kBatchCols && (int64_t)experts * lora_ceil_div(each, best) * mt * 2 <= sms) best /= 2;
+    return best;
+}
+
 struct Device {
     std::atomic<int> sms;  // 0: not looked up yet
 };
@@ -1227,11 +1250,7 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     p.y = (float *)(ws + c.y);
     p.grid = sms;
     p.spin_limit = lora_spin_limit();
-    // Few units: smaller groups, which read weights more often (from L2) but share out the work behind the products.
-    // 37 tokens over 6 experts of 1040 x 272 with adapters 61 us with groups of 64, 33 with groups of 8.
-    const int experts = p.P < d.n_experts ? p.P : d.n_experts, each = lora_ceil_div(p.P, experts), mt = lora_ceil_div(d.d_mlp, kTile);
-    p.group = kGroup;
-    while (p.group > kBatchCols && (int64_t)experts * lora_ceil_div(each, p.group) * mt * 2 <= sms) p.group /= 2;
+    p.group = group_of(d, p.P, pool != nullptr, sms);
     // A pair to a CTA of shrink13: no search for pairs, but rows of A that pairs share are read for each.
     p.single = p.P <= 256;
     if (pool) {
