@@ -1297,7 +1297,7 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     if (pool) {
         // experts, or as many sets of slots as there can be; CTAs that share the batches of one
         const int chunks = lora_ceil_div(p.R, kRanks), sets = !p.shared ? p.single ? p.P : p.E : p.L < T ? p.L : T;
-        const int slots = 3 * sms / (sets * p.n13 * chunks), share = p.single || slots < 1 ? 1 : slots > 8 ? 8 : slots;
+        const int slots = 3 * sms / (sets * p.n13 * chunks), share = p.single || slots < 1 ? 1 : slots > 16 ? 16 : slots;
         const dim3 grid((unsigned)sets, (unsigned)(p.n13 * chunks), (unsigned)(share < T ? share : T));
         LORA_CUDA_TRY(launch(shrink13_kernel, grid, kThreads, (size_t)p.P * 8, s, p, chunks));
     }
