@@ -8,14 +8,14 @@
 // memory by TMA and from there straight into tcgen05.mma, past the registers, and up to
 // 64 pairs cost what one costs.
 //
-//   shrink13   v[p] = scale A13 x        (with adapters; runs under the start of up)
+//   shrink13   v[p] = scale A13 x        (with adapters; up's CTAs start as its CTAs leave)
 //   up         g, u = W13 x + B13 v; h = act(g) u; parts of A2 h      per 128 columns of h
 //   down       y[p] = w (W2 h + B2 (scale A2 h))                      per 256 rows of W2
 //   combine    out[t] = sum of y over the token's pairs, in their order, one rounding
 //
 // Work is cut by bytes, not by tiles.  A unit is 256 weight rows (128 of gate and 128
 // of up, or 256 of W2) for one group (an expert and up to 64 of its pairs), a block 64 columns of
-// them (32 KB).  All units' blocks in a row are divided evenly among one CTA per SM,
+// them (32 KB).  All units' blocks in a row are divided evenly among one CTA per SM (whole units where they are small),
 // so a unit may be shared: its other CTAs leave fp32 sums in the workspace, and the one
 // that has its last block adds them, lower columns first, and finishes the unit.  A CTA works from its
 // last unit to its first, so what others wait for comes first, and only CTAs of
@@ -30,9 +30,15 @@
 // fence behind stores takes some 5 us while the memory is busy, which the epilogue would wait out).
 //
 // The adapters' part of eight pairs is small (256 rows of B, some ranks) and goes by m16n8k16
-// products in the epilogue's warps while a unit's weights are still on their way: the rows of
-// B, or of A2, come from global memory straight into registers, once per adapter among the eight, and the v of pairs
+// products in the epilogue's warps while a unit's weights are still on their way, for up to 32 pairs: the rows of
+// B, or of A2, come from global memory straight into registers, once per adapter among eight pairs, and the v of pairs
 // of other adapters count as zeros.
+//
+// Measured on one GB300 with 64 experts of 2048 x 1408, 8 a token (us; in brackets what their bytes take at the
+// copy rate): 1 token 36.5 (20.4), 16 159 (144), 64 182 (163), 256 213 (163); with 8 adapters of rank 16 40.6 (20.7),
+// 179 (149), 228 (178), 284 (188).  The weights go at 88% of the copy rate once they flow.  What is left are the
+// kernels' starts (3 us each until products flow), shrink13, which keeps up off its SMs (4, 8, 14 and 25 us), and the last unit's
+// epilogue, which no weights hide (1 to 8 us).
 //
 // Roundings: sums are fp32 throughout (accumulators, v, parts of A2 h, y).  h and v enter their
 // products in 16 bits: as two bf16, hi + lo, whose products are added (2^-17 of a
@@ -124,7 +130,7 @@ __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &
 // (any order of k will do as long as both have the same), a warp per eighth of the columns.
 // Several CTAs (gridDim.z) share an expert's batches of 8.  Bound by its chain of dependent reads (ids
 // and slots, then rows; rank and scale come with the rows, which are zeros past a rank) and by
-// the adapters' bytes.
+// the adapters' bytes (256 tokens of 8 adapters of rank 16: 67 MB in 20 us).
 constexpr int kBatch = 8, kRanks = 16;
 __global__ void __launch_bounds__(kThreads, 3) shrink13_kernel(const LayerArgs p, int chunks) {
     constexpr int kWarps = kThreads / 32, kAhead = 4;
@@ -241,6 +247,7 @@ template <bool DOWN>
 struct Shape {
     static constexpr int kCols = DOWN ? 2 * kGroup : kGroup;  // accumulator columns of a tile (down: hi, then lo)
     static constexpr uint32_t kStage = kABytes + kCols * 128;
+    // (16 tokens with 2, 3 and 4 stages 181, 167 and 171 us, 256 with adapters 332, 331 and 363: a deeper queue delays everyone)
     static constexpr int kStages = 3;
     static constexpr int kTmem = 4 * kCols;  // two tiles, two buffers
 };
@@ -1057,7 +1064,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
     if (warp == 1) tc::tmem_dealloc(tmem, Sh::kTmem);
 }
 
-// The pairs' results of a token in their order; the flags are left as they were found.
+// The pairs' results of a token in their order, 8 columns a thread; the flags are left as they were found.  Bound by reading y
+// back from L2 (256 tokens of 8 pairs and 2048 columns, 16.8 MB: 5 us).
 __global__ void __launch_bounds__(kThreads) combine_kernel(const LayerArgs p) {
     asm volatile("griddepcontrol.launch_dependents;");
     const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;

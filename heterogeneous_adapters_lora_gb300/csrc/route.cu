@@ -7,7 +7,8 @@
 // The choice is top_k rounds: the lanes' own maxima as order-preserving integers, the largest of them
 // (redux.sync), and a new maximum in the lane that had it.  A round takes some 45 instructions,
 // the scores as many as two rounds, and many tokens are bound by issuing them; few by the launch
-// and one read.  Warps walk over tokens and read the next one's logits ahead.
+// and one read.  Warps walk over tokens and read the next one's logits ahead.  One token of 64 experts takes
+// 2.4 us, 7995 of 256 with a bias 17.9 (their bytes 0.7).
 //
 // With a bias the fp32 scores may be off by a few 2^-24, which could order two
 // experts wrongly.  So rounds go on until the next expert is further behind than twice the error bound, and
