@@ -4,11 +4,12 @@
 // A warp takes a token and keeps its logits in registers, experts lane * N to lane * N + N - 1
 // in a lane: the lowest lane that has the largest key then has the lowest id of equal ones.  Choosing needs no
 // scores where they grow with the logits (no bias): the order is that of the logits, exact in fp32.
-// The choice is top_k rounds: the lanes' own maxima as order-preserving integers, the largest of them
-// (redux.sync), and a new maximum in the lane that had it.  A round takes some 45 instructions,
-// the scores as many as two rounds, and many tokens are bound by issuing them; few by the launch
-// and one read.  Warps walk over tokens and read the next one's logits ahead.  One token of 64 experts takes
-// 2.4 us, 7995 of 256 with a bias 17.9 (their bytes 0.7).
+// The choice is top_k rounds: the largest of the lanes' keys, order-preserving integers (redux.sync), is taken out.
+// With more than two experts a lane, rounds over the lanes' own largest first give a bound that leaves
+// a dozen experts, which go to a lane each: a round over those is a few instructions.  Many tokens are bound by issuing
+// some 1200 instructions each in chains (half of all issue slots are used); few by the launch and one
+// read.  Warps walk over tokens and read the next one's logits ahead.  One token of 64 experts takes 2.3
+// us, 7995 of 256 with a bias 15.0 (their bytes 0.7).
 //
 // With a bias the fp32 scores may be off by a few 2^-24, which could order two
 // experts wrongly.  So rounds go on until the next expert is further behind than twice the error bound, and
@@ -23,7 +24,13 @@
 
 namespace {
 
-constexpr int kThreads = 128, kCtasPerSm = 8;
+constexpr int kThreads = 128;
+// CTAs of an SM, which walk over the tokens in one wave: as many as registers without spills allow (7995 tokens of 256 experts
+// with a bias by 6 to 10 CTAs 15.0, 18.2 and 20 us; without one by 5 to 12 14.2, 11.7, 10.9, 10.5 and 9.9).
+template <int N, bool BIAS>
+__host__ __device__ constexpr int ctas_per_sm() {
+    return N == 2 ? 8 : N == 8 ? (BIAS ? 6 : 12) : BIAS ? 2 : 4;
+}
 constexpr unsigned kAll = 0xffffffffu;
 // Bounds on the absolute error of an fp32 score with the rounding of its biased sum, for sums
 // of magnitude 1 or less (larger ones in proportion).  Scores that decide take the fast exp and division: e =
@@ -115,10 +122,10 @@ __device__ __forceinline__ float load_logit(const RouteArgs &p, long long t, int
 // What a logit counts as: NaN and -inf take no part, +inf is the largest number.
 __device__ __forceinline__ float counted(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
 
-// This lane's logits of token t.  `vec`: rows are whole and aligned.
+// This lane's logits of token t.  `vec`: rows are aligned to pairs.
 template <int N>
 __device__ __forceinline__ void load_logits(const RouteArgs &p, long long t, int lane, float (&x)[N]) {
-    if (p.vec) {
+    if (p.vec && lane * N + N <= p.E) {
         if (p.wide) {
             const float *row = (const float *)p.logits + t * p.ld + lane * N;
 #pragma unroll
@@ -204,13 +211,50 @@ __device__ __noinline__ int choose_exactly(const RouteArgs &p, long long t, floa
     return chosen;
 }
 
+// The rounds.  Lane r gets the expert of round r (as who has it times M plus its place there); with a bias they go on past
+// top_k while neighbours are near: `near` says that some are, `found` how many rounds there were (33: more than lanes).
+template <int M, bool BIAS>
+__device__ __forceinline__ int rounds(const RouteArgs &p, unsigned (&key)[M], unsigned mine, float eps, int lane, bool &near, int &found) {
+    unsigned best;
+    int chosen = -1;
+    found = 0;
+    near = false;
+    if (!BIAS) {
+#pragma unroll 1
+        for (int r = 0; r < p.k; ++r) {
+            const int e = take_best<M>(key, mine, best, lane);
+            if (e < 0) break;
+            if (r == lane) chosen = e;
+        }
+        return chosen;
+    }
+    float before = 0.f, widest = 1.f;
+#pragma unroll 1
+    for (int r = 0;; ++r) {
+        const int e = take_best<M>(key, mine, best, lane);
+        if (e < 0) break;
+        const float v = key_value(best);
+        widest = fmaxf(widest, fabsf(v));
+        const bool close = r > 0 && !(before - v > 2.f * eps * widest);
+        if (r >= p.k && !close) break;  // and all that follow are further behind
+        near |= close;
+        found = r + 1;
+        if (r >= 32) break;
+        before = v;
+        if (r == lane) chosen = e;
+    }
+    return chosen;
+}
+
 // N: experts of a lane (32 N in all).
 template <int N, bool BIAS>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<N, BIAS>()) route_kernel(const RouteArgs p) {
     const int lane = threadIdx.x & 31, step = (int)gridDim.x * (kThreads / 32);
     long long t = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ unsigned s_key[N > 2 ? kThreads : 1];  // the few that can be chosen, a lane's each
+    __shared__ uint16_t s_id[N > 2 ? kThreads : 1];
     float bias[BIAS ? N : 1], ahead[N];
     if (BIAS)
 #pragma unroll
@@ -223,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
         if (t + step < p.T) load_logits<N>(p, t + step, lane, ahead);
         const unsigned top_key = warp_max(order_key(largest<N>(x)));
         const float top = top_key ? key_value(top_key) : 0.f;
-        unsigned key[N], best, mine;
+        unsigned key[N];
         int chosen = -1;  // of round `lane`
         float total = 1.f;  // of exp(x - top)
         if (!p.sigmoid) {
@@ -232,14 +276,10 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
             for (int j = 0; j < N; ++j) part += BIAS ? __expf(x[j] - top) : expf(x[j] - top);
             total = warp_sum(part);
         }
+        const float eps = p.sigmoid ? kEpsSigmoid : kEpsSoftmax;
         if (!BIAS) {
 #pragma unroll
             for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
-            mine = largest<N>(key);
-            for (int r = 0; r < p.k; ++r) {
-                const int e = take_best<N>(key, mine, best, lane);
-                if (r == lane) chosen = e;
-            }
         } else {
             const float inv = 1.f / total;
 #pragma unroll
@@ -247,34 +287,61 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
                 const float s = p.sigmoid ? __fdividef(1.f, 1.f + fminf(__expf(-x[j]), 1e30f)) : __expf(x[j] - top) * inv;
                 key[j] = x[j] > -INFINITY ? order_key(s + bias[j]) : 0u;
             }
-            mine = largest<N>(key);
-            float before = 0.f, widest = 1.f;
-            bool near = false;
-            const float eps = p.sigmoid ? kEpsSigmoid : kEpsSoftmax;
-            int found = 0;
-            bool many = false;
-            for (int r = 0;; ++r) {
-                const int e = take_best<N>(key, mine, best, lane);
-                if (e < 0) break;
-                const float v = key_value(best);
-                widest = fmaxf(widest, fabsf(v));
-                const bool close = r > 0 && !(before - v > 2.f * eps * widest);
-                if (r >= p.k && !close) break;  // and all that follow are further behind
-                near |= close;
-                many = r >= 32;
-                if (many) break;
-                before = v;
-                if (r == lane) chosen = e;
-                found = r + 1;
+        }
+        const unsigned mine = largest<N>(key);
+        bool near = false, few = false;
+        int found = 0;
+        if (N > 2) {
+            // Number k of the lanes' largest is a bound: what is below it is not chosen, nor (with a bias) what is
+            // below it by more than the widest distance that counts as near.
+            unsigned m = mine, least = 0, most = 0;
+#pragma unroll 1
+            for (int r = 0; r < p.k; ++r) {
+                least = warp_max(m);
+                if (r == 0) most = least;
+                if (!least) break;
+                if (lane == __ffs(__ballot_sync(kAll, m == least)) - 1) m = 0;
             }
-            if (many) chosen = choose_exactly<N>(p, t, top, lane);
-            else if (near) chosen = order_exactly<N>(p, t, top, lane, chosen, found);
+            if (BIAS && least) {
+                const float v = key_value(least);
+                least = order_key(v - 4.f * eps * fmaxf(1.f, fmaxf(fabsf(v), fabsf(key_value(most)))));
+            }
+            least = max(least, 1u);
+            int at = 0, n = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const unsigned some = __ballot_sync(kAll, key[j] >= least);
+                at += __popc(some & ((1u << lane) - 1));
+                n += __popc(some);
+            }
+            few = n <= 32;
+            if (few) {
+                unsigned *const keys = s_key + (threadIdx.x & ~31u);
+                uint16_t *const ids = s_id + (threadIdx.x & ~31u);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (key[j] >= least) {
+                        keys[at] = key[j];
+                        ids[at++] = (uint16_t)(lane * N + j);
+                    }
+                __syncwarp();
+                unsigned one[1] = {lane < n ? keys[lane] : 0u};
+                const int who = rounds<1, BIAS>(p, one, one[0], eps, lane, near, found);
+                chosen = who >= 0 ? (int)ids[who] : -1;
+                __syncwarp();
+            }
+        }
+        if (!few) chosen = rounds<N, BIAS>(p, key, mine, eps, lane, near, found);
+        if (BIAS) {
             if (!p.sigmoid) {  // the weights' sum, of exp itself
                 float part = 0.f;
 #pragma unroll
                 for (int j = 0; j < N; ++j) part += expf(x[j] - top);
                 total = warp_sum(part);
             }
+            // (nothing of the row is needed any more, so these calls save few registers)
+            if (found > 32) chosen = choose_exactly<N>(p, t, top, lane);
+            else if (near) chosen = order_exactly<N>(p, t, top, lane, chosen, found);
         }
         float s = 0.f;
         if (chosen >= 0) {
@@ -294,9 +361,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs p) {
 
 template <int N, bool BIAS>
 cudaError_t route_launch(RouteArgs p, int sms, cudaStream_t s) {
-    // rows as pairs of whole experts for every lane
     const int size = p.wide ? 4 : 2;
-    p.vec = p.E == 32 * N && p.ld % 2 == 0 && ((uintptr_t)p.logits & (2 * size - 1)) == 0;
+    p.vec = p.ld % 2 == 0 && ((uintptr_t)p.logits & (2 * size - 1)) == 0;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cudaLaunchAttribute at[1];
@@ -304,7 +370,7 @@ cudaError_t route_launch(RouteArgs p, int sms, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const int need = lora_ceil_div(p.T, kThreads / 32), most = sms * kCtasPerSm;
+    const int need = lora_ceil_div(p.T, kThreads / 32), most = sms * ctas_per_sm<N, BIAS>();
     cfg.gridDim = dim3((unsigned)(need < most ? need : most), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;

@@ -138,3 +138,26 @@ def test_captured_and_replayed_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert np.array_equal(ids.cpu().numpy(), reference(x.cpu().numpy(), 8, False, None, False, 1.0)[0])
+
+
+@pytest.mark.parametrize("E,k", [(200, 8), (254, 32), (1000, 32), (256, 12)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_favourites_of_one_lane_and_equals_everywhere(E, k, dtype):
+    """More candidates than lanes, all of them in one or two lanes, and borders that fall between equals."""
+    x = logits(40, E, E, dtype, spread=0.1)
+    x[:8, 40:48] += 5.0                # neighbours, in one lane
+    x[8:16, E - 12:] += 5.0
+    x[16:24] = (x[16:24] * 20).round() / 2   # many equals
+    x[24] = 1.0
+    x[25, ::2] = -np.inf
+    x[26, 3:] = -np.inf
+    x[27] = -1e30
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(6))
+    big = bias.clone()
+    big[::3] = -1e9
+    big[5] = 3e38
+    endless = bias.clone()
+    endless[7] = endless[9] = np.inf
+    for sigmoid in (False, True):
+        for b in (None, bias, torch.zeros(E), big, endless):
+            check(x, k, sigmoid, b, renormalize=True)
