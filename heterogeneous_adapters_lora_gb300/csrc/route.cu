@@ -5,7 +5,7 @@
 // in a lane: the lowest lane that has the largest key then has the lowest id of equal ones.  Choosing needs no
 // scores where they grow with the logits (no bias): the order is that of the logits, exact in fp32.
 // The choice is top_k rounds: the largest of the lanes' keys, order-preserving integers (redux.sync), is taken out.
-// With more than two experts a lane, rounds over the lanes' own largest first give a bound that leaves
+// With many tokens and more than two experts a lane, rounds over the lanes' own largest first give a bound that leaves
 // a dozen experts, which go to a lane each: a round over those is a few instructions.  Many tokens are bound by issuing
 // some 1200 instructions each in chains (half of all issue slots are used); few by the launch and one
 // read.  Warps walk over tokens and read the next one's logits ahead.  One token of 64 experts takes 2.3
@@ -35,14 +35,15 @@ constexpr unsigned kAll = 0xffffffffu;
 // Bounds on the absolute error of an fp32 score with the rounding of its biased sum, for sums
 // of magnitude 1 or less (larger ones in proportion).  Scores that decide take the fast exp and division: e =
 // exp(x) is off by 2^-22 and by 2^-24 * 1.45 |x| of itself, the quotient by 2 ulp.  Logistic
-// function: s (1 - s) <= 1/4 and s (1 - s) |x| < 0.23, so 2e-7 with the quotient's.  Softmax: s |x - top| < 0.37, the sum of up
-// to 1024 terms in 32 lanes and 5 steps takes 37 roundings, 3e-6.  The sum with the bias 6e-8.
-constexpr float kEpsSigmoid = 1.0e-6f, kEpsSoftmax = 1.0e-5f;
+// function: s (1 - s) <= 1/4 and s (1 - s) |x| < 0.23, so 2e-7 with the quotient's.  Softmax: all in proportion to the largest
+// score, s |x - top| < 0.37 of it, the sum of up to 1024 terms in 32 lanes and 5 steps takes 37 roundings, 3e-6.  The sum with
+// the bias 6e-8.
+constexpr float kEpsSigmoid = 1.0e-6f, kEpsSoftmax = 1.0e-5f, kEpsSum = 2.0e-7f;  // (softmax: of the largest score, and kEpsSum)
 
 struct RouteArgs {
     const void *logits;
     long long ld;
-    int T, E, k, sigmoid, renormalize, wide, vec;
+    int T, E, k, sigmoid, renormalize, wide, vec, many;
     float scale;
     const float *bias;
     int32_t *ids;
@@ -276,12 +277,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, BIAS>()) route_kernel
             for (int j = 0; j < N; ++j) part += BIAS ? __expf(x[j] - top) : expf(x[j] - top);
             total = warp_sum(part);
         }
-        const float eps = p.sigmoid ? kEpsSigmoid : kEpsSoftmax;
+        const float inv = 1.f / total;  // the largest score of a softmax
+        const float eps = p.sigmoid ? kEpsSigmoid : fmaf(kEpsSoftmax, inv, kEpsSum);
         if (!BIAS) {
 #pragma unroll
             for (int j = 0; j < N; ++j) key[j] = order_key(x[j]);
         } else {
-            const float inv = 1.f / total;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float s = p.sigmoid ? __fdividef(1.f, 1.f + fminf(__expf(-x[j]), 1e30f)) : __expf(x[j] - top) * inv;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, BIAS>()) route_kernel
         const unsigned mine = largest<N>(key);
         bool near = false, few = false;
         int found = 0;
-        if (N > 2) {
+        if (N > 2 && p.many) {
             // Number k of the lanes' largest is a bound: what is below it is not chosen, nor (with a bias) what is
             // below it by more than the widest distance that counts as near.
             unsigned m = mine, least = 0, most = 0;
@@ -362,6 +363,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<N, BIAS>()) route_kernel
 template <int N, bool BIAS>
 cudaError_t route_launch(RouteArgs p, int sms, cudaStream_t s) {
     const int size = p.wide ? 4 : 2;
+    // few tokens wait for their chains, which are shorter without the bound (13 tokens of 236 experts 3.9 us, with it 4.3)
+    p.many = p.T >= 8 * sms;
     p.vec = p.ld % 2 == 0 && ((uintptr_t)p.logits & (2 * size - 1)) == 0;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));

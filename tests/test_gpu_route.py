@@ -142,9 +142,10 @@ def test_captured_and_replayed_on_another_stream():
 
 @pytest.mark.parametrize("E,k", [(200, 8), (254, 32), (1000, 32), (256, 12)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_favourites_of_one_lane_and_equals_everywhere(E, k, dtype):
+@pytest.mark.parametrize("T", [40, 2500])
+def test_favourites_of_one_lane_and_equals_everywhere(T, E, k, dtype):
     """More candidates than lanes, all of them in one or two lanes, and borders that fall between equals."""
-    x = logits(40, E, E, dtype, spread=0.1)
+    x = logits(T, E, E, dtype, spread=0.1)
     x[:8, 40:48] += 5.0                # neighbours, in one lane
     x[8:16, E - 12:] += 5.0
     x[16:24] = (x[16:24] * 20).round() / 2   # many equals
@@ -152,6 +153,7 @@ def test_favourites_of_one_lane_and_equals_everywhere(E, k, dtype):
     x[25, ::2] = -np.inf
     x[26, 3:] = -np.inf
     x[27] = -1e30
+    x[T - 28:] = x[:28].clone()
     bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(6))
     big = bias.clone()
     big[::3] = -1e9
