@@ -181,6 +181,41 @@ def test_captured_with_another_workspace_and_replayed():
         layer.check()
 
 
+def test_two_graphs_and_eager_calls_share_a_workspace():
+    """Replayed in turn on one stream, with an eager call of a third batch between them."""
+    a, b, c = (Layer(T, 6, 2, 264, 136, adapters=2, rank=8, seed=30 + T, max_tokens=48) for T in (5, 48, 1))
+    b.ws = c.ws = a.ws
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for layer in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            layer.call()
+    for _ in range(3):
+        for layer in (a, b, c):
+            layer.out.fill_(7.0)
+        graphs[1].replay()
+        graphs[0].replay()
+        c.call()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        for layer in (a, b, c):
+            layer.check()
+
+
+def test_every_pair_for_one_expert_of_many():
+    """All the pairs a call takes, for one of 200 experts, and shares of groups of every size."""
+    layer = Layer(512, 200, 8, 72, 136, adapters=3, rank=8, seed=12)
+    ids = torch.full_like(layer.ids, 137)
+    layer.batch(ids=ids).call()
+    layer.check()
+    ids[:, 1:] = -1
+    ids[::3, 1] = 5
+    layer.batch(ids=ids).call()
+    layer.check()
+
+
 def test_two_layers_on_two_streams():
     layers = [Layer(20, 6, 2, 264, 136, adapters=2, rank=8, seed=20 + i) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in layers]
