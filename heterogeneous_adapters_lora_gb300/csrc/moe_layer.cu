@@ -64,7 +64,7 @@ constexpr int kBK = 64;                       // columns of a block: one 128-byt
 constexpr uint32_t kABytes = kRows * kBK * 2;
 constexpr int kStreamThreads = 352, kEpi0 = 2, kEpiThreads = 256;
 constexpr int kSms = 152;                     // where no device answers
-constexpr int kLeast = 4;                     // fewest blocks of a unit worth a CTA of their own
+constexpr int kLeast = 8;                     // fewest blocks of a unit worth a CTA of their own
 
 struct LayerArgs {
     int T, K, P, E, D, F, gelu;
@@ -472,7 +472,7 @@ __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
 
 // What a CTA does: blocks [b0, b1) of all the units' blocks in a row.  A unit of less than 2 kLeast blocks is not cut, and of
 // others no more than kLeast blocks to a CTA, equal parts where they are fewer than CTAs (160 pairs over 49 experts of
-// 136 x 128 34.2 -> 23.2 us, 37 tokens of three over 6 of 1040 x 272 30.6 -> 28.6).
+// 136 x 128 34.2 -> 23.2 us, 37 tokens of three over 6 of 1040 x 272 30.6 -> 27.0; kLeast of 4, 6, 8 and 10 29.0, 27.3, 27.0 and 27.9).
 struct Range {
     int b0, b1, grains, grain, n;  // n CTAs share them, in grains of a block or a unit
     // grains * c / n, whose parts stay below 2^31
