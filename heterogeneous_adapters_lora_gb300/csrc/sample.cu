@@ -1007,10 +1007,12 @@ __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const Sa
     if (p.logprobs) {
         float hi, lo;
         distance(s.scale, value_of(key), hi, lo);
-        // ln of the sum: 2^62 is one
-        const int lead = total.mass >> 64 ? 64 - __clzll((u64)(total.mass >> 64)) : 0;
-        const float m = (float)(u64)(total.mass >> lead);
-        p.logprobs[t] = -(hi * 0.69314718056f + (logf(m * 0x1p-62f) + (float)lead * 0.69314718056f));
+        // ln of the sum, whose largest weight is 2^62, one: accurate where the others are little, too
+        constexpr float kLn2 = 0.6931471805599453f, kLn2Rest = (float)(0.6931471805599453 - (double)kLn2);
+        const u128 others = total.mass - ((u128)1 << 62);
+        const int down = others >> 64 ? 64 - __clzll((u64)(others >> 64)) : 0;
+        const float sum = log1pf(ldexpf((float)(u64)(others >> down), down - 62));
+        p.logprobs[t] = -fmaf(hi, kLn2, fmaf(hi, kLn2Rest, fmaf(lo, kLn2, sum)));
     }
 }
 

@@ -170,6 +170,21 @@ def test_other_magnitudes(spread, temperature):
     check(x, t, [0, 0, 1000, 0, 0, 5], [0.9, 0.5, 0.99, 0.1, 1.0, 0.7], [0.0, 0.0, 0.0, 0.3, 0.01, 0.0], uniform(6, 2))
 
 
+def test_logarithm_of_a_share_that_is_nearly_all():
+    """One logit above the others: -log(1 + e) for small e, not the logarithm of a rounded sum."""
+    x = torch.zeros(4, 999, dtype=torch.bfloat16)
+    x[:, 500] = torch.tensor([16.0, 20.0, 28.0, 40.0], dtype=torch.bfloat16)
+    buf, tokens, logprobs = torch.zeros(4, 1000, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, device="cuda")
+    buf[:, :999] = x.cuda()
+    L.lora_sample(buf, 1000, 4, 999, None, None, None, None, None, tokens, logprobs)
+    assert tokens.tolist() == [500] * 4
+    for got, a in zip(logprobs.tolist(), (16.0, 20.0, 28.0, 40.0)):
+        want = -math.log1p(998 * math.exp(-a))
+        # the sum is rounded to fp32 (2^-24), ldexp and the signs are exact, log1p is off by at most 2 ulp (2^-22).  The weights
+        # exp(-a) 2^62 are integers, each off by less than 1: at 28 of 3188704 (2^-21), at 40 of 19.6 (1 / 19)
+        assert abs(got - want) <= (2.0 ** -21 + (1 / 19 if a == 40.0 else 2.0 ** -20)) * abs(want)
+
+
 def test_columns_behind_the_vocabulary_take_no_part():
     x = rows(4, 1000, 5)
     x[:, 700:] = 50.0
