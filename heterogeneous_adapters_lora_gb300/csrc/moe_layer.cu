@@ -40,9 +40,8 @@
 // kernels' starts (3 us each until products flow), shrink13, which keeps up off its SMs (4, 8, 14 and 25 us), and the last unit's
 // epilogue, which no weights hide (1 to 8 us).
 //
-// Roundings: sums are fp32 throughout (accumulators, v, parts of A2 h, y).  h and v enter their
-// products in 16 bits: as two bf16, hi + lo, whose products are added (2^-17 of a
-// value instead of 2^-9; the weights' bytes bound the kernel, not its MMAs).
+// Roundings: sums are fp32 throughout (accumulators, v, parts of A2 h, y), and h and v enter their products with all 24 bits: as
+// the sum of three bf16, a number's leading, middle and last 8 bits.  The weights' bytes bound the kernel, not its MMAs.
 #include <math.h>
 #include <stddef.h>
 #include <string.h>
@@ -85,7 +84,7 @@ struct LayerArgs {
     const float *scale;
     int R8;
     float *v13;                   // [P][2][R8], scaled (shared outer: by token), zeros past the adapter's rank
-    uint16_t *h;                  // [2][P][F]: hi, lo, in the order of the groups
+    uint16_t *h;                  // [3][P][F]: leading, middle and last bits, in the order of the groups
     float *v2;                    // [P][ceil(F / 128)][R8], parts of A2 h
     float *y;                     // [P][D], weighted
     float *part;                  // [CTA][2][kGroup][kTile] sums of shared units
@@ -111,17 +110,14 @@ __device__ __forceinline__ int slot_of(const LayerArgs &p, int t, bool note) {
     return p.enabled[a] && p.rank[a] > 0 ? a : -1;
 }
 
-// A number as the sum of two bf16; an infinite one is the first of them.
-__device__ __forceinline__ float rest(float v, float hi) { return fabsf(hi) < INFINITY ? v - hi : 0.f; }
-__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo) {
-    const __nv_bfloat16 a = __float2bfloat16_rn(v), b = __float2bfloat16_rn(rest(v, __bfloat162float(a)));
-    hi = *(const uint16_t *)&a;
-    lo = *(const uint16_t *)&b;
+// A number is the sum of three bf16 without error: its leading 8 bits, the leading 8 of what they leave, and the last 8 (of 24
+// bits; what is below bf16's smallest number is lost).  An infinite one or NaN is the first of them.
+__device__ __forceinline__ float rest(float v) {
+    return fabsf(v) < INFINITY ? v - __uint_as_float(__float_as_uint(v) & 0xffff0000u) : 0.f;
 }
-__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = bgmv::pack_bf16x2(a, b);
-    lo = bgmv::pack_bf16x2(rest(a, bf16lo(hi)), rest(b, bf16hi(hi)));
-}
+__device__ __forceinline__ uint16_t leading(float v) { return (uint16_t)(__float_as_uint(v) >> 16); }
+__device__ __forceinline__ uint32_t leading(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
+__device__ __forceinline__ float4 rest(const float4 &v) { return make_float4(rest(v.x), rest(v.y), rest(v.z), rest(v.w)); }
 
 // v = scale A13 x.  A CTA takes an expert (shared outer: the slots of one
 // remainder by the number of CTAs), a slice and 16 ranks.  It finds the expert's pairs (the slots'
@@ -245,8 +241,9 @@ struct StreamArgs {
 
 template <bool DOWN>
 struct Shape {
-    static constexpr int kCols = DOWN ? 2 * kGroup : kGroup;  // accumulator columns of a tile (down: hi, then lo)
-    static constexpr uint32_t kStage = kABytes + kCols * 128;
+    static constexpr int kCols = DOWN ? 2 * kGroup : kGroup;  // accumulator columns of a tile
+    static constexpr int kParts = DOWN ? 3 : 1;  // rows of a pair in a block
+    static constexpr uint32_t kStage = kABytes + kParts * kGroup * 128;
     // (16 tokens with 2, 3 and 4 stages 181, 167 and 171 us, 256 with adapters 332, 331 and 363: a deeper queue delays everyone)
     static constexpr int kStages = 3;
     static constexpr int kTmem = 4 * kCols;  // two tiles, two buffers
@@ -255,9 +252,9 @@ struct Shape {
 constexpr int kBatchCols = 8;                // columns that the epilogue takes at a time
 constexpr int kDPitch = kRows + 4;           // of the adapters' part of a column: no two of a product's lanes on one bank
 constexpr int kLotCols = 32;                 // ... whose adapters' part is there at once
-constexpr int kVFloats = 4096;
-static_assert(kVFloats / (2 * LORA_MAX_RANK) >= kBatchCols, "v of eight pairs");
-constexpr int kHPitch = kTile + 32;          // of a column of h: no two of 8 lanes' 16 bytes on one bank
+template <bool DOWN>
+constexpr int kVFloats = (DOWN ? 1 : 2) * LORA_MAX_RANK * kBatchCols;  // v of eight pairs at least
+constexpr int kHPitch = kTile + 4;           // of a column of h: no two of 8 lanes' 16 bytes on one bank
 
 template <bool DOWN, bool ADAPT>
 struct SharedOf {
@@ -280,12 +277,12 @@ struct SharedOf {
         } g;  // while groups are found
         struct {
             float delta[ADAPT ? kLotCols : 1][kDPitch];  // the adapters' part of a lot of columns
-            float v[ADAPT ? kVFloats : 1];     // scale A x or scale A2 h of some pairs
-            alignas(16) uint16_t h[ADAPT && !DOWN ? 2 : 1][ADAPT && !DOWN ? kGroup : 1][kHPitch];  // hi and lo of the unit's columns of h
+            float v[ADAPT ? kVFloats<DOWN> : 1];     // scale A x or scale A2 h of some pairs
+            alignas(16) float h[ADAPT && !DOWN ? kGroup : 1][kHPitch];  // the unit's columns of h
         } e;  // epilogue
     } u;
 };
-static_assert(sizeof(float[kDPitch]) % 16 == 0 && kHPitch % 8 == 0, "read 16 bytes at a time");
+static_assert(kDPitch % 4 == 0 && kHPitch % 4 == 0, "read 16 bytes at a time");
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
@@ -308,6 +305,14 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
         "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
         "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHi)
         : "memory");
+}
+// Columns that a group's pairs have in an accumulator, and rows in a block.  Down: leading, middle and last bits follow each other, all
+// three in one product; above 32 pairs two in one, and the last ones are added to the middle ones' columns by another (each product's
+// operands are read anew, and three a block made 3 tokens of 512 x 256 1.1 us slower).
+constexpr int kFew = 32;
+template <bool DOWN>
+__device__ __forceinline__ int columns_of(int pairs) {
+    return DOWN && pairs > kFew ? kGroup : (pairs + 15) & ~15;
 }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem) { return ((smem >> 4) & 0x3fffu) | (1u << 16); }
 
@@ -516,7 +521,7 @@ struct Epilogue {
 
     __device__ __forceinline__ Epilogue(const LayerArgs &p, Shared &s, int tid)
         : p(p), s(s), tid(tid), warp(tid >> 5), lane(tid & 31), g((tid & 31) >> 2), t4(tid & 3),
-          per(ADAPT ? p.R8 * (DOWN ? 1 : p.n13) : 1), lot(kVFloats / per & ~(kBatchCols - 1)) {}
+          per(ADAPT ? p.R8 * (DOWN ? 1 : p.n13) : 1), lot(kVFloats<DOWN> / per & ~(kBatchCols - 1)) {}
 
     // The weights and adapters of a group's pairs.  A barrier has to follow.
     __device__ __forceinline__ void note(const Part &x, Pairs &o) {
@@ -620,13 +625,13 @@ struct Epilogue {
                 if (q.run[k] < 0) break;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (q.run[k] == mine && q.r0[k] + t4 * 4 < p.R8) f = *(const float4 *)(v + q.r0[k]);
-                uint32_t hi[2], lo[2];
-                split(f.x, f.y, hi[0], lo[0]);
-                split(f.z, f.w, hi[1], lo[1]);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    bgmv::mma16816(d[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, hi[0], hi[1]);
-                    bgmv::mma16816(d[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, lo[0], lo[1]);
+                for (int i = 0; i < 3; ++i) {
+                    const uint32_t b0 = leading(f.x, f.y), b1 = leading(f.z, f.w);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        bgmv::mma16816(d[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, b0, b1);
+                    f = rest(f);
                 }
             }
             if (!q.left) break;
@@ -671,16 +676,19 @@ struct Epilogue {
         while (o.slot[end - 1] != slot) --end;  // pairs without an adapter come behind it
 #pragma unroll 1
         for (int c = run; c < end; c += 8) {
-            float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int col = min(c + g, kGroup - 1);
+            float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // of the leading bits, of the rest
+            const float *h = &s.u.e.h[min(c + g, kGroup - 1)][t4 * 8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                float4 f0 = *(const float4 *)(h + j * 32), f1 = *(const float4 *)(h + j * 32 + 4);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 b = *(const uint4 *)&s.u.e.h[k][col][j * 32 + t4 * 8];
-                    bgmv::mma16816(d[k], q.w[j][0].x, q.w[j][1].x, q.w[j][0].y, q.w[j][1].y, b.x, b.y);
-                    bgmv::mma16816(d[k], q.w[j][0].z, q.w[j][1].z, q.w[j][0].w, q.w[j][1].w, b.z, b.w);
+                for (int i = 0; i < 3; ++i) {
+                    bgmv::mma16816(d[i > 0], q.w[j][0].x, q.w[j][1].x, q.w[j][0].y, q.w[j][1].y, leading(f0.x, f0.y), leading(f0.z, f0.w));
+                    bgmv::mma16816(d[i > 0], q.w[j][0].z, q.w[j][1].z, q.w[j][0].w, q.w[j][1].w, leading(f1.x, f1.y), leading(f1.z, f1.w));
+                    f0 = rest(f0);
+                    f1 = rest(f1);
                 }
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int at = c + t4 * 2 + (k & 1), r = q.r0 + g + (k >> 1) * 8;
@@ -751,7 +759,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             char *dst = ring + (size_t)st * Sh::kStage;
             if (DOWN) {
                 const bool two = x.m * kRows + kTile < p.D;  // rows of the second tile that are there at all
-                tc::mbar_expect_tx(&s.full[st], (two ? kABytes : kABytes / 2) + (uint32_t)((x.n + 7) & ~7) * 128 * 2);
+                tc::mbar_expect_tx(&s.full[st], (two ? kABytes : kABytes / 2) + (uint32_t)((x.n + 7) & ~7) * 128 * Sh::kParts);
                 tma_weights(dst, &q.tm_w, k * kBK, x.m * kRows, x.e, &s.full[st], policy);
                 if (two) tma_weights(dst + kABytes / 2, &q.tm_w, k * kBK, x.m * kRows + kTile, x.e, &s.full[st], policy);
             } else {
@@ -780,10 +788,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
 #pragma unroll 1
         for (int u = u_hi; u >= u_lo && ok; --u) {
             const Part x = part_of(q, s, r, u, e_first);
-            // this lane's rows: four of x by token, or eight of h (hi, in lanes 8-15 lo)
-            const bool mine = DOWN ? lane < 16 && (lane & 7) * 8 < x.n : lane * 4 < x.n;
+            // this lane's rows: four of x by token, or eight of h (leading bits, in lanes 8-15 middle ones, then the last)
+            const bool mine = DOWN ? lane < 8 * Sh::kParts && (lane & 7) * 8 < x.n : lane * 4 < x.n;
             const uint32_t off =
-                kABytes + (uint32_t)(DOWN ? (lane & 7) * 8 + (lane >> 3) * ((x.n + 7) & ~7) : lane * 4) * 128;
+                kABytes + (uint32_t)(DOWN ? (lane & 7) * 8 + (lane >> 3) * columns_of<DOWN>(x.n) : lane * 4) * 128;
             const int row = x.pos + (lane & 7) * 8 + (lane >> 3) * p.P;
             int4 rows = make_int4(0, 0, 0, 0);
             if (!DOWN && mine) {
@@ -824,8 +832,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             const Part x = part_of(q, s, r, u, e_first);
             const int buf = i & 1;
             const bool two = !DOWN || x.m * kRows + kTile < p.D;
-            const int cols = DOWN ? 2 * ((x.n + 7) & ~7) : (x.n + 15) & ~15;
-            const uint32_t idesc = tc::idesc_bf16(kTile, cols);
+            const int cols = columns_of<DOWN>(x.n);
+            const bool few = x.n <= kFew;
+            const uint32_t idesc = tc::idesc_bf16(kTile, cols * (DOWN ? few ? 3 : 2 : 1)), idesc_last = tc::idesc_bf16(kTile, kGroup);
             if (i >= 2) ok = __all_sync(kAll, wait(&s.acce[buf], (uint32_t)(((i >> 1) - 1) & 1), p, s));
             tc::tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(buf * 2 * Sh::kCols);
@@ -842,6 +851,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                     for (int j = 0; j < kBK / 16; ++j) {
                         mma_ss(d, a0 + j * 2, b + j * 2, idesc, (k - x.k0) | j);
                         if (two) mma_ss(d + Sh::kCols, a1 + j * 2, b + j * 2, idesc, (k - x.k0) | j);
+                        if (DOWN && !few) {
+                            const uint32_t last = b + (uint32_t)(2 * kGroup * 128 >> 4) + j * 2;
+                            mma_ss(d + kGroup, a0 + j * 2, last, idesc_last, true);
+                            if (two) mma_ss(d + Sh::kCols + kGroup, a1 + j * 2, last, idesc_last, true);
+                        }
                     }
                     tc::mma_commit(&s.empty[st]);
                     if (k == x.k1 - 1) tc::mma_commit(&s.accf[buf]);
@@ -881,7 +895,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             const int buf = i & 1;
             const bool last = x.k1 == q.KB, more = u > u_lo;
             const uint32_t acc = tmem + lanes + (uint32_t)(buf * 2 * Sh::kCols);
-            const int lo_col = (x.n + 7) & ~7;
             const Part y = part_of(q, s, r, more ? u - 1 : u, e_first);  // the next unit
             int next = now;
             if (DOWN || ADAPT) {
@@ -982,12 +995,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                     tmem_ld4(acc + col, g);
                     tmem_ld4(acc + Sh::kCols + col, v);
                     if (DOWN) {
+                        const int cols = columns_of<DOWN>(x.n);
                         float gl[4], vl[4];
-                        tmem_ld4(acc + lo_col + col, gl);
-                        tmem_ld4(acc + Sh::kCols + lo_col + col, vl);
-                        tc::tmem_wait_ld();
+#pragma unroll 1
+                        for (int at = cols; at < (x.n <= kFew ? 3 * cols : 2 * cols); at += cols) {
+                            tmem_ld4(acc + at + col, gl);
+                            tmem_ld4(acc + Sh::kCols + at + col, vl);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) g[j] += gl[j], v[j] += vl[j];
+                            for (int j = 0; j < 4; ++j) g[j] += gl[j], v[j] += vl[j];
+                        }
                     } else {
                         tc::tmem_wait_ld();
                     }
@@ -1014,16 +1031,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                                 if (at < p.D) __stcg(y, g[j] * w);
                                 if (at + kTile < p.D) __stcg(y + kTile, v[j] * w);
                             } else {
-                                uint16_t hi = 0, lo = 0;
+                                float h = 0.f;
                                 if (at < p.F) {
-                                    split(activation(g[j], p.gelu) * v[j], hi, lo);
-                                    p.h[(long long)(x.pos + col + j) * p.F + at] = hi;
-                                    p.h[(long long)(p.P + x.pos + col + j) * p.F + at] = lo;
+                                    h = activation(g[j], p.gelu) * v[j];
+                                    uint16_t *to = p.h + (long long)(x.pos + col + j) * p.F + at;
+                                    const long long part = (long long)p.P * p.F;
+                                    const float middle = rest(h);
+                                    to[0] = leading(h);
+                                    to[part] = leading(middle);
+                                    to[2 * part] = leading(rest(middle));
                                 }
-                                if (ADAPT) {
-                                    s.u.e.h[0][col + j][row] = hi;
-                                    s.u.e.h[1][col + j][row] = lo;
-                                }
+                                if (ADAPT) s.u.e.h[col + j][row] = h;
                             }
                         }
                     }
@@ -1125,7 +1143,7 @@ Carve carve(const lora_moe_layer_desc_t &d, const lora_pool_t *pool, int64_t T, 
     c.part = c.flags + align256((size_t)2 * sms * 4);
     c.v13 = c.part + (size_t)sms * 2 * kGroup * kTile * 4;
     c.h = c.v13 + align256(P * 2 * R * 4);
-    c.v2 = c.h + align256(2 * P * d.d_mlp * 2);
+    c.v2 = c.h + align256(3 * P * d.d_mlp * 2);
     c.y = c.v2 + align256(P * lora_ceil_div(d.d_mlp, kTile) * R * 4);
     c.bytes = c.y + align256(P * d.d_model * 4);
     return c;
@@ -1299,7 +1317,7 @@ extern "C" lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const
     if (!lora_make_tmap_3d(&up.tm_w, w13, d.d_model, d.d_mlp, 2LL * d.n_experts, ld_w13, (long long)d.d_mlp * ld_w13, kBK, kTile) ||
         !lora_make_tmap_2d(&up.tm_b, x, d.d_model, T, ldx, kBK, 1, true) ||
         !lora_make_tmap_3d(&down.tm_w, w2, d.d_mlp, d.d_model, d.n_experts, ld_w2, (long long)d.d_model * ld_w2, kBK, kTile) ||
-        !lora_make_tmap_2d(&down.tm_b, p.h, d.d_mlp, 2LL * p.P, d.d_mlp, kBK, 8, true))
+        !lora_make_tmap_2d(&down.tm_b, p.h, d.d_mlp, 3LL * p.P, d.d_mlp, kBK, 8, true))
         return LORA_ERR_UNSUPPORTED;
     up.a = down.a = p;
     if (pool) {

@@ -671,8 +671,8 @@ LORA_API size_t lora_moe_layer_workspace_bytes(const lora_moe_layer_desc_t *desc
  * A chosen expert's weights are read once for up to 64 of its pairs (8 to 32, the rest
  * from L2, where that leaves too few pieces of work for the SMs); the call is meant for
  * batches whose time is that of reading weights.
- * Sums are fp32; h, which the second product takes in 16 bits, goes as the sum
- * of two bf16; out is rounded once.  The result does not change from run to run.
+ * Sums are fp32, h and A x enter the products behind them with all bits of fp32, and
+ * out is rounded once.  The result does not change from run to run.
  * An id of -1 is no expert, and a token without experts gets zeros.  Other ids outside
  * [0, n_experts) count as -1, slots outside [-1, max_loras) as no adapter, and both
  * set *status (an int32 device word, may be NULL) to LORA_ERR_DEVICE_INDEX.  A wait that
