@@ -31,8 +31,8 @@
 //
 // The adapters' part of eight pairs is small (256 rows of B, some ranks) and goes by m16n8k16
 // products in the epilogue's warps while a unit's weights are still on their way, for up to 32 pairs: the rows of
-// B, or of A2, come from global memory straight into registers, once per adapter among eight pairs, and the v of pairs
-// of other adapters count as zeros.
+// B, or of A2, come from global memory straight into registers, once per adapter among eight pairs, and of its product the columns
+// of its own pairs are kept.
 //
 // Measured on one GB300 with 64 experts of 2048 x 1408, 8 a token (us; in brackets what their bytes take at the
 // copy rate): 1 token 36.5 (20.4), 16 159 (144), 64 182 (163), 256 213 (163); with 8 adapters of rank 16 39.6 (20.7),
@@ -612,9 +612,12 @@ struct Epilogue {
     // first rows of B may have been asked for.  A barrier has to follow.
     __device__ __forceinline__ void rows(Rows &q, bool asked, const Part &x, const Pairs &o, int b0) {
         float d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const int col = b0 + g, all = runs(o, b0);
-        const int mine = col < x.n && o.slot[col] >= 0 ? 31 - __clz(all & ((2 << g) - 1)) : -2;  // the run of this lane's column
-        const float *v = s.u.e.v + col % lot * per + (p.n13 == 2 && tile() ? p.R8 : 0) + t4 * 4;
+        const int all = runs(o, b0);
+        int run[2];  // of the columns whose results this lane has
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            run[j] = o.slot[b0 + t4 * 2 + j] >= 0 ? 31 - __clz(all & ((2 << (t4 * 2 + j)) - 1)) : -2;
+        const float *v = s.u.e.v + (b0 + g) % lot * per + (p.n13 == 2 && tile() ? p.R8 : 0) + t4 * 4;
         if (!asked) q.left = all, q.r = 0;
 #pragma unroll 1
         for (;;) {
@@ -624,15 +627,22 @@ struct Epilogue {
             for (int k = 0; k < 4; ++k) {
                 if (q.run[k] < 0) break;
                 float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (q.run[k] == mine && q.r0[k] + t4 * 4 < p.R8) f = *(const float4 *)(v + q.r0[k]);
+                if (q.r0[k] + t4 * 4 < p.R8) f = *(const float4 *)(v + q.r0[k]);
+                float e[2][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i >> 2][i & 3] = d[i >> 2][i & 3];
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     const uint32_t b0 = leading(f.x, f.y), b1 = leading(f.z, f.w);
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        bgmv::mma16816(d[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, b0, b1);
+                        bgmv::mma16816(e[j], q.w[k][2 * j].x, q.w[k][2 * j + 1].x, q.w[k][2 * j].y, q.w[k][2 * j + 1].y, b0, b1);
                     f = rest(f);
                 }
+                // other adapters' columns keep what they have: a weight that is not finite is NaN even in a product with 0
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (q.run[k] == run[i & 1]) d[i >> 2][i & 3] = e[i >> 2][i & 3];
             }
             if (!q.left) break;
         }

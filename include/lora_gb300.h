@@ -673,6 +673,8 @@ LORA_API size_t lora_moe_layer_workspace_bytes(const lora_moe_layer_desc_t *desc
  * batches whose time is that of reading weights.
  * Sums are fp32, h and A x enter the products behind them with all bits of fp32, and
  * out is rounded once.  The result does not change from run to run.
+ * Numbers that are not finite show in the tokens that have them alone: those of an expert or of an
+ * adapter in its own pairs (a sum with an infinite weight may be NaN where the formula has infinity).
  * An id of -1 is no expert, and a token without experts gets zeros.  Other ids outside
  * [0, n_experts) count as -1, slots outside [-1, max_loras) as no adapter, and both
  * set *status (an int32 device word, may be NULL) to LORA_ERR_DEVICE_INDEX.  A wait that
