@@ -152,12 +152,15 @@ __device__ __forceinline__ void distance(const Scale &c, float v, float &hi, flo
 
 // exp((v - top) / temperature) in units of 2^-62: y = i + i1 / 64 + i2 / 4096 + i3 /
 // 2^18 + r, the three powers from tables, 2^-r by its series (r < 2^-18: the
-// cubic term is below 2^-56).
+// cubic term is below 2^-56).  Off by at most (y + 1) 2^-47 of itself, from y, and 2^-62 of the largest, as it is cut.
 __device__ __forceinline__ u64 weight62(const Scale &c, float v, const u64 *pw) {
     float hi, lo;
     distance(c, v, hi, lo);
+    const float sum = __fadd_rn(hi, lo);  // (lo can exceed a step of hi)
+    lo -= __fadd_rn(sum, -hi);
+    hi = sum;
     if (!(hi < 62.f)) return 0ull;
-    // y in units of 2^-50: its multiple of 2^-24, and the rest, each a 32-bit conversion
+    // y in units of 2^-50: its multiple of 2^-24, and the rest (half a step of hi at most, 2^-19), each a 32-bit conversion
     const int whole = __float2int_rd(hi * 0x1p24f);
     const int rest = __float2int_rn((lo + (hi - (float)whole * 0x1p-24f)) * 0x1p50f);
     long long y = ((long long)whole << 26) + rest;

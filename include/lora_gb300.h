@@ -707,8 +707,8 @@ LORA_API lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const l
  * means 1, 1, 0, 0 and 0.  Logits of -inf or NaN take no part, +inf counts as the
  * largest finite number; a row of which nothing is left gets token -1 and
  * logprob -inf.  Weights and their sums are integers of 2^-62 of the largest
- * weight, accurate to about 10^-14, so that sums do not depend on their order and the
- * token is that of the exact formula but for numbers that close to a border.
+ * weight, each weight accurate to about 2 10^-13 of itself and one such unit, so that sums do not depend
+ * on their order and the token is that of the exact formula but for numbers that close to a border.
  * Rows whose logits that matter are 0 or of magnitudes between 2^-55 and 2^9 are read twice;
  * others up to 22 times.
  * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, T < 0, ld < vocab_size or
