@@ -251,9 +251,11 @@ struct Shape {
 
 constexpr int kBatchCols = 8;                // columns that the epilogue takes at a time
 constexpr int kDPitch = kRows + 4;           // of the adapters' part of a column: no two of a product's lanes on one bank
-constexpr int kLotCols = 32;                 // ... whose adapters' part is there at once
+// ... whose adapters' part is there at once.  Down has room for fewer beside v of all 64 pairs of rank 64, which stays from unit to unit.
 template <bool DOWN>
-constexpr int kVFloats = (DOWN ? 1 : 2) * LORA_MAX_RANK * kBatchCols;  // v of eight pairs at least
+constexpr int kLotCols = DOWN ? 24 : 32;
+constexpr int kVFloats = 4096;
+static_assert(kVFloats / (2 * LORA_MAX_RANK) >= kBatchCols, "v of eight pairs");
 constexpr int kHPitch = kTile + 4;           // of a column of h: no two of 8 lanes' 16 bytes on one bank
 
 template <bool DOWN, bool ADAPT>
@@ -276,8 +278,8 @@ struct SharedOf {
             uint32_t key[kMaxP];                                       // slot << 12 | pair, by expert
         } g;  // while groups are found
         struct {
-            float delta[ADAPT ? kLotCols : 1][kDPitch];  // the adapters' part of a lot of columns
-            float v[ADAPT ? kVFloats<DOWN> : 1];     // scale A x or scale A2 h of some pairs
+            float delta[ADAPT ? kLotCols<DOWN> : 1][kDPitch];  // the adapters' part of a lot of columns
+            float v[ADAPT ? kVFloats : 1];     // scale A x or scale A2 h of some pairs
             alignas(16) float h[ADAPT && !DOWN ? kGroup : 1][kHPitch];  // the unit's columns of h
         } e;  // epilogue
     } u;
@@ -521,7 +523,7 @@ struct Epilogue {
 
     __device__ __forceinline__ Epilogue(const LayerArgs &p, Shared &s, int tid)
         : p(p), s(s), tid(tid), warp(tid >> 5), lane(tid & 31), g((tid & 31) >> 2), t4(tid & 3),
-          per(ADAPT ? p.R8 * (DOWN ? 1 : p.n13) : 1), lot(kVFloats<DOWN> / per & ~(kBatchCols - 1)) {}
+          per(ADAPT ? p.R8 * (DOWN ? 1 : p.n13) : 1), lot(kVFloats / per & ~(kBatchCols - 1)) {}
 
     // The weights and adapters of a group's pairs.  A barrier has to follow.
     __device__ __forceinline__ void note(const Part &x, Pairs &o) {
@@ -649,7 +651,7 @@ struct Epilogue {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s.u.e.delta[b0 % kLotCols + t4 * 2 + (k & 1)][warp * 32 + j * 16 + g + (k >> 1) * 8] = d[j][k];
+            for (int k = 0; k < 4; ++k) s.u.e.delta[b0 % kLotCols<DOWN> + t4 * 2 + (k & 1)][warp * 32 + j * 16 + g + (k >> 1) * 8] = d[j][k];
     }
 
     // 16 ranks of an adapter's A2, this unit's columns of them: what a warp multiplies with h at a time (up).
@@ -921,11 +923,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
             unsigned with = 0;  // batches of the lot that have an adapter's part
 #pragma unroll 1
             for (int b0 = 0; b0 < x.n; b0 += kBatchCols) {
-                if (ADAPT && b0 % kLotCols == 0) {
+                if (ADAPT && b0 % kLotCols<DOWN> == 0) {
                     // the adapters' part of a lot of columns, before their products are there
                     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
                     waited = true;
-                    const int to = min(x.n, b0 + kLotCols);
+                    const int to = min(x.n, b0 + kLotCols<DOWN>);
                     with = 0;
                     if (last)
 #pragma unroll 1
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                         epi.next_task(task, x, of);
                     }
                 }
-                const bool delta = with >> b0 % kLotCols / kBatchCols & 1;
+                const bool delta = with >> b0 % kLotCols<DOWN> / kBatchCols & 1;
                 const int col = b0 + half * 4;
                 if (b0 == 0 && last && x.k0 > 0) {
                     // Sums that other CTAs have left of this unit, while its products are still to come.
@@ -1032,8 +1034,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                         for (int j = 0; j < 4; ++j) {
                             if (col + j >= x.n) break;
                             if (delta) {
-                                g[j] += s.u.e.delta[col % kLotCols + j][row];
-                                v[j] += s.u.e.delta[col % kLotCols + j][kTile + row];
+                                g[j] += s.u.e.delta[col % kLotCols<DOWN> + j][row];
+                                v[j] += s.u.e.delta[col % kLotCols<DOWN> + j][kTile + row];
                             }
                             if (DOWN) {
                                 float *y = p.y + (long long)s.list[x.at + col + j] * p.D + at;
@@ -1057,7 +1059,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_
                     }
                 }
                 // the lot's delta is no longer read; at the end, all of h is there
-                if (ADAPT && last && ((b0 + kBatchCols) % kLotCols == 0 || b0 + kBatchCols >= x.n)) bar_sync(1, kEpiThreads);
+                if (ADAPT && last && ((b0 + kBatchCols) % kLotCols<DOWN> == 0 || b0 + kBatchCols >= x.n)) bar_sync(1, kEpiThreads);
             }
             if (!ok) {
                 if (!last) asm volatile("bar.arrive 3, %0;" ::"r"(kEpiThreads + 32) : "memory");
