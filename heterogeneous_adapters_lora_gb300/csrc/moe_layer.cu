@@ -244,7 +244,8 @@ struct Shape {
     static constexpr int kCols = DOWN ? 2 * kGroup : kGroup;  // accumulator columns of a tile
     static constexpr int kParts = DOWN ? 3 : 1;  // rows of a pair in a block
     static constexpr uint32_t kStage = kABytes + kParts * kGroup * 128;
-    // (16 tokens with 2, 3 and 4 stages 181, 167 and 171 us, 256 with adapters 332, 331 and 363: a deeper queue delays everyone)
+    // (2 and 3 stages: 16 tokens without adapters 176 and 156 us, 256 with adapters 294 and 293, 91 pairs over 51 experts of 672 x 568
+    // 32 and 29, 904 over 18 of 432 x 760 57 and 60; there is no room for 4)
     static constexpr int kStages = 3;
     static constexpr int kTmem = 4 * kCols;  // two tiles, two buffers
 };
@@ -453,7 +454,9 @@ __device__ __forceinline__ int expert_of_group(const LayerArgs &p, const Shared 
     return lo;
 }
 // The pairs of experts e0..e1, an expert's by slot (with adapters) and in their order: the same in every CTA, whatever
-// the order in which they were counted.
+// the order in which they were counted.  A pair is compared with all others of its expert, here and in shrink13, which hides behind
+// the weights up to some 500 of them and not above (D = F = 64, 4096 pairs without and with adapters: for one expert 1103 and 1751 us,
+// evenly for 64 of them 29 and 68; 512 pairs with adapters 58 and 25).
 template <class Shared>
 __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
     const int base = s.pairs[e0];
@@ -478,8 +481,9 @@ __device__ void list_pairs(const LayerArgs &p, Shared &s, int e0, int e1) {
 }
 
 // What a CTA does: blocks [b0, b1) of all the units' blocks in a row.  A unit of less than 2 kLeast blocks is not cut, and of
-// others no more than kLeast blocks to a CTA, equal parts where they are fewer than CTAs (160 pairs over 49 experts of
-// 136 x 128 34.2 -> 23.2 us, 37 tokens of three over 6 of 1040 x 272 30.6 -> 27.0; kLeast of 4, 6, 8 and 10 29.0, 27.3, 27.0 and 27.9).
+// others a CTA gets kLeast blocks at least, and all CTAs with any equal parts (160 pairs over 49 experts of
+// 136 x 128 23 us, 34 where units of 2 and 3 blocks are cut; kLeast of 4, 6, 8 and 10: 37 tokens of three over 6 of 1040 x 272 29.2, 27.3,
+// 27.3 and 28.7, 904 pairs over 18 of 432 x 760 68, 68, 60 and 60).
 struct Range {
     int b0, b1, grains, grain, n;  // n CTAs share them, in grains of a block or a unit
     // grains * c / n, whose parts stay below 2^31
@@ -1162,11 +1166,11 @@ Carve carve(const lora_moe_layer_desc_t &d, const lora_pool_t *pool, int64_t T, 
 }
 
 // Pairs of a group.  Groups of an expert read its weights once each: the batch's pairs make up to P / group of them
-// more, at some 0.5 us for a block and an SM.  A group's epilogue, of which the last one of a kernel is seen, takes some 1 us
-// for eight pairs, 2 with adapters, and a token's favourite experts may get many (91 pairs over 51 experts of 672 x 568, most for
-// one of them: groups of 64 73.7 us, of 8 31.1; 904 pairs over 18 of 432 x 760 85 us, of 16 67; 2048 pairs over 64 of
-// 2048 x 1408 284 us, of 32 359).  And where units are few, smaller groups share out the work behind the products
-// (111 pairs over 6 of 1040 x 272 with adapters: groups of 64 54 us, of 8 31).
+// more, at some 0.5 us for a block and an SM.  A group's epilogue, of which the last one of each of the two kernels is seen, takes some
+// 1 us there for eight pairs, 2 with adapters, and a token's favourite experts may get many (91 pairs over 51 experts of 672 x 568, most
+// for one of them: groups of 64 57.9 us, of 16 27.7, of 8 28.7; 904 pairs over 18 of 432 x 760 73, of 16 60; 2048 pairs over 64 of
+// 2048 x 1408 293 us, of 32 363).  And where units are few, smaller groups share out the work behind the products
+// (111 pairs over 6 of 1040 x 272 with adapters: groups of 64 43.6 us, of 8 27.3).
 int group_of(const lora_moe_layer_desc_t &d, int P, bool adapters, int sms) {
     const int experts = P < d.n_experts ? P : d.n_experts, each = lora_ceil_div(P, experts);
     const int mt = lora_ceil_div(d.d_mlp, kTile);

@@ -25,8 +25,8 @@
 namespace {
 
 constexpr int kThreads = 128;
-// CTAs of an SM, which walk over the tokens in one wave: as many as registers without spills allow (7995 tokens of 256 experts
-// with a bias by 6 to 10 CTAs 15.0, 18.2 and 20 us; without one by 5 to 12 14.2, 11.7, 10.9, 10.5 and 9.9).
+// CTAs of an SM, which walk over the tokens in one wave: as many as registers allow before spills cost (7995 tokens of 256 experts
+// with a bias by 6 to 10 CTAs 15.0, 18.2 and 20 us; without one by 5 to 12 14.2, 11.7, 10.9, 10.5 and 9.9, the last with one register spilled).
 template <int N, bool BIAS>
 __host__ __device__ constexpr int ctas_per_sm() {
     return N == 2 ? 8 : N == 8 ? (BIAS ? 6 : 12) : BIAS ? 2 : 4;

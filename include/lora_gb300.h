@@ -628,8 +628,8 @@ typedef struct {
  * times scale.  logits: [T][ld_logits] device, aligned to its type, any
  * ld_logits >= n_experts.  The order is that of the exact scores: where fp32
  * cannot tell two biased scores apart they are taken again in 64 bits.  An
- * expert whose logit or biased score is NaN or -inf is not chosen (and adds
- * nothing to a softmax); a token with fewer than top_k others gets ids of -1 and
+ * expert whose logit or biased score is NaN or -inf is not chosen (and one of such a logit
+ * adds nothing to a softmax); a token with fewer than top_k others gets ids of -1 and
  * weights of 0 in the last places.  A logit of +inf counts as the largest finite
  * number.  topk_ids: [T][top_k] int32, topk_w: [T][top_k] fp32, device, not
  * overlapping the inputs.
@@ -670,7 +670,8 @@ LORA_API size_t lora_moe_layer_workspace_bytes(const lora_moe_layer_desc_t *desc
  * needed.  Rank and scale are read on the stream.
  * A chosen expert's weights are read once for up to 64 of its pairs (8 to 32, the rest
  * from L2, where that leaves too few pieces of work for the SMs); the call is meant for
- * batches whose time is that of reading weights.
+ * batches whose time is that of reading weights.  The pairs of one expert are put in order by comparing each
+ * with all, which takes most of the time where thousands are one's (4096: over a millisecond).
  * Sums are fp32, h and A x enter the products behind them with all bits of fp32, and
  * out is rounded once.  The result does not change from run to run.
  * Numbers that are not finite show in the tokens that have them alone: those of an expert or of an
@@ -710,7 +711,7 @@ LORA_API lora_status_t lora_moe_layer(const lora_moe_layer_desc_t *desc, const l
  * weight, each weight accurate to about 2 10^-13 of itself and one such unit, so that sums do not depend
  * on their order and the token is that of the exact formula but for numbers that close to a border.
  * Rows whose logits that matter are 0 or of magnitudes between 2^-55 and 2^9 are read twice;
- * others up to 22 times.
+ * others up to 23 times.
  * Errors: LORA_ERR_INVALID_ARG (null or misaligned pointer, T < 0, ld < vocab_size or
  * not a multiple of 8), LORA_ERR_SHAPE (vocab_size < 1 or > LORA_MAX_VOCAB). */
 LORA_API lora_status_t lora_sample(const void *logits, int64_t ld, int32_t T, int32_t vocab_size,
