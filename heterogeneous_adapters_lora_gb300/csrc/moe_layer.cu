@@ -35,8 +35,8 @@
 // of its own pairs are kept.
 //
 // Measured on one GB300 with 64 experts of 2048 x 1408, 8 a token (us; in brackets what their bytes take at the
-// copy rate): 1 token 36.5 (20.4), 16 159 (144), 64 182 (163), 256 213 (163); with 8 adapters of rank 16 39.6 (20.7),
-// 176 (149), 228 (178), 282 (188).  The weights go at 88% of the copy rate once they flow.  What is left are the
+// copy rate): 1 token 36.2 (20.4), 16 157 (144), 64 182 (163), 256 217 (163); with 8 adapters of rank 16 40.5 (20.7),
+// 181 (149), 229 (178), 294 (188).  The weights go at 86% of the copy rate once they flow.  What is left are the
 // kernels' starts (3 us each until products flow), shrink13, which keeps up off its SMs (4, 8, 14 and 25 us), and the last unit's
 // epilogue, which no weights hide (1 to 8 us).
 //

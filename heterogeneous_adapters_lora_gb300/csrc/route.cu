@@ -8,8 +8,8 @@
 // With many tokens and more than two experts a lane, rounds over the lanes' own largest first give a bound that leaves
 // a dozen experts, which go to a lane each: a round over those is a few instructions.  Many tokens are bound by issuing
 // some 1200 instructions each in chains (half of all issue slots are used); few by the launch and one
-// read.  Warps walk over tokens and read the next one's logits ahead.  One token of 64 experts takes 2.3
-// us, 7995 of 256 with a bias 15.0 (their bytes 0.7).
+// read.  Warps walk over tokens and read the next one's logits ahead.  One token of 64 experts takes 2.4
+// us, 7995 of 256 with a bias 14.8 (their bytes 0.7).
 //
 // With a bias the fp32 scores may be off by a few 2^-24, which could order two
 // experts wrongly.  So rounds go on until the next expert is further behind than twice the error bound, and
