@@ -624,7 +624,7 @@ typedef struct {
  * lora_moe_apply and lora_moe_layer take them: the top_k experts of the largest
  * score + bias (bias: [n_experts] fp32 device, NULL = none), in that order, of
  * equal ones the lower id first; weight = the score itself (without the bias),
- * divided by the chosen scores' sum under renormalize (0 where that sum is 0),
+ * divided by the chosen scores' sum under renormalize (0 where that sum is 0 in 64 bits),
  * times scale.  logits: [T][ld_logits] device, aligned to its type, any
  * ld_logits >= n_experts.  The order is that of the exact scores: where fp32
  * cannot tell two biased scores apart they are taken again in 64 bits.  An
