@@ -30,7 +30,7 @@
 // fence behind stores takes some 5 us while the memory is busy, which the epilogue would wait out).
 //
 // The adapters' part of eight pairs is small (256 rows of B, some ranks) and goes by m16n8k16
-// products in the epilogue's warps while a unit's weights are still on their way, for up to 32 pairs: the rows of
+// products in the epilogue's warps while a unit's weights are still on their way, for up to 32 pairs (down: 24): the rows of
 // B, or of A2, come from global memory straight into registers, once per adapter among eight pairs, and of its product the columns
 // of its own pairs are kept.
 //
@@ -720,6 +720,7 @@ constexpr size_t stream_smem() {
 }
 static_assert(stream_smem<false, true>() <= 227 * 1024 && stream_smem<true, true>() <= 227 * 1024, "shared memory of a CTA");
 
+// (168 registers a thread are what 352 threads can have; up with adapters spills one)
 template <bool DOWN, bool ADAPT>
 __global__ void __launch_bounds__(kStreamThreads, 1) stream_kernel(const __grid_constant__ StreamArgs q) {
     typedef Shape<DOWN> Sh;

@@ -686,7 +686,8 @@ __device__ __noinline__ int eight_largest(uint4 v) {
     return n;
 }
 
-// SHARE: CTAs share a row (p.C of them; otherwise one has it).  KEEP: a CTA keeps its part of the row in shared memory.
+// SHARE: CTAs share a row (p.C of them; otherwise one has it).  KEEP: a CTA keeps its part of the row in shared memory; others run two to an
+// SM, with 64 registers a thread (two of those that share a row are spilled).
 template <bool SHARE, bool KEEP>
 __global__ void __launch_bounds__(kThreads, KEEP ? 1 : 2) sample_kernel(const SampleArgs p) {
     extern __shared__ __align__(16) char smem[];
